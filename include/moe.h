@@ -11,6 +11,12 @@
  *                  the same reading the token rows through perm, no xs copy)
  *   moe_combine    weighted sum of each token's k expert rows (+ shared row)
  *   moe_load_stats capacity, overflow / drops, skew, Gini, stragglers
+ * around it, for a whole decoder block and for gated experts:
+ *   moe_norm, moe_norm_residual  norm before the block; norm, gate, scale and
+ *                  residual behind it (with the next block's norm)
+ *   moe_route_grouped  sigmoid / softmax scores, choice bias, groups, top-k
+ *   moe_linear, moe_linear_grouped  product with bias, activation or gate, and
+ *                  residual; grouped: over the experts' segments
  * and, after the layer, the routing-bias feedback of the next step:
  *   moe_bias_update dynamic bias B from the expert counts, load fractions f_i
  *   (the mean router probabilities P_i are an optional output of moe_route)
@@ -307,6 +313,143 @@ int moe_load_stats(const int32_t* counts, int T, int E, int k, double capacity_f
  */
 int moe_bias_update(const int32_t* counts, int E, float gamma, float* bias, float* load_frac,
                     void* stream);
+
+typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind;
+
+/*
+ * moe_norm - the norm in front of a block, row by row:
+ *   MOE_NORM_RMS:   out = x / sqrt(mean(x^2) + eps) * weight + bias
+ *   MOE_NORM_LAYER: out = (x - mu) / sqrt(mean((x - mu)^2) + eps) * weight + bias,
+ *                   mu = mean(x)
+ * Means over the H elements of a row; statistics and arithmetic in fp32 (the
+ * variance around the mean, not as a difference of squares), one rounding to
+ * the output type. Any H from 1 to 16384 (H % 64 is not required; rows of
+ * 16-byte multiples are faster); a larger one is MOE_ERR_UNSUPPORTED. A row
+ * with a NaN or infinity affects only its own output row; a row without
+ * variance under eps = 0 divides by zero as the formula does.
+ * x      [rows,H] dtype          device, read
+ * weight [H] dtype or NULL       device, read (NULL = 1)
+ * bias   [H] dtype or NULL       device, read (NULL = 0)
+ * out    [rows,H] dtype          device, written; may be x itself
+ * eps: finite, >= 0. All pointers 16-byte aligned. No workspace.
+ */
+int moe_norm(const void* x, const void* weight, const void* bias, int rows, int H, float eps,
+             int kind, int dtype, void* out, void* stream);
+
+typedef enum {
+  MOE_GATE_NONE = 0,    /* 1 */
+  MOE_GATE_TOKEN = 1,   /* [rows]: one value a row */
+  MOE_GATE_CHANNEL = 2, /* [H]: one value a channel */
+  MOE_GATE_FULL = 3     /* [rows,H] */
+} moe_gate_mode;
+
+/*
+ * moe_norm_residual - what stands between two blocks, in one pass over the rows:
+ *   z        = norm(y) by kind, weight, bias (MOE_NORM_NONE: z = y)
+ *   h        = res + scale * gate * z
+ *   res_out  = h                        rounded to dtype
+ *   next_out = norm(h) by next_kind, next_weight, next_bias (of h before its
+ *              rounding); not written for MOE_NORM_NONE
+ * y, res [rows,H] dtype, gate [rows] / [H] / [rows,H] dtype by gate_mode (NULL
+ *   for MOE_GATE_NONE): device, read
+ * weight, bias, next_weight, next_bias [H] dtype or NULL: device, read; NULL
+ *   with the kind MOE_NORM_NONE
+ * res_out, next_out [rows,H] dtype: device, written. res_out may be res itself
+ *   and next_out may be y itself; no other overlap. next_out NULL with
+ *   next_kind MOE_NORM_NONE.
+ * scale: finite. eps, H, alignment and arithmetic as moe_norm.
+ */
+int moe_norm_residual(const void* y, int kind, const void* weight, const void* bias,
+                      const void* res, const void* gate, int gate_mode, float scale,
+                      int next_kind, const void* next_weight, const void* next_bias, int rows,
+                      int H, float eps, int dtype, void* res_out, void* next_out, void* stream);
+
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/*
+ * moe_route_grouped - top-k gating with a choice bias and groups of experts
+ * ([K3] router listing for scores, top-k and renormalisation; the balance bias
+ * of [DIAG] section 4.2 moves the choice here, not the weights: moe_route has
+ * it inside the softmax).
+ *   s[t,e] = sum_h x[t,h] * wg[e,h]                       (fp32 accumulation)
+ *   p[t,e] = softmax over e of s[t,:], or 1 / (1 + exp(-s[t,e]))
+ *   v[t,e] = p[t,e] + bias[e]
+ *   group j = the experts [j*E/groups, (j+1)*E/groups); its score is the
+ *            largest v in it (group_top 1) or the sum of the two largest (2)
+ *   chosen groups: the topk_groups best, equal scores to the lower group
+ *   topk_idx[t,0..k-1] = the k largest v among the experts of the chosen
+ *            groups, descending, equal ones to the lower expert id
+ *   topk_w[t,j] = scale * p[t,idx_j] / (renorm ? sum_j' p[t,idx_j'] : 1)
+ * Without a bias the experts are ordered by s (the same order as p, kept where
+ * p rounds to 0 or 1).
+ * An expert with a bias of -inf or NaN, or a NaN score, is off: it counts in no
+ * group's score (a group with one expert left scores that one alone) and is
+ * chosen only when fewer than k experts of the chosen groups are on, then with
+ * weight 0 (lower ids first). A NaN score counts as -inf in the softmax. If the
+ * chosen p are all 0 the weights are 0.
+ * x [T,H], wg [E,H] dtype, bias [E] fp32 or NULL: device, read
+ * topk_idx [T,k] int32, topk_w [T,k] fp32: device, written
+ * 1 <= groups <= 64, E % groups == 0, 1 <= topk_groups <= groups,
+ * k <= topk_groups * E / groups, scale finite; else MOE_ERR_UNSUPPORTED (or
+ * MOE_ERR_INVALID_ARG for non-positive sizes and unknown enums).
+ * ws / ws_bytes: device workspace of at least
+ *   moe_route_grouped_workspace_bytes(T,H,E,k,dtype) (NULL allowed when that is 0)
+ */
+int moe_route_grouped(const void* x, const void* wg, const float* bias, int T, int H, int E, int k,
+                      int score, int groups, int topk_groups, int group_top, int renorm,
+                      float scale, int dtype, int32_t* topk_idx, float* topk_w, void* ws,
+                      size_t ws_bytes, void* stream);
+size_t moe_route_grouped_workspace_bytes(int T, int H, int E, int k, int dtype);
+
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_GELU = 1,   /* 0.5*a*(1 + erf(a/sqrt(2))) */
+  MOE_ACT_SILU = 2,   /* a / (1 + exp(-a)) */
+  MOE_ACT_GEGLU = 3,  /* gelu(a_0) * a_1 */
+  MOE_ACT_SWIGLU = 4  /* silu(a_0) * a_1 */
+} moe_act;
+
+/*
+ * moe_linear - matrix product with its epilogue:
+ *   a[m,n] = sum_k x[m,k] * w[n,k] + bias[n]             (fp32 accumulation)
+ *   y[m,n] = act(a[m,n]) + residual[m,n]
+ * and for a gated act, with w [2,N,K] and bias [2,N] (half 0 the gate):
+ *   y[m,n] = act(a_0[m,n]) * a_1[m,n] + residual[m,n]
+ * Bias, activation, gate and residual are applied in fp32 to the accumulator;
+ * y is rounded once.
+ * x [M,K], w [N,K] or [2,N,K], bias [N] or [2,N] or NULL, residual [M,N] or NULL,
+ * all dtype: device, read; y [M,N] dtype: device, written. y may be residual
+ * itself, and overlaps no other input.
+ * K % 64 == 0, N % 64 == 0, any M >= 1.
+ * ws / ws_bytes: device workspace of at least
+ *   moe_linear_workspace_bytes(M,N,K,act,dtype) (NULL allowed when that is 0)
+ */
+int moe_linear(const void* x, const void* w, const void* bias, int act, const void* residual,
+               int M, int N, int K, int dtype, void* y, void* ws, size_t ws_bytes, void* stream);
+size_t moe_linear_workspace_bytes(int M, int N, int K, int act, int dtype);
+
+/*
+ * moe_linear_grouped - moe_linear over the experts' ragged segments: buffer row
+ * p in [offsets[e], offsets[e+1]) takes the weights w[e] and bias[e] of its
+ * expert. Two calls make gated experts ([BLOG] section 3.1's pair of Linear
+ * layers with a gate): the up half with MOE_ACT_SWIGLU reading x through perm,
+ * the down half with MOE_ACT_NONE.
+ * x [rows,K], or with perm the token rows [T,K]: buffer row p then reads
+ *   x[perm[p] / k] (a perm entry outside [0, T*k) is clamped into it)
+ * perm [rows] int32 or NULL, 1 <= k <= 8 (with perm only; T and k are
+ *   otherwise not used), rows <= T*k
+ * offsets [E+1] int32 from moe_dispatch or moe_dispatch_capped; rows is an upper
+ *   bound of offsets[E], and rows of y past offsets[E] are left as they were
+ *   (offsets are clamped into the buffer; a segment of no rows is fine)
+ * w [E,N,K] or [E,2,N,K], bias [E,N] or [E,2,N] or NULL, residual [rows,N] or NULL,
+ * y [rows,N]: as moe_linear. 1 <= E <= 256.
+ * ws / ws_bytes: moe_linear_grouped_workspace_bytes(E,rows,N,K,act,dtype)
+ */
+int moe_linear_grouped(const void* x, const int32_t* perm, int k, int T, const int32_t* offsets,
+                       int E, int rows, const void* w, const void* bias, int act,
+                       const void* residual, int N, int K, int dtype, void* y, void* ws,
+                       size_t ws_bytes, void* stream);
+size_t moe_linear_grouped_workspace_bytes(int E, int rows, int N, int K, int act, int dtype);
 
 /* Static, human-readable text for a status code. */
 const char* moe_status_string(int status);

@@ -19,6 +19,7 @@ STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED",
           -3: "MOE_ERR_WORKSPACE", -4: "MOE_ERR_HIP", -5: "MOE_ERR_SCRATCH"}
 
 _vp, _i, _sz, _d = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_double
+_f = ctypes.c_float
 
 SIGNATURES = {
     "moe_route": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
@@ -39,6 +40,17 @@ SIGNATURES = {
     "moe_bias_update": (_i, [_vp, _i, ctypes.c_float, _vp, _vp, _vp]),
     "moe_capacity": (ctypes.c_int64, [_i, _i, _i, _d]),
     "moe_dispatch_noalloc": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_norm": (_i, [_vp, _vp, _vp, _i, _i, _f, _i, _i, _vp, _vp]),
+    "moe_norm_residual": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _i, _f, _i, _vp, _vp, _i, _i, _f, _i,
+                               _vp, _vp, _vp]),
+    "moe_route_grouped": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _vp,
+                               _vp, _sz, _vp]),
+    "moe_route_grouped_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "moe_linear": (_i, [_vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "moe_linear_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "moe_linear_grouped": (_i, [_vp, _vp, _i, _i, _vp, _i, _i, _vp, _vp, _i, _vp, _i, _i, _i, _vp,
+                                _vp, _sz, _vp]),
+    "moe_linear_grouped_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "moe_status_string": (ctypes.c_char_p, [_i]),
 }
 
@@ -535,3 +547,346 @@ class MoELayerGraph:
         self.x.copy_(x)
         self.graph.replay()
         return self.out
+
+
+# ---------------------------------------------------------------- around the layer
+
+NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
+ACTS = {"none": 0, "gelu": 1, "silu": 2, "geglu": 3, "swiglu": 4}
+GATED_ACTS = ("geglu", "swiglu")
+
+
+def _enum(table, value, name: str) -> int:
+    code = table.get(value)
+    if code is None:
+        raise ValueError(f"{name} must be one of {', '.join(map(repr, table))}, got {value!r}")
+    return code
+
+
+def _ptr(t, name: str, shape, dtype, device):
+    """Address of a tensor argument after its checks: shape, type, the device of
+    the call's first tensor, and contiguity. None passes."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _ws(nbytes: int, device, ws):
+    """(address, bytes) of the workspace: the caller's, or a new one."""
+    if ws is None:
+        if nbytes == 0:
+            return None, 0, None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        have = ws.numel() * ws.element_size()
+        if have < nbytes:
+            raise ValueError(f"workspace too small: {have} bytes, needs {nbytes}")
+        if ws.device != device or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous tensor on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def _other_stream(device, stream):
+    """The stream a call has to switch to before it allocates and launches (the
+    given one, or the current one of the tensors' device when that is not the
+    current device), or None."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be GPU tensors, got {device}")
+    if stream is None:
+        return None if device.index == torch.cuda.current_device() else torch.cuda.current_stream(device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return None if stream == torch.cuda.current_stream() else stream
+
+
+def moe_norm(x, weight=None, bias=None, eps: float = 1e-6, kind: str = "rms", out=None,
+             stream=None):
+    """Norm of every row of x [T,H]: "rms" or "layer", times weight, plus bias.
+
+    bf16 or fp32, any H up to 16384; ``out`` may be x itself. Returns out."""
+    T, H = _dims(x, "x", 2)
+    dev, dtype = x.device, x.dtype
+    dt, code = _dtype_code(x), _enum(NORM_KINDS, kind, "kind")
+    xp = _ptr(x, "x", (T, H), dtype, dev)
+    wp, bp = _ptr(weight, "weight", (H,), dtype, dev), _ptr(bias, "bias", (H,), dtype, dev)
+    op = _ptr(out, "out", (T, H), dtype, dev)
+    other = _other_stream(dev, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return moe_norm(x, weight, bias, eps, kind, out)
+    if out is None:
+        out = torch.empty_like(x)
+        op = out.data_ptr()
+    _check("moe_norm", lib().moe_norm(xp, wp, bp, T, H, eps, code, dt, op,
+                                      torch.cuda.current_stream().cuda_stream))
+    return out
+
+
+def moe_norm_residual(y, res, weight=None, bias=None, gate=None, scale: float = 1.0,
+                      eps: float = 1e-6, kind: str = "rms", next_weight=None, next_bias=None,
+                      next_kind: str = "none", res_out=None, next_out=None, stream=None):
+    """h = res + scale * gate * norm(y), and the next block's norm of h, in one pass.
+
+    y, res [T,H]; kind / next_kind "none", "rms" or "layer"; gate None, [T,1]
+    (one value a row), [H] or [T,H]. Returns (h, norm of h or None). res_out may
+    be res itself, next_out y itself."""
+    T, H = _dims(y, "y", 2)
+    dev, dtype, row = y.device, y.dtype, (H,)
+    dt = _dtype_code(y)
+    code, ncode = _enum(NORM_KINDS, kind, "kind"), _enum(NORM_KINDS, next_kind, "next_kind")
+    if gate is None:
+        mode, gshape = 0, None
+    else:
+        gshape = tuple(gate.shape) if isinstance(gate, torch.Tensor) else ()
+        if gshape == (T, H):
+            mode = 3
+        elif gshape == (H,):
+            mode = 2
+        elif gshape == (T, 1):
+            mode = 1
+        else:
+            raise ValueError(f"gate must have shape {(T, 1)}, {(H,)} or {(T, H)}, got {gshape}")
+    if next_out is not None and ncode == 0:
+        raise ValueError("next_out needs a next_kind")
+    args = [_ptr(y, "y", (T, H), dtype, dev), code, _ptr(weight, "weight", row, dtype, dev),
+            _ptr(bias, "bias", row, dtype, dev), _ptr(res, "res", (T, H), dtype, dev),
+            _ptr(gate, "gate", gshape, dtype, dev), mode, scale, ncode,
+            _ptr(next_weight, "next_weight", row, dtype, dev),
+            _ptr(next_bias, "next_bias", row, dtype, dev)]
+    rp = _ptr(res_out, "res_out", (T, H), dtype, dev)
+    np_ = _ptr(next_out, "next_out", (T, H), dtype, dev)
+    other = _other_stream(dev, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return moe_norm_residual(y, res, weight, bias, gate, scale, eps, kind, next_weight,
+                                     next_bias, next_kind, res_out, next_out)
+    if res_out is None:
+        res_out = torch.empty_like(y)
+        rp = res_out.data_ptr()
+    if next_out is None and ncode != 0:
+        next_out = torch.empty_like(y)
+        np_ = next_out.data_ptr()
+    _check("moe_norm_residual", lib().moe_norm_residual(
+        *args, T, H, eps, dt, rp, np_, torch.cuda.current_stream().cuda_stream))
+    return res_out, next_out
+
+
+def moe_route_grouped_workspace_bytes(T: int, H: int, E: int, k: int, dtype_code: int) -> int:
+    return lib().moe_route_grouped_workspace_bytes(T, H, E, k, dtype_code)
+
+
+def moe_route_grouped(x, wg, bias, k: int, score: str = "sigmoid", groups: int = 1,
+                      topk_groups: int = 1, group_top: int = 2, renorm: bool = True,
+                      scale: float = 1.0, topk_idx=None, topk_w=None, ws=None, stream=None):
+    """Top-k routing with sigmoid or softmax scores, a bias (fp32 [E] or None) that
+    moves the choice only, and the choice limited to the topk_groups best of
+    ``groups`` groups of experts (by their ``group_top`` largest biased scores).
+    Returns (topk_idx int32 [T,k], topk_w fp32 [T,k])."""
+    T, H = _dims(x, "x", 2)
+    E = _dims(wg, "wg", 2)[0]
+    dev, dtype = x.device, x.dtype
+    dt, code = _dtype_code(x), _enum(SCORES, score, "score")
+    xp, wp = _ptr(x, "x", (T, H), dtype, dev), _ptr(wg, "wg", (E, H), dtype, dev)
+    bp = _ptr(bias, "bias", (E,), torch.float32, dev)
+    ip = _ptr(topk_idx, "topk_idx", (T, k), torch.int32, dev)
+    op = _ptr(topk_w, "topk_w", (T, k), torch.float32, dev)
+    other = _other_stream(dev, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return moe_route_grouped(x, wg, bias, k, score, groups, topk_groups, group_top, renorm,
+                                     scale, topk_idx, topk_w, ws)
+    L = lib()
+    wsp, wsn, ws = _ws(L.moe_route_grouped_workspace_bytes(T, H, E, k, dt), dev, ws)
+    if topk_idx is None:
+        topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        ip = topk_idx.data_ptr()
+    if topk_w is None:
+        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        op = topk_w.data_ptr()
+    _check("moe_route_grouped", L.moe_route_grouped(
+        xp, wp, bp, T, H, E, k, code, groups, topk_groups, group_top, int(renorm), scale, dt, ip, op,
+        wsp, wsn, torch.cuda.current_stream().cuda_stream))
+    return topk_idx, topk_w
+
+
+def moe_linear_workspace_bytes(M: int, N: int, K: int, act: str, dtype_code: int) -> int:
+    return lib().moe_linear_workspace_bytes(M, N, K, _enum(ACTS, act, "act"), dtype_code)
+
+
+def moe_linear(x, w, bias=None, act: str = "none", residual=None, y=None, ws=None, stream=None):
+    """y = act(x . w^T + bias) + residual, everything after the product in fp32.
+
+    x [M,K], w [N,K], bias [N], residual and y [M,N], all of one type (bf16 or
+    fp32); act "none", "gelu" (erf) or "silu". Gated: act "geglu" or "swiglu"
+    with w [2,N,K] and bias [2,N], y = act(gate half) * other half + residual.
+    y may be residual itself. Returns y."""
+    M, K = _dims(x, "x", 2)
+    code = _enum(ACTS, act, "act")
+    two = (2,) if code >= 3 else ()
+    N = _dims(w, "w", 2 + len(two))[-2]
+    dev, dtype = x.device, x.dtype
+    dt = _dtype_code(x)
+    xp, wp = _ptr(x, "x", (M, K), dtype, dev), _ptr(w, "w", (*two, N, K), dtype, dev)
+    bp = _ptr(bias, "bias", (*two, N), dtype, dev)
+    rp, yp = _ptr(residual, "residual", (M, N), dtype, dev), _ptr(y, "y", (M, N), dtype, dev)
+    other = _other_stream(dev, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return moe_linear(x, w, bias, act, residual, y, ws)
+    L = lib()
+    wsp, wsn, ws = _ws(L.moe_linear_workspace_bytes(M, N, K, code, dt), dev, ws)
+    if y is None:
+        y = torch.empty((M, N), dtype=dtype, device=dev)
+        yp = y.data_ptr()
+    _check("moe_linear", L.moe_linear(xp, wp, bp, code, rp, M, N, K, dt, yp, wsp, wsn,
+                                      torch.cuda.current_stream().cuda_stream))
+    return y
+
+
+def moe_linear_grouped_workspace_bytes(E: int, rows: int, N: int, K: int, act: str,
+                                       dtype_code: int) -> int:
+    return lib().moe_linear_grouped_workspace_bytes(E, rows, N, K, _enum(ACTS, act, "act"),
+                                                    dtype_code)
+
+
+def moe_linear_grouped(x, offsets, w, bias=None, act: str = "none", residual=None, perm=None,
+                       k: int = 1, rows=None, y=None, ws=None, stream=None):
+    """moe_linear over the experts' segments: buffer row p in [offsets[e],
+    offsets[e+1]) takes w[e] and bias[e] (offsets int32 [E+1] from moe_dispatch).
+
+    w [E,N,K] (gated: [E,2,N,K]), bias [E,N] ([E,2,N]). Without perm, x is the
+    buffer [rows,K]; with perm (int32, from moe_dispatch of k experts a token) x is
+    the token rows [T,K] and row p reads x[perm[p] // k]. rows (default: all of the
+    buffer, T*k with perm) is an upper bound of offsets[E]; rows of y past
+    offsets[E] are left as they were. Returns y [rows,N]."""
+    T, K = _dims(x, "x", 2)
+    code = _enum(ACTS, act, "act")
+    two = (2,) if code >= 3 else ()
+    dims = _dims(w, "w", 3 + len(two))
+    E, N = dims[0], dims[-2]
+    dev, dtype = x.device, x.dtype
+    dt = _dtype_code(x)
+    most = T if perm is None else T * k
+    if rows is None:
+        rows = most
+    if not 1 <= rows <= most:
+        raise ValueError(f"rows {rows} outside [1, {most}]")
+    if perm is not None and _dims(perm, "perm", 1)[0] < rows:
+        raise ValueError(f"perm must have at least rows = {rows} entries")
+    xp, wp = _ptr(x, "x", (T, K), dtype, dev), _ptr(w, "w", (E, *two, N, K), dtype, dev)
+    fp = _ptr(offsets, "offsets", (E + 1,), torch.int32, dev)
+    pp = None if perm is None else _ptr(perm, "perm", perm.shape, torch.int32, dev)
+    bp = _ptr(bias, "bias", (E, *two, N), dtype, dev)
+    rp, yp = _ptr(residual, "residual", (rows, N), dtype, dev), _ptr(y, "y", (rows, N), dtype, dev)
+    other = _other_stream(dev, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return moe_linear_grouped(x, offsets, w, bias, act, residual, perm, k, rows, y, ws)
+    L = lib()
+    wsp, wsn, ws = _ws(L.moe_linear_grouped_workspace_bytes(E, rows, N, K, code, dt), dev, ws)
+    if y is None:
+        y = torch.empty((rows, N), dtype=dtype, device=dev)
+        yp = y.data_ptr()
+    _check("moe_linear_grouped", L.moe_linear_grouped(
+        xp, pp, k, T, fp, E, rows, wp, bp, code, rp, N, K, dt, yp, wsp, wsn,
+        torch.cuda.current_stream().cuda_stream))
+    return y
+
+
+def moe_block_forward(h, wg, w_up, w_down, k: int, x=None, norm_weight=None, norm_bias=None,
+                      norm: str = "rms", eps: float = 1e-6, route_bias=None,
+                      score: str = "sigmoid", groups: int = 1, topk_groups: int = 1,
+                      group_top: int = 2, renorm: bool = True, scale: float = 1.0,
+                      act: str = "swiglu", b_up=None, b_down=None, ws_up=None, ws_down=None,
+                      capacity=None, out_norm: str = "none", out_weight=None, out_bias=None,
+                      gate=None, res_scale: float = 1.0, next_norm: str = "none",
+                      next_weight=None, next_bias=None, stream=None):
+    """A whole MoE block of a decoder on the residual stream h [T,H], on one stream
+    without host synchronisation:
+
+        x    = norm(h)                              (or given: the previous block's ``next``)
+        idx, w = moe_route_grouped(x, wg, route_bias, k, ...)
+        out  = sum_j w_j * expert_j(x) (+ shared expert(x)),
+               expert(x) = act(x . w_up^T + b_up) . w_down^T + b_down
+        res  = h + res_scale * gate * out_norm(out)
+        next = next_norm(res)                       (None without a next_norm)
+
+    w_up [E,F,H], or [E,2,F,H] for a gated act; w_down [E,H,F]; b_up [E,F] or
+    [E,2,F], b_down [E,H]; ws_up, ws_down the same without E (no biases): the
+    always-on shared expert. capacity (int) drops each expert's assignments past
+    it. Returns a dict: res, next, and the steps' x, topk_idx, topk_w, counts,
+    offsets, perm, inv, out."""
+    if (ws_up is None) != (ws_down is None):
+        raise ValueError("the shared expert needs ws_up and ws_down")
+    dev = _dims(h, "h", 2) and h.device
+    other = _other_stream(dev, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return moe_block_forward(h, wg, w_up, w_down, k, x, norm_weight, norm_bias, norm, eps,
+                                     route_bias, score, groups, topk_groups, group_top, renorm,
+                                     scale, act, b_up, b_down, ws_up, ws_down, capacity, out_norm,
+                                     out_weight, out_bias, gate, res_scale, next_norm, next_weight,
+                                     next_bias)
+    if x is None:
+        x = moe_norm(h, norm_weight, norm_bias, eps, norm)
+    idx, w = moe_route_grouped(x, wg, route_bias, k, score, groups, topk_groups, group_top, renorm,
+                               scale)
+    d = moe_dispatch(idx, x, wg.shape[0], capacity=capacity, gather=False)
+    a = moe_linear_grouped(x, d["offsets"], w_up, b_up, act, perm=d["perm"], k=k)
+    ys = moe_linear_grouped(a, d["offsets"], w_down, b_down)
+    ysh = None
+    if ws_up is not None:
+        ysh = moe_linear(moe_linear(x, ws_up, act=act), ws_down)
+    out = moe_combine(ys, d["inv"], w, ysh)
+    res, nxt = moe_norm_residual(out, h, out_weight, out_bias, gate, res_scale, eps, out_norm,
+                                 next_weight, next_bias, next_norm)
+    del d["xs"]
+    return dict(res=res, next=nxt, x=x, topk_idx=idx, topk_w=w, out=out, **d)
+
+
+class MoEBlockGraph:
+    """moe_block_forward for a fixed number of tokens T, captured once into a HIP
+    graph and replayed (the decode-latency use of MoELayerGraph).
+
+    Takes moe_block_forward's arguments after h, by keyword. ``run(h)`` copies h
+    into the static input and replays; it returns (res, next), the static outputs,
+    which the next run overwrites; ``state`` holds every step's static result. The
+    weights and biases are read where they are: their owner may update them in
+    place between runs."""
+
+    def __init__(self, T: int, wg, w_up, w_down, k: int, **kw):
+        if kw.get("x") is not None or kw.get("stream") is not None:
+            raise ValueError("a captured block makes its own x and runs on the caller's current stream")
+        dev = wg.device
+        if dev.type != "cuda":
+            raise ValueError("wg must be a GPU tensor")
+        self.h = torch.zeros((T, wg.shape[1]), dtype=wg.dtype, device=dev)
+        call = lambda: moe_block_forward(self.h, wg, w_up, w_down, k, **kw)  # noqa: E731
+        with torch.cuda.device(dev):
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                call()  # one eager pass on a side stream before capture
+            torch.cuda.current_stream().wait_stream(side)
+            torch.cuda.synchronize()
+            self.graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(self.graph):
+                self.state = call()
+            torch.cuda.synchronize()
+
+    def run(self, h):
+        """Copy h into the static input and replay; returns (res, next)."""
+        self.h.copy_(h)
+        self.graph.replay()
+        return self.state["res"], self.state["next"]

@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <initializer_list>
 
 #include "kernels.hpp"
 
@@ -41,7 +42,7 @@ const char* moe_status_string(int status) {
   switch (status) {
     case MOE_OK: return "ok";
     case MOE_ERR_INVALID_ARG: return "invalid argument (null or misaligned pointer, non-positive size or bad dtype)";
-    case MOE_ERR_UNSUPPORTED: return "unsupported shape (needs 1<=E<=256, 1<=k<=min(E,8), H%64==0, F%64==0, T*k<2^31)";
+    case MOE_ERR_UNSUPPORTED: return "unsupported shape (needs 1<=E<=256, 1<=k<=min(E,8), H%64==0, F%64==0, T*k<2^31; norms: H<=16384; moe_route_grouped: E%groups==0, groups<=64, topk_groups<=groups, k<=topk_groups*E/groups; products: N%64==0, K%64==0)";
     case MOE_ERR_WORKSPACE: return "workspace missing or smaller than the size query returned";
     case MOE_ERR_HIP: return "HIP launch failed";
     case MOE_ERR_SCRATCH: return "request exceeds the fixed 1 MiB scratch of moe_dispatch_noalloc (needs E * ceil(T / 256) * 4 <= 1 MiB; use moe_dispatch with a workspace)";
@@ -209,6 +210,162 @@ int moe_bias_update(const int32_t* counts, int E, float gamma, float* bias, floa
     return MOE_ERR_INVALID_ARG;
   if (E > kMaxExperts) return MOE_ERR_UNSUPPORTED;
   return from_hip(moe::launch_bias_update(counts, E, gamma, bias, load_frac, as_stream(stream)));
+}
+
+namespace {
+
+constexpr int kMaxNormH = 16384;
+
+bool norm_kind_ok(int kind) { return kind >= MOE_NORM_NONE && kind <= MOE_NORM_LAYER; }
+bool aligned_or_null(const void* p) { return !p || aligned16(p); }
+
+// Whether the n bytes at p and the m bytes at q share any (null: no).
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  if (!p || !q) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + m && b < a + n;
+}
+size_t elem(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
+
+int check_norm(int rows, int H, float eps, int dtype) {
+  if (rows < 1 || H < 1 || !dtype_ok(dtype) || !std::isfinite(eps) || eps < 0.0f)
+    return MOE_ERR_INVALID_ARG;
+  return H > kMaxNormH ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+int check_grouped(int E, int k, int score, int groups, int topk_groups, int group_top, int renorm,
+                  float scale) {
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (groups < 1 || topk_groups < 1 || (group_top != 1 && group_top != 2) ||
+      (renorm != 0 && renorm != 1) || !std::isfinite(scale))
+    return MOE_ERR_INVALID_ARG;
+  if (groups > 64 || E % groups != 0 || topk_groups > groups) return MOE_ERR_UNSUPPORTED;
+  return k > topk_groups * (E / groups) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+int check_linear(int E, int M, int N, int K, int act, int dtype) {
+  if (E < 1 || M < 1 || N < 1 || K < 1 || !dtype_ok(dtype) || act < MOE_ACT_NONE ||
+      act > MOE_ACT_SWIGLU)
+    return MOE_ERR_INVALID_ARG;
+  if (E > kMaxExperts || N % 64 != 0 || K % 64 != 0) return MOE_ERR_UNSUPPORTED;
+  return moe::linear_fits(E, M, N, K) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+int run_linear(const void* x, const int32_t* perm, int k, int T, const int32_t* offsets, int E,
+               int M, const void* w, const void* bias, int act, const void* residual, int N, int K,
+               int dtype, void* y, void* ws, size_t ws_bytes, void* stream) {
+  if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned_or_null(bias) ||
+      !aligned_or_null(residual) || !aligned_or_null(ws))
+    return MOE_ERR_INVALID_ARG;
+  const size_t ny = (size_t)M * N * elem(dtype);
+  if (overlap(y, ny, x, (size_t)(perm ? T : M) * K * elem(dtype)) ||
+      (y != residual && overlap(y, ny, residual, ny)))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need =
+      moe::linear_ws_bytes(E, M, N, K, act, offsets != nullptr, dtype == MOE_BF16);
+  if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  return from_hip(moe::launch_linear(x, perm, k, T, offsets, E, M, N, K, w, bias, act, residual,
+                                     dtype == MOE_BF16, y, ws, as_stream(stream)));
+}
+
+}  // namespace
+
+int moe_norm(const void* x, const void* weight, const void* bias, int rows, int H, float eps,
+             int kind, int dtype, void* out, void* stream) {
+  if (!x || !out || !norm_kind_ok(kind) || kind == MOE_NORM_NONE) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(out) || !aligned_or_null(weight) || !aligned_or_null(bias))
+    return MOE_ERR_INVALID_ARG;
+  const int st = check_norm(rows, H, eps, dtype);
+  if (st != MOE_OK) return st;
+  const size_t n = (size_t)rows * H * elem(dtype);
+  if (out != x && overlap(out, n, x, n)) return MOE_ERR_INVALID_ARG;
+  return from_hip(moe::launch_norm(x, weight, bias, rows, H, eps, kind, dtype == MOE_BF16, out,
+                                   as_stream(stream)));
+}
+
+int moe_norm_residual(const void* y, int kind, const void* weight, const void* bias,
+                      const void* res, const void* gate, int gate_mode, float scale,
+                      int next_kind, const void* next_weight, const void* next_bias, int rows,
+                      int H, float eps, int dtype, void* res_out, void* next_out, void* stream) {
+  if (!y || !res || !res_out || !norm_kind_ok(kind) || !norm_kind_ok(next_kind))
+    return MOE_ERR_INVALID_ARG;
+  if (gate_mode < MOE_GATE_NONE || gate_mode > MOE_GATE_FULL || !std::isfinite(scale))
+    return MOE_ERR_INVALID_ARG;
+  if ((gate_mode == MOE_GATE_NONE) != (gate == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (kind == MOE_NORM_NONE && (weight || bias)) return MOE_ERR_INVALID_ARG;
+  if (next_kind == MOE_NORM_NONE && (next_weight || next_bias)) return MOE_ERR_INVALID_ARG;
+  if ((next_kind == MOE_NORM_NONE) != (next_out == nullptr)) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {y, weight, bias, res, gate, next_weight, next_bias, (const void*)res_out,
+                        (const void*)next_out})
+    if (!aligned_or_null(p)) return MOE_ERR_INVALID_ARG;
+  const int st = check_norm(rows, H, eps, dtype);
+  if (st != MOE_OK) return st;
+  const size_t n = (size_t)rows * H * elem(dtype);
+  if (overlap(res_out, n, y, n) || overlap(next_out, n, res, n) || overlap(next_out, n, res_out, n) ||
+      (res_out != res && overlap(res_out, n, res, n)) || (next_out != y && overlap(next_out, n, y, n)))
+    return MOE_ERR_INVALID_ARG;
+  return from_hip(moe::launch_norm_residual(y, kind, weight, bias, res, gate, gate_mode, scale,
+                                            next_kind, next_weight, next_bias, rows, H, eps,
+                                            dtype == MOE_BF16, res_out, next_out,
+                                            as_stream(stream)));
+}
+
+size_t moe_route_grouped_workspace_bytes(int T, int H, int E, int k, int dtype) {
+  if (!dtype_ok(dtype) || check_tokens(T, H, E, k) != MOE_OK) return 0;
+  return moe::route_grouped_ws_bytes(T, H, E, dtype == MOE_BF16);
+}
+
+int moe_route_grouped(const void* x, const void* wg, const float* bias, int T, int H, int E, int k,
+                      int score, int groups, int topk_groups, int group_top, int renorm,
+                      float scale, int dtype, int32_t* topk_idx, float* topk_w, void* ws,
+                      size_t ws_bytes, void* stream) {
+  if (!x || !wg || !topk_idx || !topk_w || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(wg) || !aligned_or_null(ws)) return MOE_ERR_INVALID_ARG;
+  int st = check_tokens(T, H, E, k);
+  if (st != MOE_OK) return st;
+  st = check_grouped(E, k, score, groups, topk_groups, group_top, renorm, scale);
+  if (st != MOE_OK) return st;
+  const size_t need = moe::route_grouped_ws_bytes(T, H, E, dtype == MOE_BF16);
+  if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  return from_hip(moe::launch_route_grouped(x, wg, bias, T, H, E, k, score == MOE_SCORE_SOFTMAX,
+                                            groups, topk_groups, group_top, renorm != 0, scale,
+                                            dtype == MOE_BF16, topk_idx, topk_w, ws,
+                                            as_stream(stream)));
+}
+
+size_t moe_linear_workspace_bytes(int M, int N, int K, int act, int dtype) {
+  if (check_linear(1, M, N, K, act, dtype) != MOE_OK) return 0;
+  return moe::linear_ws_bytes(1, M, N, K, act, false, dtype == MOE_BF16);
+}
+
+int moe_linear(const void* x, const void* w, const void* bias, int act, const void* residual,
+               int M, int N, int K, int dtype, void* y, void* ws, size_t ws_bytes, void* stream) {
+  if (!x || !w || !y) return MOE_ERR_INVALID_ARG;
+  const int st = check_linear(1, M, N, K, act, dtype);
+  if (st != MOE_OK) return st;
+  return run_linear(x, nullptr, 1, M, nullptr, 1, M, w, bias, act, residual, N, K, dtype, y, ws,
+                    ws_bytes, stream);
+}
+
+size_t moe_linear_grouped_workspace_bytes(int E, int rows, int N, int K, int act, int dtype) {
+  if (check_linear(E, rows, N, K, act, dtype) != MOE_OK) return 0;
+  return moe::linear_ws_bytes(E, rows, N, K, act, true, dtype == MOE_BF16);
+}
+
+int moe_linear_grouped(const void* x, const int32_t* perm, int k, int T, const int32_t* offsets,
+                       int E, int rows, const void* w, const void* bias, int act,
+                       const void* residual, int N, int K, int dtype, void* y, void* ws,
+                       size_t ws_bytes, void* stream) {
+  if (!x || !offsets || !w || !y) return MOE_ERR_INVALID_ARG;
+  const int st = check_linear(E, rows, N, K, act, dtype);
+  if (st != MOE_OK) return st;
+  if (perm) {
+    if (T < 1 || k < 1) return MOE_ERR_INVALID_ARG;
+    if (k > kMaxTopK || (long long)T * k >= (1LL << 31) || rows > (long long)T * k)
+      return MOE_ERR_UNSUPPORTED;
+  }
+  return run_linear(x, perm, k, T, offsets, E, rows, w, bias, act, residual, N, K, dtype, y, ws,
+                    ws_bytes, stream);
 }
 
 }  // extern "C"

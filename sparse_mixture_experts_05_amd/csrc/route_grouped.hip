@@ -1,0 +1,365 @@
+// Grouped routing: sigmoid or softmax scores, a balance bias that moves the
+// choice and not the weights, experts limited to the best groups, top-k,
+// renormalised and scaled weights. The choice by biased scores with unbiased
+// weights is the other reading of the balance bias of "Kimi K3
+// 专家路由不均衡诊断" section 4.2 (moe_route has it inside the softmax); top-k and the
+// renormalisation are those of the "hncyxsy.com Kimi K3 fine-grained MoE"
+// article's router listing.
+//
+//   s = x . Wg^T                      p = sigmoid(s) or softmax(s)
+//   v = p + b (b = -inf or NaN, or a NaN score: the expert is off)
+//   group score = sum of the group's 1 or 2 largest v (experts that are on)
+//   chosen: the topk_groups best groups, in them the k largest v
+//   w_j = scale * p_j / (renorm ? sum_j' p_j' : 1)
+//
+// Without a bias the experts of the chosen groups are ordered by s itself
+// (both score functions are monotone), so scores past the point where p rounds
+// to 1 or 0 keep their order. Renormalised weights are taken relative to the
+// largest chosen score, so they do not underflow together.
+//
+// The scores come from the score tiles of route_tile.hpp (MFMA, fp32
+// accumulation); selection works on the fp32 scores in LDS.
+#include "kernels.hpp"
+#include "route_tile.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxGroups = 64;  // one bit each of a token's 64-bit group mask
+
+struct GroupArgs {
+  const float* bias;  // [E] or null
+  int groups, per, topk_groups, group_top;
+  uint32_t magic;     // e / per == (e * magic) >> 16 for e < 256
+  int softmax, renorm;
+  float scale;
+};
+
+__device__ __forceinline__ float sigmoidf(float s) { return 1.0f / (1.0f + expf(-s)); }
+
+// LDS of the group stage of BT tokens, behind the score tile.
+template <int BT>
+struct GroupLds {
+  float gs[BT][kMaxGroups];        // group scores
+  unsigned long long mask[BT];     // chosen groups
+  float top[BT], rz[BT];           // softmax: largest score, 1 / sum
+};
+
+// Value that the choice is made on: v, or with no bias at all the score.
+// NaN and -inf leave the expert off.
+__device__ __forceinline__ float prob_of(const GroupArgs& a, float s, float top, float rz) {
+  return a.softmax ? expf(s - top) * rz : sigmoidf(s);
+}
+
+template <int L, int G>
+__device__ __forceinline__ float group_max(float v) {
+  if constexpr ((1 << L) < G) return group_max<L + 1, G>(fmaxf(v, __uint_as_float(partner<L>(__float_as_uint(v)))));
+  return v;
+}
+
+// Chooses for the BT tokens whose scores are in the LDS tile sc (row stride
+// tile_stride<BT, NW>(), no bias in them). Lanes as in topk_tokens: G = 64 *
+// NW / BT lanes a token, lane g reads the experts g, g + G, ...
+template <int BT, int KP, int EPX, int NW>
+__device__ __forceinline__ void grouped_tokens(float* sc, GroupLds<BT>& L, const GroupArgs& a,
+                                               int t0, int T, int E, int k,
+                                               int32_t* __restrict__ topk_idx,
+                                               float* __restrict__ topk_w) {
+  constexpr int NT = NW * 64, G = NT / BT, S = tile_stride<BT, NW>();
+  static_assert(G >= 1 && G <= 64 && BT * G == NT, "one group of lanes per token");
+  constexpr int NSUB = (EPX + G - 1) / G;
+  constexpr int NBLK = (NSUB + KP - 1) / KP;
+  const int t = threadIdx.x / G, g = threadIdx.x % G;
+  const int tok = t0 + t;
+  const float* row = sc + t * S;
+  const bool limit = a.topk_groups < a.groups;
+
+  float top = 0.0f, rz = 1.0f;
+  if (a.softmax) {
+    float m = -INFINITY, z = 0.0f;
+    for (int e = g; e < E; e += G) m = fmaxf(m, row[e]);  // fmaxf drops a NaN
+    top = group_max<0, G>(m);
+    for (int e = g; e < E; e += G) {
+      const float d = row[e] - top;
+      z += d == d ? expf(d) : 0.0f;
+    }
+    rz = 1.0f / group_sum<0, G>(z);
+    if (g == 0) {
+      L.top[t] = top;
+      L.rz[t] = rz;
+    }
+  }
+  if (limit) {
+    if (g == 0) L.mask[t] = 0;
+    __syncthreads();
+    // one thread per (token, group); each starts at another expert of its
+    // group, which spreads the LDS banks when groups are a power of two wide
+    for (int q = threadIdx.x; q < BT * a.groups; q += NT) {
+      const int qt = q / a.groups, qg = q - qt * a.groups;
+      const float* r = sc + qt * S + qg * a.per;
+      const float* b = a.bias != nullptr ? a.bias + qg * a.per : nullptr;
+      const float tm = a.softmax ? L.top[qt] : 0.0f, z = a.softmax ? L.rz[qt] : 1.0f;
+      float b1 = -INFINITY, b2 = -INFINITY;
+      int i = qg % a.per;
+      for (int n = 0; n < a.per; ++n) {
+        float v = prob_of(a, r[i], tm, z);
+        if (b != nullptr) v += b[i];
+        v = fmaxf(v, -INFINITY);
+        b2 = fmaxf(b2, fminf(b1, v));
+        b1 = fmaxf(b1, v);
+        i = i + 1 == a.per ? 0 : i + 1;
+      }
+      // the second counts only if it is on
+      L.gs[qt][qg] = a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+    }
+    __syncthreads();
+    for (int q = threadIdx.x; q < BT * a.groups; q += NT) {
+      const int qt = q / a.groups, qg = q - qt * a.groups;
+      const float own = L.gs[qt][qg];
+      int rank = 0;
+      for (int o = 0; o < a.groups; ++o) {
+        const float v = L.gs[qt][o];
+        rank += v > own || (v == own && o < qg);
+      }
+      if (rank < a.topk_groups) atomicOr(&L.mask[qt], 1ull << qg);
+    }
+    __syncthreads();
+  }
+  const unsigned long long mask = limit ? L.mask[t] : ~0ull;
+
+  uint64_t list[KP];
+#pragma unroll
+  for (int b = 0; b < NBLK; ++b) {
+    uint64_t blk[KP];
+#pragma unroll
+    for (int i = 0; i < KP; ++i) {
+      const int e = g + G * (b * KP + i);
+      const int ec = min(e, E - 1);
+      float v = row[ec];
+      if (a.bias != nullptr) v = prob_of(a, v, top, rz) + a.bias[ec];
+      const bool in = e < E && ((mask >> ((ec * a.magic) >> 16)) & 1);
+      blk[i] = topk_key(v, e) & (uint64_t)(-(int64_t)in);
+    }
+    bitonic_sort<KP>(blk);
+    if (b == 0) {
+#pragma unroll
+      for (int i = 0; i < KP; ++i) list[i] = blk[i];
+    } else {
+      merge_top<KP>(list, blk);
+    }
+  }
+  group_merge<0, G, KP>(list);
+
+  // the chosen scores; an expert that is off (chosen only when fewer than k
+  // are on) weighs nothing
+  float sj[KP], m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < KP; ++j) {
+    sj[j] = -INFINITY;
+    if (j < k && key_score(list[j]) > -INFINITY) sj[j] = row[key_expert(list[j])];
+    m = fmaxf(m, sj[j]);
+  }
+  // renormalised: p_j times a factor that all j share (softmax: Z * exp(top - m);
+  // sigmoid: exp(-min(m, 0)))
+  if (!a.softmax) m = fminf(m, 0.0f);
+  float p[KP], sum = 0.0f;
+#pragma unroll
+  for (int j = 0; j < KP; ++j) {
+    p[j] = 0.0f;
+    if (j < k && sj[j] > -INFINITY) {
+      if (!a.renorm) p[j] = prob_of(a, sj[j], top, rz);
+      else if (a.softmax) p[j] = expf(sj[j] - m);
+      else p[j] = sj[j] > 0.0f ? sigmoidf(sj[j]) : expf(sj[j] - m) / (1.0f + expf(sj[j]));
+    }
+    sum += p[j];
+  }
+  const float f = a.renorm ? (sum > 0.0f ? a.scale / sum : sum * 0.0f) : a.scale;
+  if (tok < T) {
+#pragma unroll
+    for (int j = 0; j < KP; ++j)
+      if (j < k && j % G == g) {
+        topk_idx[(size_t)tok * k + j] = key_expert(list[j]);
+        topk_w[(size_t)tok * k + j] = p[j] * f;
+      }
+  }
+}
+
+template <int BT, int EPX, int NW = 4>
+__device__ __forceinline__ void grouped_phase(float* sc, GroupLds<BT>& L, const GroupArgs& a,
+                                              int t0, int T, int E, int k,
+                                              int32_t* __restrict__ idx, float* __restrict__ w) {
+  if (k <= 1) grouped_tokens<BT, 1, EPX, NW>(sc, L, a, t0, T, E, k, idx, w);
+  else if (k <= 2) grouped_tokens<BT, 2, EPX, NW>(sc, L, a, t0, T, E, k, idx, w);
+  else if (k <= 4) grouped_tokens<BT, 4, EPX, NW>(sc, L, a, t0, T, E, k, idx, w);
+  else grouped_tokens<BT, 8, EPX, NW>(sc, L, a, t0, T, E, k, idx, w);
+}
+
+// One launch: BT tokens x all E experts (EP >= E) over all of H, then the choice.
+template <int BT, int EP, int NW>
+__global__ __launch_bounds__(NW * 64) void grouped_bf16_kernel(
+    const uint16_t* __restrict__ x, const uint16_t* __restrict__ wg, GroupArgs a, int T, int H,
+    int E, int k, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
+  using C = RouteTile<BT, EP, NW>;
+  constexpr int NEED = C::SC_BYTES + (int)sizeof(GroupLds<BT>);
+  constexpr int LDS = C::LDS > NEED ? C::LDS : NEED;
+  static_assert(LDS <= 160 * 1024 && C::SC_BYTES % 8 == 0, "score tile and group stage in LDS");
+  __shared__ __align__(16) uint8_t smem[LDS];
+  const int t0 = blockIdx.x * BT;
+  f32x4_t acc[C::MC][C::NC];
+  score_tile<BT, EP, NW>(smem, x, wg, t0, T, 0, E, H, 0, H / 64, acc);
+  scores_to_lds<BT, EP, NW>(smem, E, nullptr, acc);
+  grouped_phase<BT, EP, NW>(reinterpret_cast<float*>(smem),
+                            *reinterpret_cast<GroupLds<BT>*>(smem + C::SC_BYTES), a, t0, T, E, k,
+                            topk_idx, topk_w);
+}
+
+// Second launch of the two-launch paths: the K slices of each score are summed
+// in slice order, then the choice.
+template <int NKS, int BT, int EPX>
+__global__ __launch_bounds__(kThreads) void grouped_select_kernel(const float* __restrict__ ws,
+                                                                  GroupArgs a, int T, int E, int k,
+                                                                  int32_t* __restrict__ topk_idx,
+                                                                  float* __restrict__ topk_w) {
+  constexpr int S = tile_stride<BT>();
+  __shared__ float sc[BT * S];
+  __shared__ GroupLds<BT> L;
+  const int t0 = blockIdx.x * BT;
+  // about 32 loads in flight per thread, from addresses clamped into the buffer
+  constexpr int PER = NKS >= 8 ? 32 / NKS : 8;
+  const int nval = min(BT, T - t0) * E;
+  for (int p0 = threadIdx.x; p0 < nval; p0 += PER * kThreads) {
+    float v[PER][NKS];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int p = p0 + i * kThreads;
+      const int tt = min(t0 + p / E, T - 1), e = p % E;
+#pragma unroll
+      for (int q = 0; q < NKS; ++q) v[i][q] = ws[((size_t)q * T + tt) * E + e];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int p = p0 + i * kThreads;
+      if (p < nval) {
+        float s = 0.0f;
+#pragma unroll
+        for (int q = 0; q < NKS; ++q) s += v[i][q];
+        sc[p / E * S + p % E] = s;
+      }
+    }
+  }
+  __syncthreads();
+  grouped_phase<BT, EPX>(sc, L, a, t0, T, E, k, topk_idx, topk_w);
+}
+
+// fp32 scores with plain dot products (small fp32 layers).
+__global__ __launch_bounds__(kThreads) void grouped_f32_kernel(
+    const float* __restrict__ x, const float* __restrict__ wg, GroupArgs a, int T, int H, int E,
+    int k, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
+  constexpr int BT = 16;
+  constexpr int S = tile_stride<BT>();
+  __shared__ float sc[BT * S];
+  __shared__ GroupLds<BT> L;
+  const int t0 = blockIdx.x * BT;
+  for (int p = threadIdx.x; p < BT * E; p += kThreads) {
+    const int t = p / E, e = p % E;
+    const float4* xr = reinterpret_cast<const float4*>(x + (size_t)min(t0 + t, T - 1) * H);
+    const float4* wr = reinterpret_cast<const float4*>(wg + (size_t)e * H);
+    float s = 0.0f;
+    for (int h = 0; h < H / 4; ++h) {
+      const float4 u = xr[h], b = wr[h];
+      s = fmaf(u.x, b.x, s);
+      s = fmaf(u.y, b.y, s);
+      s = fmaf(u.z, b.z, s);
+      s = fmaf(u.w, b.w, s);
+    }
+    sc[t * S + e] = s;
+  }
+  __syncthreads();
+  grouped_phase<BT, kMaxE>(sc, L, a, t0, T, E, k, topk_idx, topk_w);
+}
+
+template <int BT, int EPX>
+hipError_t launch_select_e(int nks, const float* ws, const GroupArgs& a, int T, int E, int k,
+                           int32_t* idx, float* w, hipStream_t s) {
+  const dim3 grid((T + BT - 1) / BT), block(kThreads);
+  switch (nks) {
+    case 1: hipLaunchKernelGGL((grouped_select_kernel<1, BT, EPX>), grid, block, 0, s, ws, a, T, E, k, idx, w); break;
+    case 2: hipLaunchKernelGGL((grouped_select_kernel<2, BT, EPX>), grid, block, 0, s, ws, a, T, E, k, idx, w); break;
+    case 4: hipLaunchKernelGGL((grouped_select_kernel<4, BT, EPX>), grid, block, 0, s, ws, a, T, E, k, idx, w); break;
+    case 8: hipLaunchKernelGGL((grouped_select_kernel<8, BT, EPX>), grid, block, 0, s, ws, a, T, E, k, idx, w); break;
+    case 16: hipLaunchKernelGGL((grouped_select_kernel<16, BT, EPX>), grid, block, 0, s, ws, a, T, E, k, idx, w); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+template <int BT>
+hipError_t launch_select(int nks, const float* ws, const GroupArgs& a, int T, int E, int k,
+                         int32_t* idx, float* w, hipStream_t s) {
+  if (E <= 64) return launch_select_e<BT, 64>(nks, ws, a, T, E, k, idx, w, s);
+  if (E <= 128) return launch_select_e<BT, 128>(nks, ws, a, T, E, k, idx, w, s);
+  return launch_select_e<BT, kMaxE>(nks, ws, a, T, E, k, idx, w, s);
+}
+
+template <int BT, int EP, int NW = 4>
+hipError_t launch_bf16(const void* x, const void* wg, const GroupArgs& a, int T, int H, int E,
+                       int k, int32_t* idx, float* w, hipStream_t s) {
+  hipLaunchKernelGGL((grouped_bf16_kernel<BT, EP, NW>), dim3((T + BT - 1) / BT), dim3(NW * 64), 0,
+                     s, static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(wg), a, T, H,
+                     E, k, idx, w);
+  return hipGetLastError();
+}
+
+template <int BT>
+hipError_t launch_bf16_bt(const void* x, const void* wg, const GroupArgs& a, int T, int H, int E,
+                          int k, int32_t* idx, float* w, hipStream_t s) {
+  if (E <= 16) return launch_bf16<BT, 16>(x, wg, a, T, H, E, k, idx, w, s);
+  if (E <= 32) return launch_bf16<BT, 32>(x, wg, a, T, H, E, k, idx, w, s);
+  if (E <= 64) return launch_bf16<BT, 64>(x, wg, a, T, H, E, k, idx, w, s);
+  if (E <= 128) return launch_bf16<BT, 128, route_waves<BT, 128>()>(x, wg, a, T, H, E, k, idx, w, s);
+  return launch_bf16<BT, 256, route_waves<BT, 256>()>(x, wg, a, T, H, E, k, idx, w, s);
+}
+
+}  // namespace
+
+size_t route_grouped_ws_bytes(int T, int H, int E, bool bf16) {
+  return scores_ws_bytes(T, H, E, bf16);
+}
+
+hipError_t launch_route_grouped(const void* x, const void* wg, const float* bias, int T, int H,
+                                int E, int k, bool softmax, int groups, int topk_groups,
+                                int group_top, bool renorm, float scale, bool bf16,
+                                int32_t* topk_idx, float* topk_w, void* ws, hipStream_t s) {
+  GroupArgs a{};
+  a.bias = bias;
+  a.groups = groups;
+  a.per = E / groups;
+  a.topk_groups = topk_groups;
+  a.group_top = group_top;
+  a.magic = (65536u + a.per - 1) / a.per;
+  a.softmax = softmax;
+  a.renorm = renorm;
+  a.scale = scale;
+  if (route_mode(T, E, bf16) != kOneLaunch) {
+    const int nks = route_kslices(T, H, E);
+    const hipError_t err = launch_partial(x, wg, T, H, E, static_cast<float*>(ws), s);
+    if (err != hipSuccess) return err;
+    const float* wsf = static_cast<const float*>(ws);
+    return select_tokens_per_block(T) == 16
+               ? launch_select<16>(nks, wsf, a, T, E, k, topk_idx, topk_w, s)
+               : launch_select<4>(nks, wsf, a, T, E, k, topk_idx, topk_w, s);
+  }
+  if (!bf16) {
+    hipLaunchKernelGGL(grouped_f32_kernel, dim3((T + 15) / 16), dim3(kThreads), 0, s,
+                       static_cast<const float*>(x), static_cast<const float*>(wg), a, T, H, E, k,
+                       topk_idx, topk_w);
+    return hipGetLastError();
+  }
+  switch (bf16_tokens_per_block(T)) {
+    case 64: return launch_bf16_bt<64>(x, wg, a, T, H, E, k, topk_idx, topk_w, s);
+    case 32: return launch_bf16_bt<32>(x, wg, a, T, H, E, k, topk_idx, topk_w, s);
+    default: return launch_bf16_bt<16>(x, wg, a, T, H, E, k, topk_idx, topk_w, s);
+  }
+}
+
+}  // namespace moe

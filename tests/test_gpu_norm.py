@@ -1,0 +1,153 @@
+"""GPU: moe_norm and moe_norm_residual against the formulas in float64.
+
+Tolerances, element by element. u = 2^-24 is the fp32 half step, half(dtype)
+the output's: bf16 2^-8, fp32 2^-24 (relative). The statistics are sums of H
+terms, at most 64 in a thread one after the other, then at most 6 + 16 levels:
+under 96 u relative to the sum of magnitudes; the square root, the division
+and the products add a few u. So norm(v) is off by at most
+    C u (r |w| (|v - mu| + mean|v|) + |b|),  C = 128, r = 1 / sqrt(var + eps)
+(the mean|v| term is the mean's own error, layer kind only), plus the rounding
+half * |y|. An error d in v itself moves norm(v) by at most
+    r |w| (d + mean d) + |v - mu| r^2 |w| rms(d)
+(the last factor: sqrt(var) moves by at most rms(d)).
+"""
+import numpy as np
+import pytest
+import torch
+
+import sparse_mixture_experts_05_amd as moe
+
+pytestmark = pytest.mark.gpu
+U, C = 2.0 ** -24, 128.0
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+DTYPES = [torch.bfloat16, torch.float32]
+ID = lambda v: str(v).replace("torch.", "")  # noqa: E731
+
+
+def draw(shape, dtype, seed, mean=0.0, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g, dtype=torch.float64) * std + mean).to(dtype)
+
+
+def norm64(v, kind, w, b, eps, dv=0.0):
+    """(norm(v), its error bound before rounding) for v known up to dv."""
+    if kind == "none":
+        return v, dv * torch.ones_like(v)
+    w = 1.0 if w is None else w.double()
+    b = torch.zeros((), dtype=torch.float64) if b is None else b.double()
+    mu = v.mean(1, keepdim=True) if kind == "layer" else 0.0
+    c = v - mu
+    r = 1 / torch.sqrt((c * c).mean(1, keepdim=True) + eps)
+    mean_abs = v.abs().mean(1, keepdim=True) if kind == "layer" else 0.0
+    aw = w.abs() if isinstance(w, torch.Tensor) else w
+    err = C * U * (r * aw * (c.abs() + mean_abs) + b.abs())
+    d = dv * torch.ones_like(v)
+    err = err + r * aw * (d + d.mean(1, keepdim=True)) \
+        + c.abs() * r * r * aw * d.square().mean(1, keepdim=True).sqrt()
+    return c * r * w + b, err
+
+
+def near(got, want, err, dtype, name):
+    got = got.cpu().double()
+    off = (got - want).abs() - (err + HALF[dtype] * want.abs() * (1 + 2.0 ** -6) + 1e-38)
+    assert not torch.isnan(got).any(), name
+    assert off.max() <= 0, f"{name}: {off.max():.3e} over, at {np.unravel_index(int(off.argmax()), got.shape)}"
+
+
+def cuda(t):
+    return None if t is None else t.cuda()
+
+
+SHAPES = [(1, 4096), (1, 1), (5, 1), (3, 63), (4, 64), (257, 512), (9001, 64), (2049, 129),
+          (3, 1000), (7, 1024), (6, 2048), (5, 2499), (33, 4096), (3, 4097), (4, 8192), (3, 12288),
+          (2, 16383), (2, 16384)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ID)
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("T,H", SHAPES)
+def test_norm(T, H, kind, dtype):
+    print(f"\n[gpu] norm {T} {H} {kind} {dtype}", flush=True)
+    # a mean well off zero: a variance as a difference of squares would lose it
+    x = draw((T, H), dtype, 1, mean=3.0)
+    w, b = draw((H,), dtype, 2, 1.0, 0.2), draw((H,), dtype, 3)
+    for ww, bb in ((w, b), (w, None), (None, None)):
+        got = moe.moe_norm(x.cuda(), cuda(ww), cuda(bb), eps=1e-5, kind=kind)
+        near(got, *norm64(x.double(), kind, ww, bb, 1e-5), dtype, "y")
+    xi = x.cuda()  # in place
+    assert moe.moe_norm(xi, w.cuda(), b.cuda(), eps=1e-5, kind=kind, out=xi) is xi
+    assert torch.equal(xi, moe.moe_norm(x.cuda(), w.cuda(), b.cuda(), eps=1e-5, kind=kind))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ID)
+@pytest.mark.parametrize("T,H", [(1, 64), (37, 320), (5, 2499), (300, 4096), (3, 16384), (4, 16381)])
+@pytest.mark.parametrize("kind,gate,nkind", [
+    ("none", None, "none"), ("rms", None, "none"), ("none", "token", "rms"),
+    ("rms", "channel", "rms"), ("layer", "full", "layer"), ("layer", "token", "none"),
+    ("none", "full", "layer")])
+def test_norm_residual(T, H, kind, gate, nkind, dtype):
+    print(f"\n[gpu] residual {T} {H} {kind} {gate} {nkind} {dtype}", flush=True)
+    y, res = draw((T, H), dtype, 1, mean=0.5), draw((T, H), dtype, 2, std=3.0)
+    gshape = {None: None, "token": (T, 1), "channel": (H,), "full": (T, H)}[gate]
+    g = None if gate is None else draw(gshape, dtype, 3)
+    par = lambda k, s: (None, None) if k == "none" else (  # noqa: E731
+        draw((H,), dtype, s, 1.0, 0.2), draw((H,), dtype, s + 1))
+    (w, b), (nw, nb) = par(kind, 4), par(nkind, 6)
+    scale, eps = 0.37, 1e-6
+    z, dz = norm64(y.double(), kind, w, b, eps)
+    f = np.float64(np.float32(scale)) * (1.0 if g is None else g.double())
+    h = res.double() + f * z
+    af = abs(f) if not isinstance(f, torch.Tensor) else f.abs()
+    dh = af * dz + 4 * U * (res.double().abs() + af * z.abs())
+    args = dict(gate=cuda(g), scale=scale, eps=eps, kind=kind, next_kind=nkind, weight=cuda(w),
+                bias=cuda(b), next_weight=cuda(nw), next_bias=cuda(nb))
+    rout, nout = moe.moe_norm_residual(y.cuda(), res.cuda(), **args)
+    near(rout, h, dh, dtype, "res_out")
+    if nkind == "none":
+        assert nout is None
+    else:
+        near(nout, *norm64(h, nkind, nw, nb, eps, dh), dtype, "next_out")
+    # in place: the residual stream and the block's output are overwritten
+    yi, ri = y.cuda(), res.cuda()
+    moe.moe_norm_residual(yi, ri, res_out=ri, next_out=None if nkind == "none" else yi, **args)
+    assert torch.equal(ri, rout)
+    assert torch.equal(yi, y.cuda() if nkind == "none" else nout)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ID)
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_rows_do_not_touch_each_other(kind, dtype):
+    print(f"\n[gpu] norm rows {kind} {dtype}", flush=True)
+    x = draw((9, 1000), dtype, 1)
+    want = moe.moe_norm(x.cuda(), kind=kind).cpu()
+    x[2, 7], x[4, 0], x[5, 999] = float("nan"), float("inf"), float("-inf")
+    got = moe.moe_norm(x.cuda(), kind=kind).cpu()
+    clean = [0, 1, 3, 6, 7, 8]
+    assert torch.equal(got[clean], want[clean])
+    assert torch.isnan(got[2]).all()
+    # a row of zeros is 0 under eps > 0; constant rows have no variance
+    z = torch.zeros((2, 333), dtype=dtype, device="cuda")
+    assert (moe.moe_norm(z, kind=kind) == 0).all()
+    if kind == "layer":
+        assert (moe.moe_norm(z + 2.0, kind=kind) == 0).all()
+
+
+def test_other_stream_and_graph():
+    print("\n[gpu] norm stream and graph", flush=True)
+    x, res = draw((64, 4096), torch.bfloat16, 1).cuda(), draw((64, 4096), torch.bfloat16, 2).cuda()
+    w = draw((4096,), torch.bfloat16, 3).cuda()
+    want = moe.moe_norm_residual(x, res, w, next_kind="rms", next_weight=w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = moe.moe_norm_residual(x, res, w, next_kind="rms", next_weight=w, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = moe.moe_norm_residual(x, res, w, next_kind="rms", next_weight=w)
+    for rep in range(4):
+        x.copy_(draw((64, 4096), torch.bfloat16, 10 + rep).cuda())
+        graph.replay()
+        want = moe.moe_norm_residual(x, res, w, next_kind="rms", next_weight=w)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), rep

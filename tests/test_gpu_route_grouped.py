@@ -1,0 +1,219 @@
+"""GPU: moe_route_grouped against its definition in float64 (numpy).
+
+Ids are compared exactly. Two kinds of input make that sound:
+  * exact scores: each token is a one-hot row and the gate holds small integers,
+    so every score is exact and ties are common; values that differ, differ by
+    far more than fp32 (asserted), values that tie, tie in every bit;
+  * random rows, drawn again until every two values (or groups) that a decision
+    is between are at least 4e-5 apart.
+Weights: a score is off by at most about 4e-6 (fp32 sums of up to 4096 products,
+|s| ~ 1), sigmoid and softmax pass on at most twice that, relative, and the
+renormalisation doubles it: 1.6e-5 relative, plus a few ulp: 2e-5.
+"""
+import numpy as np
+import pytest
+import torch
+
+import sparse_mixture_experts_05_amd as moe
+
+pytestmark = pytest.mark.gpu
+RTOL_W = 2e-5
+
+
+def oracle(s, bias, k, score, groups, topk_groups, group_top, renorm, scale):
+    """(ids, weights, least distance of two values that a decision is between)."""
+    T, E = s.shape
+    s = np.where(np.isnan(s), -np.inf, s)
+    with np.errstate(over="ignore", invalid="ignore"):
+        if score == "sigmoid":
+            p = 1 / (1 + np.exp(-s))
+        else:
+            top = s.max(1, keepdims=True)
+            p = np.exp(s - np.where(np.isfinite(top), top, 0.0))
+            p = p / np.maximum(p.sum(1, keepdims=True), 1e-300)
+    v = p if bias is None else p + bias.astype(np.float64)
+    v = np.where(np.isnan(v) | np.isneginf(s) & (bias is None), -np.inf, v)
+    key = np.where(np.isneginf(v), -np.inf, s if bias is None else v)
+    per = E // groups
+    ids, w, gap = np.zeros((T, k), np.int32), np.zeros((T, k)), np.inf
+
+    def nearest(a):
+        d = -np.diff(a)
+        d = d[np.isfinite(d) & (d > 0)]
+        return d.min() if d.size else np.inf
+
+    for t in range(T):
+        allowed = np.ones(E, bool)
+        if topk_groups < groups:
+            gs = np.empty(groups)
+            for j in range(groups):
+                b = np.sort(v[t, j * per:(j + 1) * per])[::-1][:group_top]
+                b = b[~np.isneginf(b)]
+                gs[j] = b.sum() if b.size else -np.inf
+            order = np.lexsort((np.arange(groups), -gs))
+            gap = min(gap, nearest(gs[order]))
+            allowed[:] = False
+            for j in order[:topk_groups]:
+                allowed[j * per:(j + 1) * per] = True
+        e = np.nonzero(allowed)[0]
+        order = e[np.lexsort((e, -key[t, e]))]
+        gap = min(gap, nearest(key[t, order[: k + 1]]))
+        ids[t] = order[:k]
+        on = ~np.isneginf(key[t, ids[t]])
+        if renorm and score == "softmax" and on.any():
+            q = np.where(on, np.exp(s[t, ids[t]] - s[t, ids[t]][on].max()), 0.0)
+        elif renorm and score == "sigmoid" and on.any():
+            # p times a common factor, so that small scores keep their ratios
+            si = s[t, ids[t]]
+            m = min(0.0, si[on].max())
+            with np.errstate(over="ignore"):
+                q = np.where(on, np.where(si > 0, 1 / (1 + np.exp(-si)), np.exp(si - m) / (1 + np.exp(np.minimum(si, 0)))), 0.0)
+        else:
+            q = np.where(on, p[t, ids[t]], 0.0)
+        w[t] = q * scale / q.sum() if renorm and q.sum() > 0 else q * scale
+    return ids, w, gap
+
+
+def run(x, wg, bias, k, **kw):
+    i, w = moe.moe_route_grouped(x.cuda(), wg.cuda(), None if bias is None else torch.tensor(bias).cuda(),
+                                 k, **kw)
+    return i.cpu().numpy(), w.cpu().numpy()
+
+
+def check(got, want, tag):
+    ids, w, _ = want
+    bad = np.nonzero((got[0] != ids).any(1))[0]
+    assert bad.size == 0, f"{tag}: {bad.size} tokens differ, first {bad[0]}: {got[0][bad[0]]} for {ids[bad[0]]}"
+    np.testing.assert_allclose(got[1], w, rtol=RTOL_W, atol=1e-30)
+
+
+CONFIGS = [  # (E, k, groups, topk_groups, group_top)
+    (1, 1, 1, 1, 1), (8, 2, 1, 1, 1), (16, 4, 4, 2, 2), (60, 4, 6, 3, 1), (64, 8, 64, 8, 2),
+    (128, 8, 8, 4, 2), (256, 8, 8, 4, 2), (256, 1, 2, 1, 2), (255, 8, 5, 2, 2), (40, 3, 1, 1, 2),
+    (252, 8, 63, 3, 1),
+]
+TOKENS = [1, 3, 17, 200, 1024, 2048, 4099]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("cfg", CONFIGS, ids=str)
+def test_ties_and_off_experts(cfg, score):
+    """Exact scores: ties between experts and groups, experts off by bias or NaN."""
+    E, k, groups, tg, gt = cfg
+    for T, H in ((1, 64), (65, 128), (2100, 64), (8192, 64)):
+        print(f"\n[gpu] grouped ties {cfg} {score} T={T}", flush=True)
+        rng = np.random.default_rng(E * 31 + T)
+        x = np.zeros((T, H), np.float32)
+        x[np.arange(T), rng.integers(0, H, T)] = 1.0
+        wg = rng.integers(0, 5, (E, H)).astype(np.float32)
+        # one step a group where its scores are sums: equal sums then tie in every bit
+        steps = rng.integers(0, 3, groups if gt == 2 and groups > 1 else E)
+        bias = np.repeat(steps * 8.0, E // steps.size).astype(np.float32)
+        if E > 8:
+            bias[rng.integers(0, E, 3)] = -np.inf
+            bias[rng.integers(0, E)] = np.nan
+            bias[: E // groups] = -np.inf  # a whole group off
+        s = (x @ wg.T).astype(np.float64)
+        for b in (bias, None):
+            kw = dict(score=score, groups=groups, topk_groups=tg, group_top=gt, renorm=bool(T % 2),
+                      scale=2.5)
+            want = oracle(s, b, k, **kw)
+            assert want[2] > 1e-5
+            got = run(torch.tensor(x).bfloat16(), torch.tensor(wg).bfloat16(), b, k, **kw)
+            check(got, want, f"T={T} bias={b is not None}")
+
+
+def conditioned(T, H, E, k, dtype, bias, seed, **kw):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((T, H), generator=g).to(dtype)
+    wg = (torch.randn((E, H), generator=g) / H ** 0.5).to(dtype)
+    for _ in range(200):
+        s = (x.double() @ wg.double().t()).numpy()
+        bad = [t for t in range(T) if oracle(s[t:t + 1], bias, k, **kw)[2] < 4e-5]
+        if not bad:
+            return x, wg, s
+        x[bad] = torch.randn((len(bad), H), generator=g).to(dtype)
+    raise RuntimeError("no rows with clear decisions")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("T", TOKENS)
+def test_random_rows(T, dtype):
+    for n, (E, k, groups, tg, gt) in enumerate([(128, 8, 8, 4, 2), (256, 8, 1, 1, 1), (60, 4, 6, 3, 1)]):
+        if T > 2048 and n != 1:
+            continue
+        score, renorm = ("sigmoid", "softmax")[n % 2], n != 2
+        bias = (np.random.default_rng(n).standard_normal(E) * 0.05).astype(np.float32) if n == 0 else None
+        kw = dict(score=score, groups=groups, topk_groups=tg, group_top=gt, renorm=renorm, scale=1.5)
+        print(f"\n[gpu] grouped random T={T} E={E} {score} {dtype}", flush=True)
+        x, wg, s = conditioned(T, 320, E, k, dtype, bias, T + n, **kw)
+        check(run(x, wg, bias, k, **kw), oracle(s, bias, k, **kw), f"E={E}")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_far_scores_and_nothing_left(score):
+    """Scores past the rounding of p keep their order without a bias and their
+    ratios when renormalised; all experts off: weights 0, ids still valid."""
+    print(f"\n[gpu] grouped far {score}", flush=True)
+    E, H, k = 16, 64, 4
+    x = np.zeros((2, H), np.float32)
+    x[0, 0] = x[1, 1] = 1.0
+    wg = np.zeros((E, H), np.float32)
+    wg[:, 0] = 40.0 + np.arange(E)          # sigmoid rounds to 1
+    wg[:, 1] = -130.0 - np.arange(E)        # sigmoid (and exp) underflow
+    xt, wt = torch.tensor(x).bfloat16(), torch.tensor(wg).bfloat16()
+    s = wg[:, :2].T.astype(np.float64)
+    got = run(xt, wt, None, k, score=score)
+    want = oracle(s, None, k, score, 1, 1, 2, True, 1.0)
+    assert np.array_equal(got[0], want[0])
+    np.testing.assert_allclose(got[1], want[1], rtol=RTOL_W, atol=1e-12)
+    wi = wt.clone()
+    wi[:, 5] = -np.inf  # 0 * -inf: every score is NaN, nothing is on
+    got_i, got_w = run(xt, wi, None, k, score=score)
+    assert (got_w == 0).all() and (got_i == np.arange(k)).all()
+    off = np.full(E, -np.inf, np.float32)
+    got_i, got_w = run(xt, wt, off, k, score=score, groups=4, topk_groups=2)
+    assert (got_w == 0).all() and (got_i == np.arange(k)).all()
+    off[9] = 0.0
+    got_i, got_w = run(xt, wt, off, k, score=score, groups=4, topk_groups=1)
+    assert (got_i[:, 0] == 9).all() and (got_i[:, 1:] == [8, 10, 11]).all()
+    assert (got_w[:, 0] == 1).all() and (got_w[:, 1:] == 0).all()
+
+
+def test_stream_graph_and_bias_step():
+    """Captured with dispatch and the bias step: every replay routes with the bias
+    that the one before it left, like the eager calls."""
+    print("\n[gpu] grouped graph", flush=True)
+    T, H, E, k = 48, 256, 32, 4
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn((T, H), generator=g).bfloat16().cuda()
+    wg = (torch.randn((E, H), generator=g) / 16).bfloat16().cuda()
+    kw = dict(groups=4, topk_groups=2, scale=2.5)
+    bias, eager = (torch.zeros(E, device="cuda") for _ in range(2))
+
+    def step(b):
+        i, w = moe.moe_route_grouped(x, wg, b, k, **kw)
+        d = moe.moe_dispatch(i, x, E, gather=False)
+        moe.moe_bias_update(d["counts"], b, 0.01)
+        return i, w
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(bias)
+    torch.cuda.current_stream().wait_stream(side)
+    bias.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(bias)
+    bias.zero_()
+    for rep in range(5):
+        x.copy_(torch.randn((T, H), generator=g).bfloat16())
+        graph.replay()
+        want = step(eager)
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]) and torch.equal(bias, eager), rep
+    got = moe.moe_route_grouped(x, wg, bias, k, stream=side, **kw)
+    side.synchronize()
+    want = moe.moe_route_grouped(x, wg, bias, k, **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

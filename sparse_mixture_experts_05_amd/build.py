@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libmoe.so")
 PROBE_LIB = os.path.join(PKG, "libmoe_probe.so")
 
 SOURCES = ["route.hip", "dispatch.hip", "ffn.hip", "combine.hip", "stats.hip", "bias.hip",
-           "norm.hip", "route_grouped.hip", "linear.hip", "moe_api.cpp"]
+           "norm.hip", "route_grouped.hip", "linear.hip", "linear_big.hip", "moe_api.cpp"]
 PROBE_SOURCES = ["probe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -16,47 +16,14 @@
 
 #include "common.hpp"
 #include "kernels.hpp"
+#include "linear.hpp"
 
 namespace moe {
 namespace {
 
+using namespace lin;
+
 constexpr int kThreads = 256;
-
-struct LinArgs {
-  const void* x;     // [M, K] rows, or [gT, K] token rows with gather
-  const void* w;     // [E, N, K] or [E, 2, N, K]
-  const void* bias;  // [E, N] or [E, 2, N], or null
-  const void* res;   // [M, N] or null
-  void* y;           // [M, N]
-  const int32_t* offsets;  // [E+1], or null: one segment of all M rows
-  const int32_t* gather;   // buffer row p reads token gather[p] / gk, or null
-  int gk, gT;
-  int E, M, N, K;
-  int act;
-};
-
-__device__ __forceinline__ bool gated(int act) { return act == kActGeglu || act == kActSwiglu; }
-
-// x / (1 + exp(-x)); the bf16 form has the hardware's exp2 and reciprocal
-// (within a few fp32 ulp, far below the bf16 step of the result).
-__device__ __forceinline__ float silu_bf16(float a) {
-  return a * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(a * -1.44269504f));
-}
-__device__ __forceinline__ float silu_f32(float a) { return a / (1.0f + expf(-a)); }
-
-template <bool BF16>
-__device__ __forceinline__ float activate(int act, float a) {
-  if (act == kActGelu || act == kActGeglu) return BF16 ? gelu_bf16(a) : gelu_erf(a);
-  if (act == kActSilu || act == kActSwiglu) return BF16 ? silu_bf16(a) : silu_f32(a);
-  return a;
-}
-
-// Source row in x of buffer row p (perm clamped into [0, T*k): no read leaves x).
-__device__ __forceinline__ size_t x_row(const LinArgs& a, int p) {
-  if (a.gather == nullptr) return (size_t)p;
-  const long long last = (long long)a.gT * a.gk - 1;
-  return (size_t)(min((long long)max(a.gather[p], 0), last) / a.gk);
-}
 
 // Weight row of row r of a tile of interleaved gate and up rows whose first
 // output column is n0: rows 4q, 4q+1 are the gate rows of columns n0 + 2q,
@@ -318,23 +285,39 @@ bool linear_fits(int E, int M, int N, int K) {
   return lin_grid(a, 32, 32) < (1LL << 31);
 }
 
-size_t linear_ws_bytes(int, int, int, int, int, bool, bool) { return 0; }
+// Whether a launch takes the 256 x 256 tiles.
+static bool use_big(const lin::LinArgs& a, bool grouped) {
+  return a.M >= 64 * a.E && a.M >= 256 && lin::big_ok(a);
+}
+
+static LinArgs lin_args(const void* x, const int32_t* gather, int gk, int gT, const int32_t* offsets,
+                        int E, int M, int N, int K, int act) {
+  LinArgs a{};
+  a.x = x, a.offsets = offsets, a.gather = gather, a.gk = gk, a.gT = gT;
+  a.E = E, a.M = M, a.N = N, a.K = K, a.act = act;
+  return a;
+}
+
+size_t linear_ws_bytes(int E, int M, int N, int K, int act, bool grouped, bool bf16) {
+  if (!bf16) return 0;
+  const int32_t some = 0;  // only tested for null
+  const LinArgs a = lin_args(nullptr, nullptr, 1, M, grouped ? &some : nullptr, E, M, N, K, act);
+  return use_big(a, grouped) ? big_ws_bytes(a) : 0;
+}
 
 hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
                          const int32_t* offsets, int E, int M, int N, int K, const void* w,
-                         const void* bias, int act, const void* res, bool bf16, void* y, void*,
+                         const void* bias, int act, const void* res, bool bf16, void* y, void* ws,
                          hipStream_t s) {
-  LinArgs a{};
-  a.x = x, a.w = w, a.bias = bias, a.res = res, a.y = y;
-  a.offsets = offsets, a.gather = gather, a.gk = gk, a.gT = gT;
-  a.E = E, a.M = M, a.N = N, a.K = K, a.act = act;
+  LinArgs a = lin_args(x, gather, gk, gT, offsets, E, M, N, K, act);
+  a.w = w, a.bias = bias, a.res = res, a.y = y;
   const int bnc = act == kActGeglu || act == kActSwiglu ? 32 : 64;
-  if (bf16) {
-    hipLaunchKernelGGL((lin_bf16_kernel<64>), dim3((unsigned)lin_grid(a, 64, bnc)), dim3(kThreads), 0,
-                       s, a);
-  } else {
+  if (!bf16) {
     hipLaunchKernelGGL(lin_f32_kernel, dim3((unsigned)lin_grid(a, 64, bnc)), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
   }
+  if (use_big(a, offsets != nullptr)) return launch_big(a, ws, s);
+  hipLaunchKernelGGL((lin_bf16_kernel<64>), dim3((unsigned)lin_grid(a, 64, bnc)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

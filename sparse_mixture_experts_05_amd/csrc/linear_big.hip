@@ -1,0 +1,566 @@
+// The products with an epilogue (linear.hip) on large tiles: launches with
+// enough rows to be bound by the matrix cores.
+//
+// A workgroup of 4 waves (one per SIMD) computes 256 rows x 256 weight rows;
+// wave w the 128 x 128 block (rows (w / 2) * 128, weight rows (w % 2) * 128) as
+// 4 x 4 accumulators of v_mfma_f32_32x32x16_bf16 (all 256 accumulation
+// registers). The weights are the MFMA's A operand and the rows its B, so a lane
+// ends with runs of 4 consecutive output columns of one row: bias and residual
+// come and the result goes 8 bytes at a time, with no exchange between lanes.
+// A gated product gives each wave the gate rows of 64 columns in its first two
+// weight sub-tiles and their up rows in the other two: both factors of an output
+// meet in one lane, and the tile has 128 output columns.
+//
+// With one wave per SIMD nothing else feeds the matrix core, so the stage is
+// hand-ordered: the 8 fragment reads of the next 16-deep k slice and the LDS
+// copies of the stage after the next (global_load_lds, the rows in two stage
+// buffers, the weights in three) sit between the slice's 16 MFMAs, held there by
+// sched_barrier.
+//
+// Tile order and the split of a long K in the last round are plan.hpp's. A
+// grouped launch reads its tiles from a table that a planning launch writes from
+// the device's offsets; a dense launch works its tile out in place.
+#include <algorithm>
+#include <type_traits>
+#include <utility>
+
+#include "linear.hpp"
+#include "plan.hpp"
+
+namespace moe {
+namespace {
+
+using namespace lin;
+
+constexpr int kThreads = 256;
+constexpr int BM = 256, BN = 256;                // rows, weight rows of a tile
+constexpr int kTableInt4 = plan::kEntryInts / 4;
+constexpr size_t kPartTiles = (size_t)plan::kXcds * plan::kSlots;  // split units at most
+
+template <typename F, int... I>
+__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_impl(f, std::make_integer_sequence<int, N>{});
+}
+
+// The planner's view of a launch: weight rows as columns (a gated product has
+// 2 N), the dense form as the one group that has no offsets.
+MOE_HD inline plan::Shape shape_of(const LinArgs& a, bool gated_act) {
+  const int cols = gated_act ? 2 * a.N : a.N;
+  plan::Shape s{};
+  if (a.offsets != nullptr) {
+    s.E = a.E, s.rows = a.M, s.routed_N = cols, s.routed_K = a.K;
+    s.shared_N = cols, s.shared_K = a.K;
+  } else {
+    s.shared_M = a.M, s.shared_N = cols, s.shared_K = a.K;
+    s.routed_N = cols, s.routed_K = a.K;
+  }
+  s.split = a.part != nullptr ? 1 : 0;
+  s.slots = a.slots;
+  return s;
+}
+
+// Writes the tile table of a grouped launch: entries [0, slots) for the product
+// (workgroup g: slot g / 8 on XCD g % 8), then kReduceSlots for its split-K
+// reduce. Every workgroup scans the segments and resolves 256 slots.
+__global__ __launch_bounds__(kThreads) void lin_plan_kernel(LinArgs a) {
+  __shared__ plan::Tables L;
+  const plan::Shape sh = shape_of(a, gated(a.act));
+  const int tid = threadIdx.x;
+  int off, cnt, all, big, sml;
+  plan::group_entry<BM, BN>(sh, a.offsets, tid, off, cnt, all, big, sml);
+  L.goff[tid] = off;
+  L.gcnt[tid] = cnt;
+  L.pa[tid] = all;
+  L.ps[tid] = 0;  // no pairs of short segments
+  __syncthreads();
+  for (int d = 1; d < 256; d <<= 1) {
+    const int v = tid >= d ? L.pa[tid - d] : 0;
+    __syncthreads();
+    L.pa[tid] += v;
+    __syncthreads();
+  }
+  const plan::Sched S = plan::finish_schedule(sh, L);
+  const int i = blockIdx.x * kThreads + tid;
+  if (i >= a.slots + plan::kReduceSlots) return;
+  const int mode = i < a.slots ? 0 : 1;
+  const int g = mode ? i - a.slots : i;
+  plan::Tile ta{}, tb{};
+  const int kind = plan::resolve_slot<BM, BN, plan::kBlockCols>(sh, S, L, g % plan::kXcds,
+                                                                g / plan::kXcds, mode, ta, tb);
+  int e[plan::kEntryInts];
+  plan::encode_entry(kind, ta, tb, e);
+  int4* dst = const_cast<int4*>(a.table) + (size_t)kTableInt4 * i;
+#pragma unroll
+  for (int q = 0; q < kTableInt4; ++q)
+    dst[q] = make_int4(e[4 * q], e[4 * q + 1], e[4 * q + 2], e[4 * q + 3]);
+}
+
+// The same in every lane (the planner's values come through LDS or arithmetic the
+// compiler cannot prove uniform; the copies take their bases from scalars).
+__device__ __forceinline__ plan::Tile uniform(const plan::Tile& t) {
+  auto u = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  return plan::Tile{u(t.group), u(t.e), u(t.row0), u(t.M), u(t.n0), u(t.spl), u(t.ks), u(t.unit0)};
+}
+
+// Tile of slot i (of the product, or with reduce of its reduce launch). L: LDS
+// scratch for the dense form. False: no work.
+__device__ __forceinline__ bool tile_of(const LinArgs& a, bool gt, int i, bool reduce,
+                                        plan::Tables& L, plan::Tile& t) {
+  if (a.offsets != nullptr) {
+    const int4* e = a.table + (size_t)kTableInt4 * (reduce ? a.slots + i : i);
+    const int4 d0 = e[0];
+    if (d0.x != 0) return false;
+    const int4 d1 = e[1], d2 = e[2];
+    t = uniform(plan::Tile{0, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w, d2.x});
+    return true;
+  }
+  const plan::Shape sh = shape_of(a, gt);
+  if (threadIdx.x == 0) {
+    int off, cnt, all, big, sml;
+    plan::group_entry<BM, BN>(sh, nullptr, 0, off, cnt, all, big, sml);
+    L.goff[0] = off, L.gcnt[0] = cnt, L.pa[0] = all, L.pf[0] = all, L.ps[0] = 0;
+  }
+  __syncthreads();
+  const plan::Sched S = plan::finish_schedule(sh, L);
+  plan::Tile tb;
+  const int kind = plan::resolve_slot<BM, BN, plan::kBlockCols>(
+      sh, S, L, i % plan::kXcds, i / plan::kXcds, reduce ? 1 : 0, t, tb);
+  __syncthreads();  // L is the first stage buffer
+  t = uniform(t);
+  return kind == 0;
+}
+
+// Output of one lane: 4 consecutive columns of a row (16-bit, 8-byte aligned).
+struct Out4 {
+  float v[4];
+};
+__device__ __forceinline__ Out4 widen4(uint2 q) {
+  return Out4{{bf16_to_f32(q.x & 0xffffu), __uint_as_float(q.x & 0xffff0000u),
+               bf16_to_f32(q.y & 0xffffu), __uint_as_float(q.y & 0xffff0000u)}};
+}
+
+// act(g + bg) [* (u + bu)] [+ res] of 4 columns, packed to bf16 (no bias: zeros).
+template <int ACT>
+__device__ __forceinline__ uint2 finish4(const f32x4_t& g, const f32x4_t& u, const Out4& bg,
+                                         const Out4& bu, bool has_res, const Out4& res) {
+  constexpr bool GT = ACT == kActGeglu || ACT == kActSwiglu;
+  float o[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float x = activate<true>(ACT, g[c] + bg.v[c]);
+    if constexpr (GT) x *= u[c] + bu.v[c];
+    if (has_res) x += res.v[c];
+    o[c] = x;
+  }
+  return make_uint2(cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3]));
+}
+
+// Weight row of row r of a tile: the expert's row n0 + r, or for a gated product
+// (n0, N in output columns) wave half r / 128, sub-tile (r / 32) % 4: two of gate
+// rows, then two of up rows, of the same 64 columns.
+template <bool GT>
+__device__ __forceinline__ size_t tile_weight_row(int r, int n0, int N) {
+  if constexpr (!GT) return (size_t)min(n0 + r, N - 1);
+  const int j = (r >> 5) & 3;
+  return (size_t)(j >> 1) * N + min(n0 + (r >> 7) * 64 + (j & 1) * 32 + (r & 31), N - 1);
+}
+
+template <int ACT, bool RES>
+__global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
+  constexpr bool GT = ACT == kActGeglu || ACT == kActSwiglu;
+  constexpr int NW = 4, BK = 64;
+  constexpr int ROWB = BK * 2;                 // 128 bytes = 8 chunks of 16
+  constexpr int SM = 4, SN = 4;                // 32 x 32 sub-tiles of a wave
+  constexpr int RPI = 8;                       // rows per copy instruction
+  constexpr int A_INST = BM / RPI / NW, B_INST = BN / RPI / NW;  // copies per wave per stage
+  constexpr int A_STAGE = BM * ROWB, B_STAGE = BN * ROWB;
+  constexpr int LDS_BYTES = 2 * A_STAGE + 3 * B_STAGE;
+  constexpr int BC = GT ? BN / 2 : BN;         // output columns of a tile
+  static_assert(LDS_BYTES <= 160 * 1024 && BM * BC * 2 <= LDS_BYTES, "LDS of one workgroup");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[LDS_BYTES];
+
+  plan::Tile t;
+  if (!tile_of(a, GT, blockIdx.x, false, *reinterpret_cast<plan::Tables*>(smem), t)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int N = a.N, K = a.K, M = t.M;
+  const int n0 = GT ? t.n0 / 2 : t.n0;         // first output column
+  const int nvalid = min(BC, N - n0);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int wv = __builtin_amdgcn_readfirstlane(wave);
+
+  // Copy q of a wave fills 8 rows of a stage buffer, lane i row (wave * 8 + q) *
+  // 8 + i / 8, slot i & 7, which holds chunk (i & 7) ^ ((r >> 1) & 7) of the row
+  // (the 16 lanes a 128-bit LDS read serves together then hit all 64 banks
+  // once). ov: byte offset of the lane's chunk of K stage 0 from the operand's
+  // base (the host checked that it fits 32 bits); rows and columns past the end
+  // are clamped.
+  const uint16_t* xb = static_cast<const uint16_t*>(a.x);
+  if (a.gather == nullptr) xb += (size_t)t.row0 * K;
+  const uint16_t* wb = static_cast<const uint16_t*>(a.w) + (size_t)t.e * (GT ? 2 : 1) * N * K;
+  const int lrow = lane >> 3;
+  uint32_t ov[A_INST + B_INST];
+#pragma unroll
+  for (int q = 0; q < A_INST; ++q) {
+    const int r = (wave * A_INST + q) * RPI + lrow;
+    const int c = (lane & 7) ^ ((r >> 1) & 7);
+    const int p = min(r, M - 1);
+    const size_t row = a.gather == nullptr ? (size_t)p : x_row(a, t.row0 + p);
+    ov[q] = (uint32_t)((row * K + c * 8) * 2);
+  }
+#pragma unroll
+  for (int q = 0; q < B_INST; ++q) {
+    const int r = (wave * B_INST + q) * RPI + lrow;
+    const int c = (lane & 7) ^ ((r >> 1) & 7);
+    ov[A_INST + q] = (uint32_t)((tile_weight_row<GT>(r, n0, N) * K + c * 8) * 2);
+  }
+  const int KT0 = K / BK;
+  const int kbase = t.ks * KT0 / t.spl;
+  const int KT = (t.ks + 1) * KT0 / t.spl - kbase;
+  const int last = KT - 1;
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) uint8_t*)smem);
+  const uint8_t* A8 = reinterpret_cast<const uint8_t*>(xb);
+  const uint8_t* B8 = reinterpret_cast<const uint8_t*>(wb);
+  auto a_buf = [&](int kt) { return smem + (kt & 1) * A_STAGE; };
+  auto b_buf = [&](int slot) { return smem + 2 * A_STAGE + slot * B_STAGE; };
+  // copy q of stage kt (q < 8: rows into row buffer kt & 1; else weights into
+  // weight buffer bslot)
+  auto copy = [&](int kt, int bslot, int q) {
+    const size_t kb = (size_t)(kbase + kt) * (BK * 2);
+    const uint32_t m0 =
+        q < A_INST ? lds0 + (uint32_t)((kt & 1) * A_STAGE + (wv * A_INST + q) * RPI * ROWB)
+                   : lds0 + (uint32_t)(2 * A_STAGE + bslot * B_STAGE +
+                                       (wv * B_INST + q - A_INST) * RPI * ROWB);
+    const uint8_t* base = (q < A_INST ? A8 : B8) + kb;
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(ov[q]), "s"(base), "s"(m0)
+                 : "memory");
+  };
+
+  f32x16_t acc[SM][SN];  // [row sub-tile][weight sub-tile]
+#pragma unroll
+  for (int i = 0; i < SM; ++i)
+#pragma unroll
+    for (int j = 0; j < SN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+  // Every fragment row of this lane is lane % 32 of a 32-row sub-tile: one LDS
+  // offset per operand, the sub-tiles 32 rows apart (a constant of the read).
+  const int fa0 = (wm * 128 + (lane & 31)) * ROWB;
+  const int fb0 = (wn * 128 + (lane & 31)) * ROWB;
+  const int sw = (lane >> 1) & 7;
+  const int khalf = lane >> 5;
+  // row sub-tiles of this wave that hold data: all of them except in a segment's
+  // last, partial row tile (a wave-uniform count)
+  const int nsub = __builtin_amdgcn_readfirstlane(min(SM, max(0, (M - wm * 128 + 31) / 32)));
+
+  u32x4_t ca[SM], cb[SN], na[SM], nb[SN];
+  // fragment read r of k slice ks (0..7: b0, a0, b1, b2, b3, a1, a2, a3, the
+  // order of first use)
+  auto read_r = [&](const uint8_t* sa, const uint8_t* sb, int ks, int r, u32x4_t (&fa_)[SM],
+                    u32x4_t (&fb_)[SN]) {
+    const int off = ((ks * 2 + khalf) ^ sw) << 4;
+    if (r == 0) fb_[0] = ld16(sb + fb0 + off);
+    else if (r == 1) fa_[0] = ld16(sa + fa0 + off);
+    else if (r <= 4) fb_[r - 1] = ld16(sb + fb0 + (r - 1) * 32 * ROWB + off);
+    else fa_[r - 4] = ld16(sa + fa0 + (r - 4) * 32 * ROWB + off);
+  };
+  // NS: row sub-tiles with data, a compile-time count, so that a partial tile's
+  // loop has no branch between its MFMAs (its empty sub-tiles are skipped)
+  auto main_loop = [&](auto ns_tag) {
+    constexpr int NS = decltype(ns_tag)::value;
+    // one k slice: 16 MFMAs on (fa_, fb_); after each of the first 8 a read of
+    // slice rks of the buffers (rsa, rsb) into (ra_, rb_); copies q0 .. q1-1
+    // spread evenly over the 16 (rows of stage akt for q < 8, weights of stage
+    // bkt into slot bslot for q >= 8)
+    auto slice = [&](const u32x4_t (&fa_)[SM], const u32x4_t (&fb_)[SN], const uint8_t* rsa,
+                     const uint8_t* rsb, int rks, u32x4_t (&ra_)[SM], u32x4_t (&rb_)[SN],
+                     auto q0c, auto q1c, int akt, int bkt, int bslot) {
+      constexpr int q0 = decltype(q0c)::value, nq = decltype(q1c)::value - q0;
+      static_for<16>([&](auto mc) {
+        constexpr int m = decltype(mc)::value, i = m >> 2, j = m & 3;
+        if constexpr (i < NS)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(fb_[j]), as_bf16x8(fa_[i]),
+                                                              acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (m < 8) {
+          read_r(rsa, rsb, rks, m, ra_, rb_);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (nq > 0 && (m * nq) / 16 != ((m + 1) * nq) / 16) {
+          constexpr int q = q0 + (m * nq) / 16;
+          copy(q < A_INST ? akt : bkt, bslot, q);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      });
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I8 = std::integral_constant<int, 8>;
+    using I11 = std::integral_constant<int, 11>;
+    using I14 = std::integral_constant<int, 14>;
+    using I16 = std::integral_constant<int, 16>;
+    // prologue: stages 0 and 1 and the weights of stage 2 in flight, in the order
+    // the waits count them; stage 0 landed everywhere
+    static_for<A_INST + B_INST>([&](auto q) { copy(0, 0, decltype(q)::value); });
+    static_for<A_INST + B_INST>([&](auto q) { copy(min(1, last), 1, decltype(q)::value); });
+    static_for<B_INST>([&](auto q) { copy(min(2, last), 2, A_INST + decltype(q)::value); });
+    wait_vmcnt<A_INST + 2 * B_INST>();
+    lds_barrier();
+    static_for<8>([&](auto r) { read_r(a_buf(0), b_buf(0), 0, decltype(r)::value, ca, cb); });
+    // One code path for every stage: past the end the copies fetch the last stage
+    // again into buffers nobody reads any more and the reads fetch a stale buffer
+    // (both in bounds); the copies are drained before the epilogue reuses the LDS.
+    int bs = 0;  // weight slot of stage kt (kt mod 3)
+    for (int kt = 0; kt < KT; ++kt) {
+      const int bs1 = bs == 2 ? 0 : bs + 1;
+      const int bsp = bs == 0 ? 2 : bs - 1;  // slot of stage kt-1 = stage kt+2
+      const int k2 = min(kt + 2, last);
+      const uint8_t* sa = a_buf(kt);
+      const uint8_t* sb = b_buf(bs);
+      slice(ca, cb, sa, sb, 1, na, nb, I8{}, I11{}, 0, k2, bsp);
+      slice(na, nb, sa, sb, 2, ca, cb, I11{}, I14{}, 0, k2, bsp);
+      slice(ca, cb, sa, sb, 3, na, nb, I14{}, I16{}, 0, k2, bsp);
+      // stage kt+1 landed for this wave (only the weights of stage kt+2 issued
+      // above may still be in flight), then for everyone; stage kt fully read, so
+      // row buffer kt & 1 is free
+      wait_vmcnt<B_INST>();
+      lds_barrier();
+      slice(na, nb, a_buf(kt + 1), b_buf(bs1), 0, ca, cb, I0{}, I8{}, k2, 0, 0);
+      bs = bs1;
+    }
+    wait_vmcnt<0>();
+    // every accumulator leaves each variant in its accumulation registers, so the
+    // variants meet the epilogue with one register assignment
+#pragma unroll
+    for (int i = 0; i < SM; ++i)
+#pragma unroll
+      for (int j = 0; j < SN; ++j) asm volatile("" : "+a"(acc[i][j]));
+  };
+  switch (nsub) {
+    case 4: main_loop(std::integral_constant<int, 4>{}); break;
+    case 3: main_loop(std::integral_constant<int, 3>{}); break;
+    case 2: main_loop(std::integral_constant<int, 2>{}); break;
+    case 1: main_loop(std::integral_constant<int, 1>{}); break;
+    default: main_loop(std::integral_constant<int, 0>{}); break;
+  }
+
+  // 32x32 D layout: lane holds row lane % 32 of x (column of D) and the weight
+  // rows (v / 4) * 8 + (lane / 32) * 4 + v % 4 of each sub-tile.
+  if (t.unit0 >= 0) {
+    // one K slice of a split tile: 16 bytes per lane in accumulator order; the
+    // reduce launch sums the slices and runs the epilogue
+    float* P = a.part + (size_t)(t.unit0 + t.ks) * BM * BN + wave * (BM * BN / 4) + lane * 4;
+#pragma unroll
+    for (int i = 0; i < SM; ++i)
+#pragma unroll
+      for (int j = 0; j < SN; ++j) {
+        asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<f32x4_t*>(P + ((i * SN + j) * 4 + q) * 256) =
+              f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+      }
+    return;
+  }
+  // Finished columns go to a [256 x BC] bf16 tile in LDS (the stages are free),
+  // then whole rows to memory, 16 bytes a lane. The 16-byte chunks of a row are
+  // XOR-swizzled by its low 4 bits, so the rows of a write spread over the banks.
+  constexpr int CROWB = BC * 2;
+  const uint16_t* bias = static_cast<const uint16_t*>(a.bias);
+  const uint16_t* res = static_cast<const uint16_t*>(a.res);
+  const int lr = wm * 128 + (lane & 31);            // first row of this lane in the tile
+  const int lc = wn * (BC / 2) + khalf * 4;         // first column
+  constexpr int STEPS = (GT ? SN / 2 : SN) * 4;     // (weight sub-tile, 4-column run) pairs
+  // the bias of every run up front (a branch in every step would have the
+  // compiler spill accumulators)
+  uint2 bgs[STEPS], bus[GT ? STEPS : 1];
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    bgs[s] = make_uint2(0u, 0u);
+    if constexpr (GT) bus[s] = make_uint2(0u, 0u);
+  }
+  if (bias != nullptr) {
+    bias += (size_t)t.e * (GT ? 2 : 1) * N + n0;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int cc = min(lc + (s >> 2) * 32 + (s & 3) * 8, nvalid - 4);
+      bgs[s] = *reinterpret_cast<const uint2*>(bias + cc);
+      if constexpr (GT) bus[s] = *reinterpret_cast<const uint2*>(bias + N + cc);
+    }
+  }
+  if constexpr (RES) res += (size_t)t.row0 * N + n0;
+  lds_barrier();  // every wave has read the last stage
+  static_for<STEPS>([&](auto sc) {
+    constexpr int s = decltype(sc)::value, j = s >> 2, q = s & 3;
+    const int col = lc + j * 32 + q * 8;
+    const Out4 bg = widen4(bgs[s]), bu = widen4(bus[GT ? s : 0]);
+    Out4 rv[SM] = {};
+    if constexpr (RES) {
+#pragma unroll
+      for (int i = 0; i < SM; ++i)
+        rv[i] = widen4(*reinterpret_cast<const uint2*>(res + (size_t)min(lr + i * 32, M - 1) * N +
+                                                       min(col, nvalid - 4)));
+    }
+#pragma unroll
+    for (int i = 0; i < SM; ++i) {
+      // pinned to the accumulation registers up to here: without this the compiler
+      // reads all of them out before the first branch of the epilogue, and spills
+      asm volatile("" : "+a"(acc[i][j]));
+      if constexpr (GT) asm volatile("" : "+a"(acc[i][j + 2]));
+      const f32x16_t& g = acc[i][j];
+      const f32x16_t& u = acc[i][GT ? j + 2 : j];
+      const uint2 o = finish4<ACT>(f32x4_t{g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]},
+                                   f32x4_t{u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]},
+                                   bg, bu, RES, rv[i]);
+      const int row = lr + i * 32;
+      *reinterpret_cast<uint2*>(smem + row * CROWB + (((col >> 3) ^ (row & 15)) << 4) + khalf * 8) = o;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  });
+  lds_barrier();
+  constexpr int LPR = CROWB / 16, RPW = 64 / LPR;   // lanes per row, rows per store
+  uint16_t* y = static_cast<uint16_t*>(a.y) + (size_t)t.row0 * N + n0;
+  const int cl = lane % LPR;
+  const bool cok = cl * 8 < nvalid;  // N % 64 == 0: 8-column chunks are all or nothing
+#pragma unroll 4
+  for (int it = 0; it < BM / NW / RPW; ++it) {
+    const int row = wave * (BM / NW) + it * RPW + lane / LPR;
+    const u32x4_t v = ld16(smem + row * CROWB + ((cl ^ (row & 15)) << 4));
+    if (cok && row < M) st16(y + (size_t)row * N + cl * 8, v);
+  }
+}
+
+// Sums the K slices of each split tile in slice order and runs the epilogue.
+// kReduceParts workgroups share a tile (one wave's row sub-tiles are spread over
+// them), so the partials stream through many CUs.
+constexpr int kReduceParts = 8;
+
+template <int ACT>
+__global__ __launch_bounds__(kThreads) void lin_reduce_kernel(LinArgs a) {
+  constexpr bool GT = ACT == kActGeglu || ACT == kActSwiglu;
+  __shared__ plan::Tables L;
+  plan::Tile t;
+  if (!tile_of(a, GT, blockIdx.x / kReduceParts, true, L, t)) return;
+  const int N = a.N;
+  const int n0 = GT ? t.n0 / 2 : t.n0;
+  const int nvalid = N - n0;
+  const uint16_t* bias = static_cast<const uint16_t*>(a.bias);
+  const uint16_t* res = static_cast<const uint16_t*>(a.res);
+  const bool has_bias = bias != nullptr, has_res = res != nullptr;
+  if (has_bias) bias += (size_t)t.e * (GT ? 2 : 1) * N + n0;
+  const float* P = a.part + (size_t)t.unit0 * BM * BN;
+  const int spl = t.spl;
+  constexpr int JS = GT ? 2 : 4;  // weight sub-tiles that give outputs
+  constexpr int RUNS = 4 * 4 * JS * 4 * 64;  // runs of 4 columns in a tile
+  for (int e = (blockIdx.x % kReduceParts) * kThreads + threadIdx.x; e < RUNS;
+       e += kReduceParts * kThreads) {
+    // e = (((wave * 4 + i) * JS + j) * 4 + q) * 64 + lane, the partials' order
+    const int lane = e & 63, q = (e >> 6) & 3, j = (e >> 8) % JS, wi = (e >> 8) / JS;
+    const int wave = wi >> 2, i = wi & 3;
+    const int row = (wave >> 1) * 128 + i * 32 + (lane & 31);
+    const int col = (wave & 1) * (GT ? 64 : 128) + j * 32 + q * 8 + (lane >> 5) * 4;
+    if (row >= t.M || col >= nvalid) continue;
+    const float* src = P + (size_t)wave * (BM * BN / 4) + lane * 4;
+    f32x4_t g{}, u{};
+    f32x4_t vg[plan::kMaxSplit], vu[plan::kMaxSplit];
+#pragma unroll
+    for (int ks = 0; ks < plan::kMaxSplit; ++ks) {  // all loads first, from clamped slices
+      const float* sl = src + (size_t)min(ks, spl - 1) * BM * BN;
+      vg[ks] = *reinterpret_cast<const f32x4_t*>(sl + ((i * 4 + j) * 4 + q) * 256);
+      if constexpr (GT) vu[ks] = *reinterpret_cast<const f32x4_t*>(sl + ((i * 4 + j + 2) * 4 + q) * 256);
+    }
+#pragma unroll
+    for (int ks = 0; ks < plan::kMaxSplit; ++ks)
+      if (ks < spl) {
+        g += vg[ks];
+        if constexpr (GT) u += vu[ks];
+      }
+    Out4 bg{}, bu{}, rv{};
+    if (has_bias) {
+      bg = widen4(*reinterpret_cast<const uint2*>(bias + col));
+      if constexpr (GT) bu = widen4(*reinterpret_cast<const uint2*>(bias + N + col));
+    }
+    const size_t at = (size_t)(t.row0 + row) * N + n0 + col;
+    if (has_res) rv = widen4(*reinterpret_cast<const uint2*>(res + at));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
+        finish4<ACT>(g, u, bg, bu, has_res, rv);
+  }
+}
+
+// Split flag, workgroups and workspace layout (partial tiles | table) of a launch.
+struct BigLayout {
+  bool split;
+  int slots;
+  size_t part, table, bytes;
+};
+
+BigLayout big_layout(const LinArgs& a) {
+  LinArgs b = a;
+  b.part = nullptr;
+  b.slots = 0;
+  plan::Shape sh = shape_of(b, a.act == kActGeglu || a.act == kActSwiglu);
+  BigLayout L{};
+  sh.split = L.split = plan::split_ok(sh);
+  L.slots = plan::launch_slots<BM, BN>(sh);
+  L.table = L.split ? kPartTiles * BM * BN * sizeof(float) : 0;
+  L.bytes = L.table + (a.offsets ? (size_t)(L.slots + plan::kReduceSlots) * kTableInt4 * sizeof(int4) : 0);
+  return L;
+}
+
+template <int ACT>
+hipError_t run_big(const LinArgs& a, hipStream_t s) {
+  if (a.res != nullptr)
+    hipLaunchKernelGGL((lin_big_kernel<ACT, true>), dim3(a.slots), dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((lin_big_kernel<ACT, false>), dim3(a.slots), dim3(kThreads), 0, s, a);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || a.part == nullptr) return err;
+  hipLaunchKernelGGL((lin_reduce_kernel<ACT>), dim3(plan::kReduceSlots * kReduceParts),
+                     dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+namespace lin {
+
+// The kernel's 32-bit byte offsets: the gathered rows from x, 256 buffer rows,
+// and an expert's weights from the tile's base.
+bool big_ok(const LinArgs& a) {
+  const size_t lim = size_t(1) << 32, row = (size_t)a.K * 2;
+  const bool gt = a.act == kActGeglu || a.act == kActSwiglu;
+  const size_t x = (size_t)(a.gather ? a.gT : BM) * row;
+  return x < lim && (size_t)(gt ? 2 : 1) * a.N * row < lim;
+}
+
+size_t big_ws_bytes(const LinArgs& a) { return big_layout(a).bytes; }
+
+hipError_t launch_big(LinArgs a, void* ws, hipStream_t s) {
+  const BigLayout L = big_layout(a);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  a.part = L.split ? reinterpret_cast<float*>(base) : nullptr;
+  a.slots = L.slots;
+  if (a.offsets) {
+    a.table = reinterpret_cast<const int4*>(base + L.table);
+    const int n = L.slots + plan::kReduceSlots;
+    hipLaunchKernelGGL(lin_plan_kernel, dim3((n + kThreads - 1) / kThreads), dim3(kThreads), 0, s, a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  switch (a.act) {
+    case kActNone: return run_big<kActNone>(a, s);
+    case kActGelu: return run_big<kActGelu>(a, s);
+    case kActSilu: return run_big<kActSilu>(a, s);
+    case kActGeglu: return run_big<kActGeglu>(a, s);
+    default: return run_big<kActSwiglu>(a, s);
+  }
+}
+
+}  // namespace lin
+}  // namespace moe

@@ -610,6 +610,13 @@ def _other_stream(device, stream):
     return None if stream == torch.cuda.current_stream() else stream
 
 
+# Handle of a device's current stream. The public torch.cuda.current_stream() builds
+# a Stream object for it, 2.8 us of a call that takes 7; torch's own generated code
+# takes this one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def moe_norm(x, weight=None, bias=None, eps: float = 1e-6, kind: str = "rms", out=None,
              stream=None):
     """Norm of every row of x [T,H]: "rms" or "layer", times weight, plus bias.
@@ -629,7 +636,7 @@ def moe_norm(x, weight=None, bias=None, eps: float = 1e-6, kind: str = "rms", ou
         out = torch.empty_like(x)
         op = out.data_ptr()
     _check("moe_norm", lib().moe_norm(xp, wp, bp, T, H, eps, code, dt, op,
-                                      torch.cuda.current_stream().cuda_stream))
+                                      _raw_stream(dev.index)))
     return out
 
 
@@ -678,7 +685,7 @@ def moe_norm_residual(y, res, weight=None, bias=None, gate=None, scale: float = 
         next_out = torch.empty_like(y)
         np_ = next_out.data_ptr()
     _check("moe_norm_residual", lib().moe_norm_residual(
-        *args, T, H, eps, dt, rp, np_, torch.cuda.current_stream().cuda_stream))
+        *args, T, H, eps, dt, rp, np_, _raw_stream(dev.index)))
     return res_out, next_out
 
 
@@ -716,7 +723,7 @@ def moe_route_grouped(x, wg, bias, k: int, score: str = "sigmoid", groups: int =
         op = topk_w.data_ptr()
     _check("moe_route_grouped", L.moe_route_grouped(
         xp, wp, bp, T, H, E, k, code, groups, topk_groups, group_top, int(renorm), scale, dt, ip, op,
-        wsp, wsn, torch.cuda.current_stream().cuda_stream))
+        wsp, wsn, _raw_stream(dev.index)))
     return topk_idx, topk_w
 
 
@@ -750,7 +757,7 @@ def moe_linear(x, w, bias=None, act: str = "none", residual=None, y=None, ws=Non
         y = torch.empty((M, N), dtype=dtype, device=dev)
         yp = y.data_ptr()
     _check("moe_linear", L.moe_linear(xp, wp, bp, code, rp, M, N, K, dt, yp, wsp, wsn,
-                                      torch.cuda.current_stream().cuda_stream))
+                                      _raw_stream(dev.index)))
     return y
 
 
@@ -800,7 +807,7 @@ def moe_linear_grouped(x, offsets, w, bias=None, act: str = "none", residual=Non
         yp = y.data_ptr()
     _check("moe_linear_grouped", L.moe_linear_grouped(
         xp, pp, k, T, fp, E, rows, wp, bp, code, rp, N, K, dt, yp, wsp, wsn,
-        torch.cuda.current_stream().cuda_stream))
+        _raw_stream(dev.index)))
     return y
 
 

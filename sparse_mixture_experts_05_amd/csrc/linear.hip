@@ -25,195 +25,379 @@ using namespace lin;
 
 constexpr int kThreads = 256;
 
-// Weight row of row r of a tile of interleaved gate and up rows whose first
-// output column is n0: rows 4q, 4q+1 are the gate rows of columns n0 + 2q,
-// n0 + 2q + 1 and rows 4q+2, 4q+3 their up rows, so the 4 consecutive rows a
-// lane accumulates hold both factors of 2 outputs.
-__device__ __forceinline__ int gated_row(int r, int n0, int N) {
-  return ((r >> 1) & 1) * N + n0 + (r >> 2) * 2 + (r & 1);
-}
-
 struct LinTile {
   int e, row0, M, n0;  // expert; first buffer row and rows of the tile; first output column
+  int q;               // number of the tile
 };
 
-// The tile of this workgroup: row tiles of BM rows, segment by segment, each
-// with its column tiles of BNC output columns. False: no work.
-template <int BM, int BNC>
-__device__ bool lin_tile(const LinArgs& a, LinTile& t) {
-  const int ntn = (a.N + BNC - 1) / BNC;
-  const int mt = blockIdx.x / ntn;
-  t.n0 = (blockIdx.x % ntn) * BNC;
-  if (a.offsets == nullptr) {
-    t.e = 0;
-    t.row0 = mt * BM;
-    t.M = min(BM, a.M - t.row0);
-    return t.M > 0;
-  }
-  __shared__ int pre[256];
-  __shared__ int sel[3];
-  const int tid = threadIdx.x;
-  int off = 0, cnt = 0, tiles = 0;
-  if (tid < a.E) {
-    // clamped: a segment never leaves the buffer, whatever the offsets hold
-    off = min(max(a.offsets[tid], 0), a.M);
-    cnt = min(max(a.offsets[tid + 1], off), a.M) - off;
-    tiles = (cnt + BM - 1) / BM;
-  }
-  pre[tid] = tiles;
-  if (tid == 0) sel[0] = -1;
-  __syncthreads();
-  for (int d = 1; d < 256; d <<= 1) {
-    const int v = tid >= d ? pre[tid - d] : 0;
-    __syncthreads();
-    pre[tid] += v;
-    __syncthreads();
-  }
-  if (tid < a.E) {
-    const int excl = pre[tid] - tiles;
-    if (mt >= excl && mt < pre[tid]) {
-      sel[0] = tid;
-      sel[1] = off + (mt - excl) * BM;
-      sel[2] = min(BM, cnt - (mt - excl) * BM);
+// Row tile `mt` of BM rows of the segments: each wave finds it for itself (no
+// barrier): lane l sums the row tiles of experts 4 l .. 4 l + 3, a wave scan
+// orders the lanes. Segments are clamped into the buffer, whatever the offsets
+// hold. total: all row tiles.
+struct SegScan {
+  int off[4], cnt[4], nb[4];
+  int incl, total;
+};
+template <int BM>
+__device__ __forceinline__ void scan_segments(const LinArgs& a, SegScan& s) {
+  const int lane = threadIdx.x & 63;
+  int sum = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = lane * 4 + j;
+    s.off[j] = s.cnt[j] = 0;
+    if (e < a.E) {
+      s.off[j] = min(max(a.offsets[e], 0), a.M);
+      s.cnt[j] = min(max(a.offsets[e + 1], s.off[j]), a.M) - s.off[j];
     }
+    s.nb[j] = (s.cnt[j] + BM - 1) / BM;
+    sum += s.nb[j];
   }
-  __syncthreads();
-  t.e = sel[0];
-  t.row0 = sel[1];
-  t.M = sel[2];
-  return t.e >= 0;
+  s.incl = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(s.incl, d);
+    if (lane >= d) s.incl += v;
+  }
+  s.total = __shfl(s.incl, 63);
 }
 
-// Epilogue of 4 accumulators of one row: 4 outputs from column c, or the
-// gate and up halves of 2 outputs from column c (gated). bias: the expert's.
-__device__ __forceinline__ void store4_bf16(const LinArgs& a, const uint16_t* bias, size_t row,
-                                            int c, const f32x4_t& acc) {
-  uint16_t* y = static_cast<uint16_t*>(a.y) + row * a.N + c;
-  const uint16_t* res = static_cast<const uint16_t*>(a.res);
-  if (res != nullptr) res += row * a.N + c;
-  if (gated(a.act)) {
-    float o[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float g = acc[j], u = acc[2 + j];
-      if (bias != nullptr) {
-        g += bf16_to_f32(bias[c + j]);
-        u += bf16_to_f32(bias[a.N + c + j]);
-      }
-      o[j] = activate<true>(a.act, g) * u;
-      if (res != nullptr) o[j] += bf16_to_f32(res[j]);
-    }
-    *reinterpret_cast<uint32_t*>(y) = cvt_bf16x2(o[0], o[1]);
-  } else {
-    float o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float g = acc[j];
-      if (bias != nullptr) g += bf16_to_f32(bias[c + j]);
-      o[j] = activate<true>(a.act, g);
-      if (res != nullptr) o[j] += bf16_to_f32(res[j]);
-    }
-    *reinterpret_cast<uint2*>(y) = make_uint2(cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3]));
+// The tile of this workgroup, BM rows x bnc output columns. Tiles are numbered
+// segment by segment, column tile by column tile, row tile by row tile, and XCD
+// x (workgroups x, x + 8, ...) takes a contiguous run of them: the tiles that
+// share a weight panel run on one XCD at about one time. False: no work.
+template <int BM>
+__device__ __forceinline__ bool lin_tile(const LinArgs& a, int bnc, LinTile& t) {
+  const int ntn = (a.N + bnc - 1) / bnc;
+  const int g = blockIdx.x;
+  if (a.offsets == nullptr) {
+    const int nm = (a.M + BM - 1) / BM;
+    const long long total = (long long)nm * ntn;
+    const int chunk = (int)((total + 7) / 8);
+    const long long q = (long long)(g & 7) * chunk + (g >> 3);
+    if ((g >> 3) >= chunk || q >= total) return false;
+    t.e = 0;
+    t.q = (int)q;
+    t.row0 = t.q % nm * BM;
+    t.n0 = t.q / nm * bnc;
+    t.M = min(BM, a.M - t.row0);
+    return true;
   }
+  SegScan s;
+  scan_segments<BM>(a, s);
+  const long long total = (long long)s.total * ntn;
+  const int chunk = (int)((total + 7) / 8);
+  const long long q = (long long)(g & 7) * chunk + (g >> 3);
+  if ((g >> 3) >= chunk || q >= total) return false;
+  const int lane = threadIdx.x & 63;
+  int excl = s.incl;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) excl -= s.nb[j];
+  const bool mine = q >= (long long)excl * ntn && q < (long long)s.incl * ntn;
+  const int src = __ffsll((unsigned long long)__ballot(mine)) - 1;
+  int e = 0, off = 0, cnt = 0, nb = 1, base = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (mine && q >= (long long)excl * ntn && q < (long long)(excl + s.nb[j]) * ntn)
+      e = lane * 4 + j, off = s.off[j], cnt = s.cnt[j], nb = s.nb[j], base = excl;
+    excl += s.nb[j];
+  }
+  e = __shfl(e, src), off = __shfl(off, src), cnt = __shfl(cnt, src);
+  nb = __shfl(nb, src), base = __shfl(base, src);
+  const int local = (int)(q - (long long)base * ntn);
+  const int m = local % nb;
+  t.e = e;
+  t.q = (int)q;
+  t.row0 = off + m * BM;
+  t.M = min(BM, cnt - m * BM);
+  t.n0 = local / nb * bnc;
+  return true;
 }
 
 // ----------------------------------------------------------------- bf16 tiles
 
-// BM rows x 64 weight rows (64 output columns, or 32 of a gated product), 4
-// waves, wave w the weight rows [16 w, 16 w + 16) for all BM rows. Operand
-// rows are copied global -> LDS with global_load_lds (8 rows of 128 bytes an
-// instruction) into a ring of 3 stages of 64 k; 16-byte chunk c of row r sits
-// at slot c ^ ((r >> 1) & 7), so the 16 lanes of a fragment read (16
-// consecutive rows, one chunk) touch 16 distinct 4-bank groups.
-// v_mfma_f32_16x16x32_bf16 takes the weights as A and the rows as B: lane l
-// ends with 4 consecutive weight rows of row l % 16 of x.
-template <int BM>
-struct LinTileShape {
-  static constexpr int BN = 64, NS = 3;
+// Tiles of BM rows x BN weight rows (BN output columns, or BN / 2 of a gated
+// product) by 4 waves in a 2 x 2 grid. Operand rows are copied global -> LDS with
+// global_load_lds (8 rows of 128 bytes an instruction) into a ring of NS stages
+// of 64 k; 16-byte chunk c of row r sits at slot c ^ ((r >> 1) & 7), so the 16
+// lanes of a fragment read (16 consecutive rows, one chunk) touch 16 distinct
+// 4-bank groups. v_mfma_f32_16x16x32_bf16 takes the weights as A and the rows as
+// B: lane l ends with 4 consecutive weight rows of row l % 16 of x. In a gated
+// product the first half of a wave's weight sub-tiles holds gate rows, the second
+// the up rows of the same columns.
+//
+// blockIdx.y of gridDim.y: a K slice. With several, a slice writes its
+// accumulators to a.part and lin_tile_reduce_kernel finishes the tile.
+template <int BM_, int BN_, int NS_>
+struct TileShape {
+  static constexpr int BM = BM_, BN = BN_, NS = NS_;
+  static constexpr int TM = BM / 2 / 16, TN = BN / 2 / 16;  // sub-tiles of a wave
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int NI = (BM + BN) / 8 / 4;  // copies per wave per stage
-  static_assert((BM + BN) % 32 == 0, "whole copies");
+  static_assert((BM + BN) % 32 == 0 && TN % 2 == 0, "whole copies, whole halves");
 };
 
-template <int BM>
-__global__ __launch_bounds__(kThreads) void lin_bf16_kernel(LinArgs a) {
-  using Sh = LinTileShape<BM>;
-  constexpr int BN = Sh::BN, NS = Sh::NS, STAGE = Sh::STAGE, NI = Sh::NI, SM = BM / 16;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[NS * STAGE];
+template <typename Sh>
+__device__ __forceinline__ int tile_col(int wn, int j, bool gt) {  // first column of a sub-tile
+  constexpr int W = Sh::BN / 2;
+  return gt ? wn * (W / 2) + j * 16 : wn * W + j * 16;
+}
+
+// Epilogue of a wave's accumulators, straight to memory.
+template <typename Sh>
+__device__ __forceinline__ void tile_store(const LinArgs& a, const LinTile& t,
+                                           const f32x4_t (&acc)[Sh::TM][Sh::TN]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
   const bool gt = gated(a.act);
+#pragma unroll
+  for (int i = 0; i < Sh::TM; ++i) {
+    const int r = wm * (Sh::BM / 2) + i * 16 + (lane & 15);
+    if (r >= t.M) continue;
+#pragma unroll
+    for (int j = 0; j < Sh::TN; ++j) {
+      if (gt && j >= Sh::TN / 2) continue;
+      const int c = t.n0 + tile_col<Sh>(wn, j, gt) + (lane >> 4) * 4;
+      if (c < a.N) store4(a, t.e, (size_t)(t.row0 + r), c, acc[i][j], acc[i][(j + Sh::TN / 2) % Sh::TN]);
+    }
+  }
+}
+
+// Accumulator (i, j) of this thread in slice ks of a tile's partials.
+template <typename Sh>
+__device__ __forceinline__ float* tile_part(const LinArgs& a, const LinTile& t, int ks, int nks,
+                                            int i, int j) {
+  return a.part + ((size_t)t.q * nks + ks) * Sh::BM * Sh::BN +
+         ((size_t)(i * Sh::TN + j) * kThreads + threadIdx.x) * 4;
+}
+
+template <typename Sh>
+__device__ __forceinline__ bool find(const LinArgs& a, LinTile& t) {
+  return lin_tile<Sh::BM>(a, gated(a.act) ? Sh::BN / 2 : Sh::BN, t);
+}
+
+template <typename Sh>
+__global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
+  constexpr int BM = Sh::BM, BN = Sh::BN, NS = Sh::NS, STAGE = Sh::STAGE, NI = Sh::NI;
+  constexpr int TM = Sh::TM, TN = Sh::TN;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[NS * STAGE];
   LinTile t;
-  if (!(gt ? lin_tile<BM, BN / 2>(a, t) : lin_tile<BM, BN>(a, t))) return;
+  if (!find<Sh>(a, t)) return;
+  const bool gt = gated(a.act);
   const int N = a.N, K = a.K;
   const uint16_t* x = static_cast<const uint16_t*>(a.x);
   const uint16_t* w = static_cast<const uint16_t*>(a.w) + (size_t)t.e * (gt ? 2 : 1) * N * K;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int KT0 = K / 64;
+  const int kbase = (int)((long long)blockIdx.y * KT0 / gridDim.y);
+  const int KT = (int)((long long)(blockIdx.y + 1) * KT0 / gridDim.y) - kbase;
 
   const uint16_t* src[NI];
-  int dst[NI];
 #pragma unroll
   for (int q = 0; q < NI; ++q) {
-    const int g = wave * NI + q;
-    const int r = 8 * g + (lane >> 3);
+    const int r = 8 * (wave * NI + q) + (lane >> 3);
     const int chunk = (lane & 7) ^ ((r >> 1) & 7);
     const uint16_t* row;
-    if (r < BM) row = x + x_row(a, t.row0 + min(r, t.M - 1)) * K;  // rows past the end: its last
-    else row = w + (size_t)(gt ? gated_row(r - BM, t.n0, N) : t.n0 + r - BM) * K;
-    src[q] = row + chunk * 8;
-    dst[q] = g * 1024;
+    if (r < BM) {
+      row = x + x_row(a, t.row0 + min(r, t.M - 1)) * K;  // rows past the end: its last
+    } else {
+      const int b = r - BM, j = b / 16 % TN;
+      const int half = gt && j >= TN / 2 ? 1 : 0;
+      const int c = t.n0 + tile_col<Sh>(b / (BN / 2), j - half * (TN / 2), gt) + b % 16;
+      row = w + ((size_t)half * N + min(c, N - 1)) * K;  // columns past the end: its last
+    }
+    src[q] = row + kbase * 64 + chunk * 8;
   }
-  const int KT = K / 64;
   auto issue = [&](int kt) {
     uint8_t* base = smem + (kt % NS) * STAGE;
 #pragma unroll
-    for (int q = 0; q < NI; ++q) lds_dma16(src[q] + kt * 64, base + dst[q]);
+    for (int q = 0; q < NI; ++q) lds_dma16(src[q] + kt * 64, base + (wave * NI + q) * 1024);
   };
-  f32x4_t acc[SM];
+  f32x4_t acc[TM][TN];
 #pragma unroll
-  for (int i = 0; i < SM; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const int fr = (lane & 15) * 128;
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int fx = (wm * (BM / 2) + (lane & 15)) * 128;
+  const int fw = (BM + wn * (BN / 2) + (lane & 15)) * 128;
   const int sw = (lane >> 1) & 7;  // (row >> 1) & 7 of every fragment row of this lane
 
 #pragma unroll
   for (int st = 0; st < NS - 1; ++st)
     if (st < KT) issue(st);
   for (int kt = 0; kt < KT; ++kt) {
+    // stage kt landed: at most the copies of the stages after it are in flight
     if (kt + NS - 2 < KT) wait_vmcnt<(NS - 2) * NI>();
     else wait_vmcnt<0>();
-    lds_barrier();  // stage kt landed for every wave; stage kt-1 is no longer read
+    lds_barrier();  // for every wave; stage kt-1 is no longer read
     if (kt + NS - 1 < KT) issue(kt + NS - 1);
     const uint8_t* cur = smem + (kt % NS) * STAGE;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       const int slot = ((ks * 4 + (lane >> 4)) ^ sw) * 16;
-      const u32x4_t fw = ld16(cur + (BM + wave * 16) * 128 + fr + slot);
+      u32x4_t xf[TM], wf[TN];
 #pragma unroll
-      for (int i = 0; i < SM; ++i) {
-        const u32x4_t fx = ld16(cur + i * 16 * 128 + fr + slot);
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(fw), as_bf16x8(fx), acc[i], 0, 0, 0);
-      }
+      for (int j = 0; j < TN; ++j) wf[j] = ld16(cur + fw + j * 16 * 128 + slot);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) xf[i] = ld16(cur + fx + i * 16 * 128 + slot);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wf[j]), as_bf16x8(xf[i]),
+                                                              acc[i][j], 0, 0, 0);
     }
   }
-  const uint16_t* bias = a.bias == nullptr ? nullptr
-                             : static_cast<const uint16_t*>(a.bias) + (size_t)t.e * (gt ? 2 : 1) * N;
-  const int c = t.n0 + (wave * 16 + (lane >> 4) * 4) / (gt ? 2 : 1);
-#pragma unroll
-  for (int i = 0; i < SM; ++i) {
-    const int r = i * 16 + (lane & 15);
-    if (r < t.M) store4_bf16(a, bias, (size_t)(t.row0 + r), c, acc[i]);
+  if (gridDim.y == 1) {
+    tile_store<Sh>(a, t, acc);
+    return;
   }
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+    if (wm * (BM / 2) + i * 16 < t.M)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        *reinterpret_cast<f32x4_t*>(tile_part<Sh>(a, t, blockIdx.y, gridDim.y, i, j)) = acc[i][j];
+}
+
+// Sums the nks K slices of each tile in slice order, then the epilogue. One
+// workgroup per row sub-tile i of a tile (blockIdx.y), so that a launch with few
+// tiles still has many.
+constexpr int kMaxSlices = 16;
+
+template <typename Sh>
+__global__ __launch_bounds__(kThreads) void lin_tile_reduce_kernel(LinArgs a, int nks) {
+  LinTile t;
+  if (!find<Sh>(a, t)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool gt = gated(a.act);
+  const int i = blockIdx.y;
+  const int r = (wave >> 1) * (Sh::BM / 2) + i * 16 + (lane & 15);
+  f32x4_t acc[Sh::TN];
+  if ((wave >> 1) * (Sh::BM / 2) + i * 16 >= t.M) return;
+#pragma unroll
+  for (int j = 0; j < Sh::TN; ++j) {
+    f32x4_t v[kMaxSlices];
+#pragma unroll
+    for (int s = 0; s < kMaxSlices; ++s)  // all loads first, from clamped slices
+      v[s] = *reinterpret_cast<const f32x4_t*>(tile_part<Sh>(a, t, min(s, nks - 1), nks, i, j));
+    acc[j] = v[0];
+#pragma unroll
+    for (int s = 1; s < kMaxSlices; ++s)
+      if (s < nks) acc[j] += v[s];
+  }
+  if (r >= t.M) return;
+#pragma unroll
+  for (int j = 0; j < Sh::TN; ++j) {
+    if (gt && j >= Sh::TN / 2) continue;
+    const int c = t.n0 + tile_col<Sh>(wave & 1, j, gt) + (lane >> 4) * 4;
+    if (c < a.N) store4(a, t.e, (size_t)(t.row0 + r), c, acc[j], acc[(j + Sh::TN / 2) % Sh::TN]);
+  }
+}
+
+// ----------------------------------------------------------------- bf16, few rows
+
+// Decode: a few rows per segment, so a launch is a stream of the weights. A
+// workgroup takes up to 16 rows of one segment and 16 output columns; its KQ
+// waves share K in 32-deep steps. Weights go from memory straight to registers
+// (no other wave reads them): one 16-byte load per lane per 16 weight rows x 32 k,
+// in chunks of U steps with the next chunk in flight while one is multiplied.
+// v_mfma_f32_16x16x32_bf16 takes the weights as A and the rows as B, lane l
+// loads weight row l % 16 and x row l % 16 at k = 8 (l / 16) of each step. Rows
+// past the block's end read its last row and are not stored. The waves' sums are
+// added in wave order through LDS.
+template <bool GT, int KQ>
+__global__ __launch_bounds__(KQ * 64) void lin_rows_kernel(LinArgs a) {
+  constexpr int U = 4, H = GT ? 2 : 1;
+  __shared__ f32x4_t red[KQ][H][64];
+  LinTile t;
+  if (!lin_tile<16>(a, 16, t)) return;
+  const int N = a.N, K = a.K;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int S = K / 32;
+  const int s0 = wave * S / KQ, s1 = (wave + 1) * S / KQ;
+  const uint16_t* wp[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    wp[h] = static_cast<const uint16_t*>(a.w) +
+            ((size_t)(t.e * H + h) * N + t.n0 + (lane & 15)) * K + (lane >> 4) * 8;
+  const uint16_t* xp = static_cast<const uint16_t*>(a.x) +
+                       x_row(a, t.row0 + min(lane & 15, t.M - 1)) * K + (lane >> 4) * 8;
+  f32x4_t acc[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) acc[h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4_t wa[U][H], xa[U], wb[U][H], xb[U];
+  auto load = [&](u32x4_t (&w)[U][H], u32x4_t (&x)[U], int s) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) w[u][h] = ld16(wp[h] + (size_t)(s + u) * 32);
+      x[u] = ld16(xp + (size_t)(s + u) * 32);
+    }
+  };
+  auto mma = [&](const u32x4_t (&w)[U][H], const u32x4_t (&x)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        acc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w[u][h]), as_bf16x8(x[u]), acc[h], 0, 0, 0);
+  };
+  int s = s0;
+  if (s + U <= s1) {
+    load(wa, xa, s);
+    for (;;) {
+      s += U;
+      const bool more = s + U <= s1;
+      if (more) load(wb, xb, s);
+      mma(wa, xa);
+      if (!more) break;
+      s += U;
+      const bool again = s + U <= s1;
+      if (again) load(wa, xa, s);
+      mma(wb, xb);
+      if (!again) break;
+    }
+  }
+  for (; s < s1; ++s) {
+    const u32x4_t x1 = ld16(xp + (size_t)s * 32);
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      acc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(ld16(wp[h] + (size_t)s * 32)),
+                                                       as_bf16x8(x1), acc[h], 0, 0, 0);
+  }
+  if (wave != 0) {
+#pragma unroll
+    for (int h = 0; h < H; ++h) red[wave][h][lane] = acc[h];
+  }
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int q = 1; q < KQ; ++q)
+#pragma unroll
+    for (int h = 0; h < H; ++h) acc[h] += red[q][h][lane];
+  const int r = lane & 15;
+  if (r < t.M) store4(a, t.e, (size_t)(t.row0 + r), t.n0 + (lane >> 4) * 4, acc[0], acc[H - 1]);
 }
 
 // ----------------------------------------------------------------- fp32
 
-// 64 x 64 tiles of plain FMA (small fp32 layers); the weight rows of a gated
-// product interleaved as in the bf16 tiles.
+// Weight row of row r of a tile of interleaved gate and up rows whose first
+// output column is n0: rows 4q, 4q+1 are the gate rows of columns n0 + 2q,
+// n0 + 2q + 1 and rows 4q+2, 4q+3 their up rows, so the 4 consecutive rows of a
+// thread hold both factors of 2 outputs.
+__device__ __forceinline__ int gated_row(int r, int n0, int N) {
+  return ((r >> 1) & 1) * N + n0 + (r >> 2) * 2 + (r & 1);
+}
+
+// 64 x 64 tiles of plain FMA (small fp32 layers).
 __global__ __launch_bounds__(kThreads) void lin_f32_kernel(LinArgs a) {
   constexpr int BM = 64, BN = 64, BK = 16;
   __shared__ float As[BK][BM + 4];
   __shared__ float Bs[BK][BN + 4];
   const bool gt = gated(a.act);
   LinTile t;
-  if (!(gt ? lin_tile<BM, BN / 2>(a, t) : lin_tile<BM, BN>(a, t))) return;
+  if (!lin_tile<BM>(a, gt ? BN / 2 : BN, t)) return;
   const int N = a.N, K = a.K;
   const float* w = static_cast<const float*>(a.w) + (size_t)t.e * (gt ? 2 : 1) * N * K;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
@@ -268,41 +452,95 @@ __global__ __launch_bounds__(kThreads) void lin_f32_kernel(LinArgs a) {
 
 // ----------------------------------------------------------------- host side
 
-// Workgroups of a launch of BM-row tiles: sum_e ceil(c_e / BM) <= M / BM +
-// #{e : c_e > 0} row tiles, each with all column tiles.
-long long lin_grid(const LinArgs& a, int BM, int bnc) {
+// Tiles of a launch, at most: sum_e ceil(c_e / BM) <= M / BM + #{e : c_e > 0} row
+// tiles, each with all column tiles.
+long long lin_tiles(const LinArgs& a, int BM, int bnc) {
   const long long mt = a.offsets ? (long long)a.M / BM + std::min(a.E, a.M)
                                  : ((long long)a.M + BM - 1) / BM;
   return mt * ((a.N + bnc - 1) / bnc);
 }
-
-}  // namespace
-
-bool linear_fits(int E, int M, int N, int K) {
-  LinArgs a{};
-  a.E = E, a.M = M, a.N = N, a.K = K;
-  a.offsets = reinterpret_cast<const int32_t*>(sizeof(int32_t));  // only tested for null
-  return lin_grid(a, 32, 32) < (1LL << 31);
+unsigned lin_grid(const LinArgs& a, int BM, int bnc) {  // whole rounds of the 8 XCDs
+  return (unsigned)((lin_tiles(a, BM, bnc) + 7) / 8 * 8);
 }
 
-// Whether a launch takes the 256 x 256 tiles.
-static bool use_big(const lin::LinArgs& a, bool grouped) {
-  return a.M >= 64 * a.E && a.M >= 256 && lin::big_ok(a);
+using Tile64 = TileShape<64, 64, 3>;
+using Tile128 = TileShape<128, 128, 2>;
+
+enum LinPath { kRows, kTile64, kTile128, kBig };
+struct LinPlan {
+  LinPath path;
+  int nks;  // K slices of the tile paths; waves of the few-row path
+};
+
+bool host_gated(int act) { return act == kActGeglu || act == kActSwiglu; }
+
+#ifdef LIN_FORCE
+LinPlan lin_plan(const LinArgs& a) {
+  const char* s = getenv("LIN_FORCE");
+  LinPlan p{kTile64, 1};
+  int path = 1, n = 1;
+  sscanf(s, "%d,%d", &path, &n);
+  p.path = (LinPath)path; p.nks = n;
+  return p;
+}
+#else
+LinPlan lin_plan(const LinArgs& a) {
+  if (a.M <= 16 || (a.offsets && a.M <= 2 * a.E)) return LinPlan{kRows, 4};
+  if (a.M >= 64 * a.E && a.M >= 256 && big_ok(a)) return LinPlan{kBig, 1};
+  return LinPlan{kTile64, 1};
+}
+#endif
+
+template <typename Sh>
+size_t tile_ws_bytes(const LinArgs& a, int nks) {
+  if (nks <= 1) return 0;
+  return (size_t)lin_tiles(a, Sh::BM, host_gated(a.act) ? Sh::BN / 2 : Sh::BN) * nks * Sh::BM *
+         Sh::BN * sizeof(float);
 }
 
-static LinArgs lin_args(const void* x, const int32_t* gather, int gk, int gT, const int32_t* offsets,
-                        int E, int M, int N, int K, int act) {
+template <typename Sh>
+hipError_t run_tile(LinArgs a, int nks, void* ws, hipStream_t s) {
+  const unsigned grid = lin_grid(a, Sh::BM, host_gated(a.act) ? Sh::BN / 2 : Sh::BN);
+  a.part = static_cast<float*>(ws);
+  hipLaunchKernelGGL((lin_tile_kernel<Sh>), dim3(grid, nks), dim3(kThreads), 0, s, a);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || nks <= 1) return err;
+  hipLaunchKernelGGL((lin_tile_reduce_kernel<Sh>), dim3(grid, Sh::TM), dim3(kThreads), 0, s, a, nks);
+  return hipGetLastError();
+}
+
+template <bool GT>
+hipError_t run_rows(const LinArgs& a, int kq, hipStream_t s) {
+  const dim3 grid(lin_grid(a, 16, 16));
+  if (kq >= 16) hipLaunchKernelGGL((lin_rows_kernel<GT, 16>), grid, dim3(1024), 0, s, a);
+  else if (kq >= 8) hipLaunchKernelGGL((lin_rows_kernel<GT, 8>), grid, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((lin_rows_kernel<GT, 4>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+LinArgs lin_args(const void* x, const int32_t* gather, int gk, int gT, const int32_t* offsets,
+                 int E, int M, int N, int K, int act) {
   LinArgs a{};
   a.x = x, a.offsets = offsets, a.gather = gather, a.gk = gk, a.gT = gT;
   a.E = E, a.M = M, a.N = N, a.K = K, a.act = act;
   return a;
 }
 
+}  // namespace
+
+bool linear_fits(int E, int M, int N, int K) {
+  const int32_t some = 0;  // only tested for null
+  return lin_tiles(lin_args(nullptr, nullptr, 1, M, &some, E, M, N, K, 0), 16, 16) < (1LL << 31) - 8;
+}
+
 size_t linear_ws_bytes(int E, int M, int N, int K, int act, bool grouped, bool bf16) {
   if (!bf16) return 0;
-  const int32_t some = 0;  // only tested for null
+  const int32_t some = 0;
   const LinArgs a = lin_args(nullptr, nullptr, 1, M, grouped ? &some : nullptr, E, M, N, K, act);
-  return use_big(a, grouped) ? big_ws_bytes(a) : 0;
+  const LinPlan p = lin_plan(a);
+  if (p.path == kBig) return big_ws_bytes(a);
+  if (p.path == kTile128) return tile_ws_bytes<Tile128>(a, p.nks);
+  return p.path == kTile64 ? tile_ws_bytes<Tile64>(a, p.nks) : 0;
 }
 
 hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
@@ -311,14 +549,18 @@ hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
                          hipStream_t s) {
   LinArgs a = lin_args(x, gather, gk, gT, offsets, E, M, N, K, act);
   a.w = w, a.bias = bias, a.res = res, a.y = y;
-  const int bnc = act == kActGeglu || act == kActSwiglu ? 32 : 64;
+  const bool gt = host_gated(act);
   if (!bf16) {
-    hipLaunchKernelGGL(lin_f32_kernel, dim3((unsigned)lin_grid(a, 64, bnc)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL(lin_f32_kernel, dim3(lin_grid(a, 64, gt ? 32 : 64)), dim3(kThreads), 0, s, a);
     return hipGetLastError();
   }
-  if (use_big(a, offsets != nullptr)) return launch_big(a, ws, s);
-  hipLaunchKernelGGL((lin_bf16_kernel<64>), dim3((unsigned)lin_grid(a, 64, bnc)), dim3(kThreads), 0, s, a);
-  return hipGetLastError();
+  const LinPlan p = lin_plan(a);
+  switch (p.path) {
+    case kRows: return gt ? run_rows<true>(a, p.nks, s) : run_rows<false>(a, p.nks, s);
+    case kTile64: return run_tile<Tile64>(a, p.nks, ws, s);
+    case kTile128: return run_tile<Tile128>(a, p.nks, ws, s);
+    default: return launch_big(a, ws, s);
+  }
 }
 
 }  // namespace moe

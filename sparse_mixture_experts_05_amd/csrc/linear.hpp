@@ -45,6 +45,48 @@ __device__ __forceinline__ size_t x_row(const LinArgs& a, int p) {
   return (size_t)((unsigned)min(max(a.gather[p], 0), a.gT * a.gk - 1) / (unsigned)a.gk);
 }
 
+// Output of one lane: 4 consecutive columns of a row (bf16, 8-byte aligned).
+struct Out4 {
+  float v[4];
+};
+__device__ __forceinline__ Out4 widen4(uint2 q) {
+  return Out4{{bf16_to_f32(q.x & 0xffffu), __uint_as_float(q.x & 0xffff0000u),
+               bf16_to_f32(q.y & 0xffffu), __uint_as_float(q.y & 0xffff0000u)}};
+}
+
+// act(g + bg) [* (u + bu)] [+ res] of 4 columns, packed to bf16 (no bias: zeros).
+__device__ __forceinline__ uint2 finish4(int act, const f32x4_t& g, const f32x4_t& u,
+                                         const Out4& bg, const Out4& bu, bool has_res,
+                                         const Out4& res) {
+  float o[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float x = activate<true>(act, g[c] + bg.v[c]);
+    if (gated(act)) x *= u[c] + bu.v[c];
+    if (has_res) x += res.v[c];
+    o[c] = x;
+  }
+  return make_uint2(cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3]));
+}
+
+// Bias and residual of the 4 columns c .. c + 3 of buffer row `row`, then finish4
+// and the store. e: the row's expert.
+__device__ __forceinline__ void store4(const LinArgs& a, int e, size_t row, int c,
+                                       const f32x4_t& g, const f32x4_t& u) {
+  const bool gt = gated(a.act);
+  Out4 bg{}, bu{}, rv{};
+  if (a.bias != nullptr) {
+    const uint16_t* b = static_cast<const uint16_t*>(a.bias) + (size_t)e * (gt ? 2 : 1) * a.N + c;
+    bg = widen4(*reinterpret_cast<const uint2*>(b));
+    if (gt) bu = widen4(*reinterpret_cast<const uint2*>(b + a.N));
+  }
+  const size_t at = row * a.N + c;
+  if (a.res != nullptr)
+    rv = widen4(*reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.res) + at));
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
+      finish4(a.act, g, u, bg, bu, a.res != nullptr, rv);
+}
+
 // Big-tile path (linear_big.hip): 256 x 256 tiles.
 bool big_ok(const LinArgs& a);           // the shape's offsets fit the kernel's addressing
 size_t big_ws_bytes(const LinArgs& a);

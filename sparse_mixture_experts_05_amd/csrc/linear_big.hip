@@ -134,31 +134,6 @@ __device__ __forceinline__ bool tile_of(const LinArgs& a, bool gt, int i, bool r
   return kind == 0;
 }
 
-// Output of one lane: 4 consecutive columns of a row (16-bit, 8-byte aligned).
-struct Out4 {
-  float v[4];
-};
-__device__ __forceinline__ Out4 widen4(uint2 q) {
-  return Out4{{bf16_to_f32(q.x & 0xffffu), __uint_as_float(q.x & 0xffff0000u),
-               bf16_to_f32(q.y & 0xffffu), __uint_as_float(q.y & 0xffff0000u)}};
-}
-
-// act(g + bg) [* (u + bu)] [+ res] of 4 columns, packed to bf16 (no bias: zeros).
-template <int ACT>
-__device__ __forceinline__ uint2 finish4(const f32x4_t& g, const f32x4_t& u, const Out4& bg,
-                                         const Out4& bu, bool has_res, const Out4& res) {
-  constexpr bool GT = ACT == kActGeglu || ACT == kActSwiglu;
-  float o[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    float x = activate<true>(ACT, g[c] + bg.v[c]);
-    if constexpr (GT) x *= u[c] + bu.v[c];
-    if (has_res) x += res.v[c];
-    o[c] = x;
-  }
-  return make_uint2(cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3]));
-}
-
 // Weight row of row r of a tile: the expert's row n0 + r, or for a gated product
 // (n0, N in output columns) wave half r / 128, sub-tile (r / 32) % 4: two of gate
 // rows, then two of up rows, of the same 64 columns.
@@ -415,7 +390,7 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
       if constexpr (GT) asm volatile("" : "+a"(acc[i][j + 2]));
       const f32x16_t& g = acc[i][j];
       const f32x16_t& u = acc[i][GT ? j + 2 : j];
-      const uint2 o = finish4<ACT>(f32x4_t{g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]},
+      const uint2 o = finish4(ACT, f32x4_t{g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]},
                                    f32x4_t{u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]},
                                    bg, bu, RES, rv[i]);
       const int row = lr + i * 32;
@@ -450,10 +425,6 @@ __global__ __launch_bounds__(kThreads) void lin_reduce_kernel(LinArgs a) {
   const int N = a.N;
   const int n0 = GT ? t.n0 / 2 : t.n0;
   const int nvalid = N - n0;
-  const uint16_t* bias = static_cast<const uint16_t*>(a.bias);
-  const uint16_t* res = static_cast<const uint16_t*>(a.res);
-  const bool has_bias = bias != nullptr, has_res = res != nullptr;
-  if (has_bias) bias += (size_t)t.e * (GT ? 2 : 1) * N + n0;
   const float* P = a.part + (size_t)t.unit0 * BM * BN;
   const int spl = t.spl;
   constexpr int JS = GT ? 2 : 4;  // weight sub-tiles that give outputs
@@ -481,15 +452,7 @@ __global__ __launch_bounds__(kThreads) void lin_reduce_kernel(LinArgs a) {
         g += vg[ks];
         if constexpr (GT) u += vu[ks];
       }
-    Out4 bg{}, bu{}, rv{};
-    if (has_bias) {
-      bg = widen4(*reinterpret_cast<const uint2*>(bias + col));
-      if constexpr (GT) bu = widen4(*reinterpret_cast<const uint2*>(bias + N + col));
-    }
-    const size_t at = (size_t)(t.row0 + row) * N + n0 + col;
-    if (has_res) rv = widen4(*reinterpret_cast<const uint2*>(res + at));
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
-        finish4<ACT>(g, u, bg, bu, has_res, rv);
+    store4(a, t.e, (size_t)(t.row0 + row), n0 + col, g, u);
   }
 }
 

@@ -13,6 +13,7 @@
 // accumulator to the store happens in fp32, with one rounding to the output
 // type.
 #include <algorithm>
+#include <cmath>
 
 #include "common.hpp"
 #include "kernels.hpp"
@@ -116,7 +117,7 @@ __device__ __forceinline__ bool lin_tile(const LinArgs& a, int bnc, LinTile& t) 
 
 // ----------------------------------------------------------------- bf16 tiles
 
-// Tiles of BM rows x BN weight rows (BN output columns, or BN / 2 of a gated
+// Tiles of 64 rows x 64 weight rows (64 output columns, or 32 of a gated
 // product) by 4 waves in a 2 x 2 grid. Operand rows are copied global -> LDS with
 // global_load_lds (8 rows of 128 bytes an instruction) into a ring of NS stages
 // of 64 k; 16-byte chunk c of row r sits at slot c ^ ((r >> 1) & 7), so the 16
@@ -128,61 +129,54 @@ __device__ __forceinline__ bool lin_tile(const LinArgs& a, int bnc, LinTile& t) 
 //
 // blockIdx.y of gridDim.y: a K slice. With several, a slice writes its
 // accumulators to a.part and lin_tile_reduce_kernel finishes the tile.
-template <int BM_, int BN_, int NS_>
-struct TileShape {
-  static constexpr int BM = BM_, BN = BN_, NS = NS_;
+struct Tile64 {
+  static constexpr int BM = 64, BN = 64, NS = 3;
   static constexpr int TM = BM / 2 / 16, TN = BN / 2 / 16;  // sub-tiles of a wave
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int NI = (BM + BN) / 8 / 4;  // copies per wave per stage
-  static_assert((BM + BN) % 32 == 0 && TN % 2 == 0, "whole copies, whole halves");
 };
 
-template <typename Sh>
 __device__ __forceinline__ int tile_col(int wn, int j, bool gt) {  // first column of a sub-tile
-  constexpr int W = Sh::BN / 2;
+  constexpr int W = Tile64::BN / 2;
   return gt ? wn * (W / 2) + j * 16 : wn * W + j * 16;
 }
 
 // Epilogue of a wave's accumulators, straight to memory.
-template <typename Sh>
 __device__ __forceinline__ void tile_store(const LinArgs& a, const LinTile& t,
-                                           const f32x4_t (&acc)[Sh::TM][Sh::TN]) {
+                                           const f32x4_t (&acc)[Tile64::TM][Tile64::TN]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 1, wn = wave & 1;
   const bool gt = gated(a.act);
 #pragma unroll
-  for (int i = 0; i < Sh::TM; ++i) {
-    const int r = wm * (Sh::BM / 2) + i * 16 + (lane & 15);
+  for (int i = 0; i < Tile64::TM; ++i) {
+    const int r = wm * (Tile64::BM / 2) + i * 16 + (lane & 15);
     if (r >= t.M) continue;
 #pragma unroll
-    for (int j = 0; j < Sh::TN; ++j) {
-      if (gt && j >= Sh::TN / 2) continue;
-      const int c = t.n0 + tile_col<Sh>(wn, j, gt) + (lane >> 4) * 4;
-      if (c < a.N) store4(a, t.e, (size_t)(t.row0 + r), c, acc[i][j], acc[i][(j + Sh::TN / 2) % Sh::TN]);
+    for (int j = 0; j < Tile64::TN; ++j) {
+      if (gt && j >= Tile64::TN / 2) continue;
+      const int c = t.n0 + tile_col(wn, j, gt) + (lane >> 4) * 4;
+      if (c < a.N) store4(a, t.e, (size_t)(t.row0 + r), c, acc[i][j], acc[i][(j + Tile64::TN / 2) % Tile64::TN]);
     }
   }
 }
 
 // Accumulator (i, j) of this thread in slice ks of a tile's partials.
-template <typename Sh>
 __device__ __forceinline__ float* tile_part(const LinArgs& a, const LinTile& t, int ks, int nks,
                                             int i, int j) {
-  return a.part + ((size_t)t.q * nks + ks) * Sh::BM * Sh::BN +
-         ((size_t)(i * Sh::TN + j) * kThreads + threadIdx.x) * 4;
+  return a.part + ((size_t)t.q * nks + ks) * Tile64::BM * Tile64::BN +
+         ((size_t)(i * Tile64::TN + j) * kThreads + threadIdx.x) * 4;
 }
 
-template <typename Sh>
 __device__ __forceinline__ bool find(const LinArgs& a, LinTile& t) {
-  return lin_tile<Sh::BM>(a, gated(a.act) ? Sh::BN / 2 : Sh::BN, t);
+  return lin_tile<Tile64::BM>(a, gated(a.act) ? Tile64::BN / 2 : Tile64::BN, t);
 }
 
-template <typename Sh>
 __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
-  constexpr int BM = Sh::BM, BN = Sh::BN, NS = Sh::NS, STAGE = Sh::STAGE, NI = Sh::NI;
-  constexpr int TM = Sh::TM, TN = Sh::TN;
+  constexpr int BM = Tile64::BM, BN = Tile64::BN, NS = Tile64::NS, STAGE = Tile64::STAGE, NI = Tile64::NI;
+  constexpr int TM = Tile64::TM, TN = Tile64::TN;
   __shared__ __attribute__((aligned(16))) uint8_t smem[NS * STAGE];
   LinTile t;
-  if (!find<Sh>(a, t)) return;
+  if (!find(a, t)) return;
   const bool gt = gated(a.act);
   const int N = a.N, K = a.K;
   const uint16_t* x = static_cast<const uint16_t*>(a.x);
@@ -204,7 +198,7 @@ __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
     } else {
       const int b = r - BM, j = b / 16 % TN;
       const int half = gt && j >= TN / 2 ? 1 : 0;
-      const int c = t.n0 + tile_col<Sh>(b / (BN / 2), j - half * (TN / 2), gt) + b % 16;
+      const int c = t.n0 + tile_col(b / (BN / 2), j - half * (TN / 2), gt) + b % 16;
       row = w + ((size_t)half * N + min(c, N - 1)) * K;  // columns past the end: its last
     }
     src[q] = row + kbase * 64 + chunk * 8;
@@ -250,7 +244,7 @@ __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
     }
   }
   if (gridDim.y == 1) {
-    tile_store<Sh>(a, t, acc);
+    tile_store(a, t, acc);
     return;
   }
 #pragma unroll
@@ -258,7 +252,7 @@ __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
     if (wm * (BM / 2) + i * 16 < t.M)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        *reinterpret_cast<f32x4_t*>(tile_part<Sh>(a, t, blockIdx.y, gridDim.y, i, j)) = acc[i][j];
+        *reinterpret_cast<f32x4_t*>(tile_part(a, t, blockIdx.y, gridDim.y, i, j)) = acc[i][j];
 }
 
 // Sums the nks K slices of each tile in slice order, then the epilogue. One
@@ -266,22 +260,21 @@ __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
 // tiles still has many.
 constexpr int kMaxSlices = 16;
 
-template <typename Sh>
 __global__ __launch_bounds__(kThreads) void lin_tile_reduce_kernel(LinArgs a, int nks) {
   LinTile t;
-  if (!find<Sh>(a, t)) return;
+  if (!find(a, t)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const bool gt = gated(a.act);
   const int i = blockIdx.y;
-  const int r = (wave >> 1) * (Sh::BM / 2) + i * 16 + (lane & 15);
-  f32x4_t acc[Sh::TN];
-  if ((wave >> 1) * (Sh::BM / 2) + i * 16 >= t.M) return;
+  const int r = (wave >> 1) * (Tile64::BM / 2) + i * 16 + (lane & 15);
+  f32x4_t acc[Tile64::TN];
+  if ((wave >> 1) * (Tile64::BM / 2) + i * 16 >= t.M) return;
 #pragma unroll
-  for (int j = 0; j < Sh::TN; ++j) {
+  for (int j = 0; j < Tile64::TN; ++j) {
     f32x4_t v[kMaxSlices];
 #pragma unroll
     for (int s = 0; s < kMaxSlices; ++s)  // all loads first, from clamped slices
-      v[s] = *reinterpret_cast<const f32x4_t*>(tile_part<Sh>(a, t, min(s, nks - 1), nks, i, j));
+      v[s] = *reinterpret_cast<const f32x4_t*>(tile_part(a, t, min(s, nks - 1), nks, i, j));
     acc[j] = v[0];
 #pragma unroll
     for (int s = 1; s < kMaxSlices; ++s)
@@ -289,27 +282,28 @@ __global__ __launch_bounds__(kThreads) void lin_tile_reduce_kernel(LinArgs a, in
   }
   if (r >= t.M) return;
 #pragma unroll
-  for (int j = 0; j < Sh::TN; ++j) {
-    if (gt && j >= Sh::TN / 2) continue;
-    const int c = t.n0 + tile_col<Sh>(wave & 1, j, gt) + (lane >> 4) * 4;
-    if (c < a.N) store4(a, t.e, (size_t)(t.row0 + r), c, acc[j], acc[(j + Sh::TN / 2) % Sh::TN]);
+  for (int j = 0; j < Tile64::TN; ++j) {
+    if (gt && j >= Tile64::TN / 2) continue;
+    const int c = t.n0 + tile_col(wave & 1, j, gt) + (lane >> 4) * 4;
+    if (c < a.N) store4(a, t.e, (size_t)(t.row0 + r), c, acc[j], acc[(j + Tile64::TN / 2) % Tile64::TN]);
   }
 }
 
 // ----------------------------------------------------------------- bf16, few rows
 
 // Decode: a few rows per segment, so a launch is a stream of the weights. A
-// workgroup takes up to 16 rows of one segment and 16 output columns; its KQ
-// waves share K in 32-deep steps. Weights go from memory straight to registers
+// workgroup takes up to 16 rows of one segment and 16 output columns; its 4
+// waves share K in 32-deep steps (8 or 16 waves were no faster, 1 x 4096 x 4096
+// to 16 x 512 x 4096: 7.3-11.4 us either way). Weights go from memory straight to registers
 // (no other wave reads them): one 16-byte load per lane per 16 weight rows x 32 k,
 // in chunks of U steps with the next chunk in flight while one is multiplied.
 // v_mfma_f32_16x16x32_bf16 takes the weights as A and the rows as B, lane l
 // loads weight row l % 16 and x row l % 16 at k = 8 (l / 16) of each step. Rows
 // past the block's end read its last row and are not stored. The waves' sums are
 // added in wave order through LDS.
-template <bool GT, int KQ>
-__global__ __launch_bounds__(KQ * 64) void lin_rows_kernel(LinArgs a) {
-  constexpr int U = 4, H = GT ? 2 : 1;
+template <bool GT>
+__global__ __launch_bounds__(kThreads) void lin_rows_kernel(LinArgs a) {
+  constexpr int KQ = 4, U = 4, H = GT ? 2 : 1;
   __shared__ f32x4_t red[KQ][H][64];
   LinTile t;
   if (!lin_tile<16>(a, 16, t)) return;
@@ -463,58 +457,91 @@ unsigned lin_grid(const LinArgs& a, int BM, int bnc) {  // whole rounds of the 8
   return (unsigned)((lin_tiles(a, BM, bnc) + 7) / 8 * 8);
 }
 
-using Tile64 = TileShape<64, 64, 3>;
-using Tile128 = TileShape<128, 128, 2>;
-
-enum LinPath { kRows, kTile64, kTile128, kBig };
+enum LinPath { kRows, kTile64, kBigHalf, kBig };
 struct LinPlan {
   LinPath path;
-  int nks;  // K slices of the tile paths; waves of the few-row path
+  int nks;  // K slices (64 x 64 tiles)
 };
 
 bool host_gated(int act) { return act == kActGeglu || act == kActSwiglu; }
 
-#ifdef LIN_FORCE
+// Path of a bf16 product: the least of the four paths' estimated times, in us. The
+// estimates hold what was measured (graph replay, no act; M x N x K dense, then E
+// experts with evenly drawn rows):
+//                        rows    64x64 (slices)   256x128   256x256
+//   1 x 4096 x 4096       8.7     11.7 (8)           41        44
+//   64 x 4096 x 4096              14.2 (4)           41        50
+//   256 x 4096 x 4096             23.8 (2)           44        69
+//   512 x 4096 x 4096             32.9 (1)           44        70
+//   1024 x 4096 x 4096            60.2 (1)           45        70
+//   2048 x 4096 x 4096           139   (1)           60        74
+//   4096 x 4096 x 4096           309   (1)          117       105
+//   64 x 1024 x 1024      5.0      8.1 (8)           15        19
+//   2048 x 512 x 4096             27.7 (1)           42        68
+//   E 8, 64 rows, 1024 x 1024    7.1     10.0 (1)    15        18
+//   E 8, 512 rows, 4096 x 4096           60.8 (1)    62        76
+//   E 8, 1024 rows, 4096 x 4096         101   (1)    68        83
+//   E 8, 8192 rows, 4096 x 4096         530   (1)   285       274
+//   E 128, 1024 rows, 1024 x 4096       190   (1)   229       188
+//   E 64, 16384 rows, 1024 x 1024        85   (1)    65        58
+// A stage is 64 k. Few-row kernel: every block of 16 rows x 16 columns reads both
+// operands from the caches (8.5 TB/s), and a wave walks a quarter of K (1 us per
+// 1000). 64x64 tiles: 0.36 us a stage while fewer than 1.75 workgroups share a CU,
+// then in proportion, a fifth of which does not hide behind the weights' stream;
+// slices add a launch (3 us) and their partials' round trip. The large tiles run one
+// workgroup a CU: 0.55 or 0.94 us a stage on an idle chip, 0.9 or 1.5 when every CU
+// runs one (power and cache traffic).
 LinPlan lin_plan(const LinArgs& a) {
-  const char* s = getenv("LIN_FORCE");
-  LinPlan p{kTile64, 1};
-  int path = 1, n = 1;
-  sscanf(s, "%d,%d", &path, &n);
-  p.path = (LinPath)path; p.nks = n;
-  return p;
+  const double h = host_gated(a.act) ? 2.0 : 1.0, cols = h * a.N;  // weight rows of an expert
+  // experts with rows, as if each row drew its expert
+  const double live = a.offsets ? a.E * (1.0 - std::exp(-(double)a.M / a.E)) : 1.0;
+  const double stages = a.K / 64;
+  // row tiles of a segmented launch: each segment's last one is half full on average
+  auto row_tiles = [&](int bm) {
+    return a.offsets ? std::max(live, (double)a.M / bm + live / 2) : std::ceil((double)a.M / bm);
+  };
+  auto big = [&](int bn, double idle, double full) {
+    const double tiles = row_tiles(256) * std::ceil(cols / bn);
+    const double whole = std::floor(tiles / 256), rest = tiles - 256 * whole;
+    return 8.0 + (a.offsets ? 2.0 : 0.0) +
+           stages * (whole * full + (rest <= 0 ? 0.0
+                                     : a.K >= 8192 ? full * rest / 256  // split over K
+                                                   : std::max(idle, full * rest / 256)));
+  };
+  const double hbm = 2.0 * ((double)a.M * a.K + live * cols * a.K) / 5.3e6;
+  LinPlan best{kRows, 1};
+  double t = 3.2 + std::max({1.1 * hbm, a.K / 1000.0,
+                             row_tiles(16) * (a.N / 16) * (16 * h + std::min(16.0, a.M / live)) * a.K * 2 / 8.5e6});
+  auto take = [&](LinPath path, int nks, double us) {
+    if (us < t) t = us, best = LinPlan{path, nks};
+  };
+  const double tiles = row_tiles(64) * std::ceil(cols / 64);
+  for (int nks = 1; nks <= 16; nks *= 2) {
+    if (nks > 1 && (a.K / 64 < 2 * nks || tiles * nks > 2048)) break;
+    double us = 4.4 + std::ceil(stages / nks) * 0.36 * std::max(1.0, tiles * nks / 448);
+    if (nks > 1) us += 3.0 + 8.0 * a.M * cols * nks / 5e6;
+    take(kTile64, nks, std::max(us, 3.0 + hbm) + 0.2 * std::min(us, hbm));
+  }
+  if (big_ok(a)) {
+    take(kBigHalf, 1, std::max(big(128, 0.55, 0.9), 8.0 + 1.1 * hbm));
+    take(kBig, 1, std::max(big(256, 0.94, 1.5), 8.0 + hbm));
+  }
+  return best;
 }
-#else
-LinPlan lin_plan(const LinArgs& a) {
-  if (a.M <= 16 || (a.offsets && a.M <= 2 * a.E)) return LinPlan{kRows, 4};
-  if (a.M >= 64 * a.E && a.M >= 256 && big_ok(a)) return LinPlan{kBig, 1};
-  return LinPlan{kTile64, 1};
-}
-#endif
 
-template <typename Sh>
 size_t tile_ws_bytes(const LinArgs& a, int nks) {
   if (nks <= 1) return 0;
-  return (size_t)lin_tiles(a, Sh::BM, host_gated(a.act) ? Sh::BN / 2 : Sh::BN) * nks * Sh::BM *
-         Sh::BN * sizeof(float);
+  return (size_t)lin_tiles(a, Tile64::BM, host_gated(a.act) ? Tile64::BN / 2 : Tile64::BN) * nks * Tile64::BM *
+         Tile64::BN * sizeof(float);
 }
 
-template <typename Sh>
 hipError_t run_tile(LinArgs a, int nks, void* ws, hipStream_t s) {
-  const unsigned grid = lin_grid(a, Sh::BM, host_gated(a.act) ? Sh::BN / 2 : Sh::BN);
+  const unsigned grid = lin_grid(a, Tile64::BM, host_gated(a.act) ? Tile64::BN / 2 : Tile64::BN);
   a.part = static_cast<float*>(ws);
-  hipLaunchKernelGGL((lin_tile_kernel<Sh>), dim3(grid, nks), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((lin_tile_kernel), dim3(grid, nks), dim3(kThreads), 0, s, a);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || nks <= 1) return err;
-  hipLaunchKernelGGL((lin_tile_reduce_kernel<Sh>), dim3(grid, Sh::TM), dim3(kThreads), 0, s, a, nks);
-  return hipGetLastError();
-}
-
-template <bool GT>
-hipError_t run_rows(const LinArgs& a, int kq, hipStream_t s) {
-  const dim3 grid(lin_grid(a, 16, 16));
-  if (kq >= 16) hipLaunchKernelGGL((lin_rows_kernel<GT, 16>), grid, dim3(1024), 0, s, a);
-  else if (kq >= 8) hipLaunchKernelGGL((lin_rows_kernel<GT, 8>), grid, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((lin_rows_kernel<GT, 4>), grid, dim3(256), 0, s, a);
+  hipLaunchKernelGGL((lin_tile_reduce_kernel), dim3(grid, Tile64::TM), dim3(kThreads), 0, s, a, nks);
   return hipGetLastError();
 }
 
@@ -538,9 +565,8 @@ size_t linear_ws_bytes(int E, int M, int N, int K, int act, bool grouped, bool b
   const int32_t some = 0;
   const LinArgs a = lin_args(nullptr, nullptr, 1, M, grouped ? &some : nullptr, E, M, N, K, act);
   const LinPlan p = lin_plan(a);
-  if (p.path == kBig) return big_ws_bytes(a);
-  if (p.path == kTile128) return tile_ws_bytes<Tile128>(a, p.nks);
-  return p.path == kTile64 ? tile_ws_bytes<Tile64>(a, p.nks) : 0;
+  if (p.path >= kBigHalf) return big_ws_bytes(a, p.path == kBigHalf);
+  return p.path == kTile64 ? tile_ws_bytes(a, p.nks) : 0;
 }
 
 hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
@@ -554,12 +580,18 @@ hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
     hipLaunchKernelGGL(lin_f32_kernel, dim3(lin_grid(a, 64, gt ? 32 : 64)), dim3(kThreads), 0, s, a);
     return hipGetLastError();
   }
-  const LinPlan p = lin_plan(a);
+  LinPlan p = lin_plan(a);
+  // gathered rows past the large tiles' 32-bit offsets: no workspace needed either
+  if (p.path >= kBigHalf && gather && !big_gather_ok(a)) p = LinPlan{kTile64, 1};
   switch (p.path) {
-    case kRows: return gt ? run_rows<true>(a, p.nks, s) : run_rows<false>(a, p.nks, s);
-    case kTile64: return run_tile<Tile64>(a, p.nks, ws, s);
-    case kTile128: return run_tile<Tile128>(a, p.nks, ws, s);
-    default: return launch_big(a, ws, s);
+    case kRows: {
+      const dim3 grid(lin_grid(a, 16, 16));
+      if (gt) hipLaunchKernelGGL((lin_rows_kernel<true>), grid, dim3(kThreads), 0, s, a);
+      else hipLaunchKernelGGL((lin_rows_kernel<false>), grid, dim3(kThreads), 0, s, a);
+      return hipGetLastError();
+    }
+    case kTile64: return run_tile(a, p.nks, ws, s);
+    default: return launch_big(a, p.path == kBigHalf, ws, s);
   }
 }
 

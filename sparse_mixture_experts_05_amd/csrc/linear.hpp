@@ -87,10 +87,12 @@ __device__ __forceinline__ void store4(const LinArgs& a, int e, size_t row, int 
       finish4(a.act, g, u, bg, bu, a.res != nullptr, rv);
 }
 
-// Big-tile path (linear_big.hip): 256 x 256 tiles.
-bool big_ok(const LinArgs& a);           // the shape's offsets fit the kernel's addressing
-size_t big_ws_bytes(const LinArgs& a);
-hipError_t launch_big(LinArgs a, void* ws, hipStream_t s);
+// Big-tile path (linear_big.hip): 256 rows x 256 weight rows, or half as many
+// weight rows.
+bool big_ok(const LinArgs& a);         // the shape's offsets fit the kernel's addressing
+bool big_gather_ok(const LinArgs& a);  // and those of the gathered rows
+size_t big_ws_bytes(const LinArgs& a, bool half);
+hipError_t launch_big(LinArgs a, bool half, void* ws, hipStream_t s);
 
 }  // namespace lin
 }  // namespace moe

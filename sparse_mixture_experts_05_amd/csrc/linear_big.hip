@@ -33,7 +33,10 @@ namespace {
 using namespace lin;
 
 constexpr int kThreads = 256;
-constexpr int BM = 256, BN = 256;                // rows, weight rows of a tile
+constexpr int BM = 256;                          // rows of a tile
+// Column tiles per n-block of the tile order: the same panel width for both tiles.
+template <int BN>
+constexpr int kBlock = plan::kBlockCols * 256 / BN;
 constexpr int kTableInt4 = plan::kEntryInts / 4;
 constexpr size_t kPartTiles = (size_t)plan::kXcds * plan::kSlots;  // split units at most
 
@@ -66,6 +69,7 @@ MOE_HD inline plan::Shape shape_of(const LinArgs& a, bool gated_act) {
 // Writes the tile table of a grouped launch: entries [0, slots) for the product
 // (workgroup g: slot g / 8 on XCD g % 8), then kReduceSlots for its split-K
 // reduce. Every workgroup scans the segments and resolves 256 slots.
+template <int BN>
 __global__ __launch_bounds__(kThreads) void lin_plan_kernel(LinArgs a) {
   __shared__ plan::Tables L;
   const plan::Shape sh = shape_of(a, gated(a.act));
@@ -89,7 +93,7 @@ __global__ __launch_bounds__(kThreads) void lin_plan_kernel(LinArgs a) {
   const int mode = i < a.slots ? 0 : 1;
   const int g = mode ? i - a.slots : i;
   plan::Tile ta{}, tb{};
-  const int kind = plan::resolve_slot<BM, BN, plan::kBlockCols>(sh, S, L, g % plan::kXcds,
+  const int kind = plan::resolve_slot<BM, BN, kBlock<BN>>(sh, S, L, g % plan::kXcds,
                                                                 g / plan::kXcds, mode, ta, tb);
   int e[plan::kEntryInts];
   plan::encode_entry(kind, ta, tb, e);
@@ -108,6 +112,7 @@ __device__ __forceinline__ plan::Tile uniform(const plan::Tile& t) {
 
 // Tile of slot i (of the product, or with reduce of its reduce launch). L: LDS
 // scratch for the dense form. False: no work.
+template <int BN>
 __device__ __forceinline__ bool tile_of(const LinArgs& a, bool gt, int i, bool reduce,
                                         plan::Tables& L, plan::Tile& t) {
   if (a.offsets != nullptr) {
@@ -127,29 +132,31 @@ __device__ __forceinline__ bool tile_of(const LinArgs& a, bool gt, int i, bool r
   __syncthreads();
   const plan::Sched S = plan::finish_schedule(sh, L);
   plan::Tile tb;
-  const int kind = plan::resolve_slot<BM, BN, plan::kBlockCols>(
+  const int kind = plan::resolve_slot<BM, BN, kBlock<BN>>(
       sh, S, L, i % plan::kXcds, i / plan::kXcds, reduce ? 1 : 0, t, tb);
   __syncthreads();  // L is the first stage buffer
   t = uniform(t);
   return kind == 0;
 }
 
-// Weight row of row r of a tile: the expert's row n0 + r, or for a gated product
-// (n0, N in output columns) wave half r / 128, sub-tile (r / 32) % 4: two of gate
-// rows, then two of up rows, of the same 64 columns.
-template <bool GT>
+// Weight row of row r of a tile of 64 SN weight rows: the expert's row n0 + r, or
+// for a gated product (n0, N in output columns) wave half r / (32 SN), sub-tile
+// (r / 32) % SN: half of them gate rows, then the up rows of the same columns.
+template <bool GT, int SN>
 __device__ __forceinline__ size_t tile_weight_row(int r, int n0, int N) {
   if constexpr (!GT) return (size_t)min(n0 + r, N - 1);
-  const int j = (r >> 5) & 3;
-  return (size_t)(j >> 1) * N + min(n0 + (r >> 7) * 64 + (j & 1) * 32 + (r & 31), N - 1);
+  constexpr int HS = SN / 2;
+  const int j = (r >> 5) % SN;
+  return (size_t)(j / HS) * N + min(n0 + r / (32 * SN) * (32 * HS) + j % HS * 32 + (r & 31), N - 1);
 }
 
-template <int ACT, bool RES>
+template <int ACT, bool RES, int SN>
 __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
   constexpr bool GT = ACT == kActGeglu || ACT == kActSwiglu;
   constexpr int NW = 4, BK = 64;
   constexpr int ROWB = BK * 2;                 // 128 bytes = 8 chunks of 16
-  constexpr int SM = 4, SN = 4;                // 32 x 32 sub-tiles of a wave
+  constexpr int SM = 4;                        // 32 x 32 sub-tiles of a wave: 4 x SN
+  constexpr int BN = 64 * SN;                  // weight rows of a tile
   constexpr int RPI = 8;                       // rows per copy instruction
   constexpr int A_INST = BM / RPI / NW, B_INST = BN / RPI / NW;  // copies per wave per stage
   constexpr int A_STAGE = BM * ROWB, B_STAGE = BN * ROWB;
@@ -159,7 +166,7 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[LDS_BYTES];
 
   plan::Tile t;
-  if (!tile_of(a, GT, blockIdx.x, false, *reinterpret_cast<plan::Tables*>(smem), t)) return;
+  if (!tile_of<BN>(a, GT, blockIdx.x, false, *reinterpret_cast<plan::Tables*>(smem), t)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int N = a.N, K = a.K, M = t.M;
   const int n0 = GT ? t.n0 / 2 : t.n0;         // first output column
@@ -190,7 +197,7 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
   for (int q = 0; q < B_INST; ++q) {
     const int r = (wave * B_INST + q) * RPI + lrow;
     const int c = (lane & 7) ^ ((r >> 1) & 7);
-    ov[A_INST + q] = (uint32_t)((tile_weight_row<GT>(r, n0, N) * K + c * 8) * 2);
+    ov[A_INST + q] = (uint32_t)((tile_weight_row<GT, SN>(r, n0, N) * K + c * 8) * 2);
   }
   const int KT0 = K / BK;
   const int kbase = t.ks * KT0 / t.spl;
@@ -228,7 +235,7 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
   // Every fragment row of this lane is lane % 32 of a 32-row sub-tile: one LDS
   // offset per operand, the sub-tiles 32 rows apart (a constant of the read).
   const int fa0 = (wm * 128 + (lane & 31)) * ROWB;
-  const int fb0 = (wn * 128 + (lane & 31)) * ROWB;
+  const int fb0 = (wn * (BN / 2) + (lane & 31)) * ROWB;
   const int sw = (lane >> 1) & 7;
   const int khalf = lane >> 5;
   // row sub-tiles of this wave that hold data: all of them except in a segment's
@@ -236,50 +243,52 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
   const int nsub = __builtin_amdgcn_readfirstlane(min(SM, max(0, (M - wm * 128 + 31) / 32)));
 
   u32x4_t ca[SM], cb[SN], na[SM], nb[SN];
-  // fragment read r of k slice ks (0..7: b0, a0, b1, b2, b3, a1, a2, a3, the
-  // order of first use)
+  constexpr int NM = SM * SN, NR = SM + SN;  // MFMAs, fragment reads of a k slice
+  static_assert(NR <= NM, "a read after each of the first MFMAs");
+  // fragment read r of k slice ks: b0, a0, the other b, the other a (the order of
+  // first use)
   auto read_r = [&](const uint8_t* sa, const uint8_t* sb, int ks, int r, u32x4_t (&fa_)[SM],
                     u32x4_t (&fb_)[SN]) {
     const int off = ((ks * 2 + khalf) ^ sw) << 4;
     if (r == 0) fb_[0] = ld16(sb + fb0 + off);
     else if (r == 1) fa_[0] = ld16(sa + fa0 + off);
-    else if (r <= 4) fb_[r - 1] = ld16(sb + fb0 + (r - 1) * 32 * ROWB + off);
-    else fa_[r - 4] = ld16(sa + fa0 + (r - 4) * 32 * ROWB + off);
+    else if (r <= SN) fb_[r - 1] = ld16(sb + fb0 + (r - 1) * 32 * ROWB + off);
+    else fa_[r - SN] = ld16(sa + fa0 + (r - SN) * 32 * ROWB + off);
   };
   // NS: row sub-tiles with data, a compile-time count, so that a partial tile's
   // loop has no branch between its MFMAs (its empty sub-tiles are skipped)
   auto main_loop = [&](auto ns_tag) {
     constexpr int NS = decltype(ns_tag)::value;
-    // one k slice: 16 MFMAs on (fa_, fb_); after each of the first 8 a read of
+    // one k slice: NM MFMAs on (fa_, fb_); after each of the first NR a read of
     // slice rks of the buffers (rsa, rsb) into (ra_, rb_); copies q0 .. q1-1
-    // spread evenly over the 16 (rows of stage akt for q < 8, weights of stage
+    // spread evenly over them (rows of stage akt for q < 8, weights of stage
     // bkt into slot bslot for q >= 8)
     auto slice = [&](const u32x4_t (&fa_)[SM], const u32x4_t (&fb_)[SN], const uint8_t* rsa,
                      const uint8_t* rsb, int rks, u32x4_t (&ra_)[SM], u32x4_t (&rb_)[SN],
                      auto q0c, auto q1c, int akt, int bkt, int bslot) {
       constexpr int q0 = decltype(q0c)::value, nq = decltype(q1c)::value - q0;
-      static_for<16>([&](auto mc) {
-        constexpr int m = decltype(mc)::value, i = m >> 2, j = m & 3;
+      static_for<NM>([&](auto mc) {
+        constexpr int m = decltype(mc)::value, i = m / SN, j = m % SN;
         if constexpr (i < NS)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(fb_[j]), as_bf16x8(fa_[i]),
                                                               acc[i][j], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (m < 8) {
+        if constexpr (m < NR) {
           read_r(rsa, rsb, rks, m, ra_, rb_);
           __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (nq > 0 && (m * nq) / 16 != ((m + 1) * nq) / 16) {
-          constexpr int q = q0 + (m * nq) / 16;
+        if constexpr (nq > 0 && (m * nq) / NM != ((m + 1) * nq) / NM) {
+          constexpr int q = q0 + (m * nq) / NM;
           copy(q < A_INST ? akt : bkt, bslot, q);
           __builtin_amdgcn_sched_barrier(0);
         }
       });
     };
-    using I0 = std::integral_constant<int, 0>;
-    using I8 = std::integral_constant<int, 8>;
-    using I11 = std::integral_constant<int, 11>;
-    using I14 = std::integral_constant<int, 14>;
-    using I16 = std::integral_constant<int, 16>;
+    using Q0 = std::integral_constant<int, 0>;  // copies: rows, then weights in three parts
+    using Q1 = std::integral_constant<int, A_INST>;
+    using Q2 = std::integral_constant<int, A_INST + (B_INST * 3 + 7) / 8>;
+    using Q3 = std::integral_constant<int, A_INST + (B_INST * 6 + 7) / 8>;
+    using Q4 = std::integral_constant<int, A_INST + B_INST>;
     // prologue: stages 0 and 1 and the weights of stage 2 in flight, in the order
     // the waits count them; stage 0 landed everywhere
     static_for<A_INST + B_INST>([&](auto q) { copy(0, 0, decltype(q)::value); });
@@ -287,7 +296,7 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
     static_for<B_INST>([&](auto q) { copy(min(2, last), 2, A_INST + decltype(q)::value); });
     wait_vmcnt<A_INST + 2 * B_INST>();
     lds_barrier();
-    static_for<8>([&](auto r) { read_r(a_buf(0), b_buf(0), 0, decltype(r)::value, ca, cb); });
+    static_for<NR>([&](auto r) { read_r(a_buf(0), b_buf(0), 0, decltype(r)::value, ca, cb); });
     // One code path for every stage: past the end the copies fetch the last stage
     // again into buffers nobody reads any more and the reads fetch a stale buffer
     // (both in bounds); the copies are drained before the epilogue reuses the LDS.
@@ -298,15 +307,15 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
       const int k2 = min(kt + 2, last);
       const uint8_t* sa = a_buf(kt);
       const uint8_t* sb = b_buf(bs);
-      slice(ca, cb, sa, sb, 1, na, nb, I8{}, I11{}, 0, k2, bsp);
-      slice(na, nb, sa, sb, 2, ca, cb, I11{}, I14{}, 0, k2, bsp);
-      slice(ca, cb, sa, sb, 3, na, nb, I14{}, I16{}, 0, k2, bsp);
+      slice(ca, cb, sa, sb, 1, na, nb, Q1{}, Q2{}, 0, k2, bsp);
+      slice(na, nb, sa, sb, 2, ca, cb, Q2{}, Q3{}, 0, k2, bsp);
+      slice(ca, cb, sa, sb, 3, na, nb, Q3{}, Q4{}, 0, k2, bsp);
       // stage kt+1 landed for this wave (only the weights of stage kt+2 issued
       // above may still be in flight), then for everyone; stage kt fully read, so
       // row buffer kt & 1 is free
       wait_vmcnt<B_INST>();
       lds_barrier();
-      slice(na, nb, a_buf(kt + 1), b_buf(bs1), 0, ca, cb, I0{}, I8{}, k2, 0, 0);
+      slice(na, nb, a_buf(kt + 1), b_buf(bs1), 0, ca, cb, Q0{}, Q1{}, k2, 0, 0);
       bs = bs1;
     }
     wait_vmcnt<0>();
@@ -345,8 +354,9 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
   }
   // Finished columns go to a [256 x BC] bf16 tile in LDS (the stages are free),
   // then whole rows to memory, 16 bytes a lane. The 16-byte chunks of a row are
-  // XOR-swizzled by its low 4 bits, so the rows of a write spread over the banks.
+  // XOR-swizzled by its low bits, so the rows of a write spread over the banks.
   constexpr int CROWB = BC * 2;
+  constexpr int SWZ = (CROWB / 16 < 16 ? CROWB / 16 : 16) - 1;
   const uint16_t* bias = static_cast<const uint16_t*>(a.bias);
   const uint16_t* res = static_cast<const uint16_t*>(a.res);
   const int lr = wm * 128 + (lane & 31);            // first row of this lane in the tile
@@ -387,14 +397,14 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
       // pinned to the accumulation registers up to here: without this the compiler
       // reads all of them out before the first branch of the epilogue, and spills
       asm volatile("" : "+a"(acc[i][j]));
-      if constexpr (GT) asm volatile("" : "+a"(acc[i][j + 2]));
+      if constexpr (GT) asm volatile("" : "+a"(acc[i][j + SN / 2]));
       const f32x16_t& g = acc[i][j];
-      const f32x16_t& u = acc[i][GT ? j + 2 : j];
+      const f32x16_t& u = acc[i][GT ? j + SN / 2 : j];
       const uint2 o = finish4(ACT, f32x4_t{g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]},
                                    f32x4_t{u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]},
                                    bg, bu, RES, rv[i]);
       const int row = lr + i * 32;
-      *reinterpret_cast<uint2*>(smem + row * CROWB + (((col >> 3) ^ (row & 15)) << 4) + khalf * 8) = o;
+      *reinterpret_cast<uint2*>(smem + row * CROWB + (((col >> 3) ^ (row & SWZ)) << 4) + khalf * 8) = o;
     }
     __builtin_amdgcn_sched_barrier(0);
   });
@@ -406,7 +416,7 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
 #pragma unroll 4
   for (int it = 0; it < BM / NW / RPW; ++it) {
     const int row = wave * (BM / NW) + it * RPW + lane / LPR;
-    const u32x4_t v = ld16(smem + row * CROWB + ((cl ^ (row & 15)) << 4));
+    const u32x4_t v = ld16(smem + row * CROWB + ((cl ^ (row & SWZ)) << 4));
     if (cok && row < M) st16(y + (size_t)row * N + cl * 8, v);
   }
 }
@@ -416,18 +426,19 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
 // them), so the partials stream through many CUs.
 constexpr int kReduceParts = 8;
 
-template <int ACT>
+template <int ACT, int SN>
 __global__ __launch_bounds__(kThreads) void lin_reduce_kernel(LinArgs a) {
   constexpr bool GT = ACT == kActGeglu || ACT == kActSwiglu;
+  constexpr int BN = 64 * SN;
   __shared__ plan::Tables L;
   plan::Tile t;
-  if (!tile_of(a, GT, blockIdx.x / kReduceParts, true, L, t)) return;
+  if (!tile_of<BN>(a, GT, blockIdx.x / kReduceParts, true, L, t)) return;
   const int N = a.N;
   const int n0 = GT ? t.n0 / 2 : t.n0;
   const int nvalid = N - n0;
   const float* P = a.part + (size_t)t.unit0 * BM * BN;
   const int spl = t.spl;
-  constexpr int JS = GT ? 2 : 4;  // weight sub-tiles that give outputs
+  constexpr int JS = GT ? SN / 2 : SN;  // weight sub-tiles that give outputs
   constexpr int RUNS = 4 * 4 * JS * 4 * 64;  // runs of 4 columns in a tile
   for (int e = (blockIdx.x % kReduceParts) * kThreads + threadIdx.x; e < RUNS;
        e += kReduceParts * kThreads) {
@@ -435,7 +446,7 @@ __global__ __launch_bounds__(kThreads) void lin_reduce_kernel(LinArgs a) {
     const int lane = e & 63, q = (e >> 6) & 3, j = (e >> 8) % JS, wi = (e >> 8) / JS;
     const int wave = wi >> 2, i = wi & 3;
     const int row = (wave >> 1) * 128 + i * 32 + (lane & 31);
-    const int col = (wave & 1) * (GT ? 64 : 128) + j * 32 + q * 8 + (lane >> 5) * 4;
+    const int col = (wave & 1) * (JS * 32) + j * 32 + q * 8 + (lane >> 5) * 4;
     if (row >= t.M || col >= nvalid) continue;
     const float* src = P + (size_t)wave * (BM * BN / 4) + lane * 4;
     f32x4_t g{}, u{};
@@ -443,8 +454,8 @@ __global__ __launch_bounds__(kThreads) void lin_reduce_kernel(LinArgs a) {
 #pragma unroll
     for (int ks = 0; ks < plan::kMaxSplit; ++ks) {  // all loads first, from clamped slices
       const float* sl = src + (size_t)min(ks, spl - 1) * BM * BN;
-      vg[ks] = *reinterpret_cast<const f32x4_t*>(sl + ((i * 4 + j) * 4 + q) * 256);
-      if constexpr (GT) vu[ks] = *reinterpret_cast<const f32x4_t*>(sl + ((i * 4 + j + 2) * 4 + q) * 256);
+      vg[ks] = *reinterpret_cast<const f32x4_t*>(sl + ((i * SN + j) * 4 + q) * 256);
+      if constexpr (GT) vu[ks] = *reinterpret_cast<const f32x4_t*>(sl + ((i * SN + j + SN / 2) * 4 + q) * 256);
     }
 #pragma unroll
     for (int ks = 0; ks < plan::kMaxSplit; ++ks)
@@ -463,6 +474,7 @@ struct BigLayout {
   size_t part, table, bytes;
 };
 
+template <int BN>
 BigLayout big_layout(const LinArgs& a) {
   LinArgs b = a;
   b.part = nullptr;
@@ -476,53 +488,61 @@ BigLayout big_layout(const LinArgs& a) {
   return L;
 }
 
-template <int ACT>
+template <int ACT, int SN>
 hipError_t run_big(const LinArgs& a, hipStream_t s) {
   if (a.res != nullptr)
-    hipLaunchKernelGGL((lin_big_kernel<ACT, true>), dim3(a.slots), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((lin_big_kernel<ACT, true, SN>), dim3(a.slots), dim3(kThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((lin_big_kernel<ACT, false>), dim3(a.slots), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((lin_big_kernel<ACT, false, SN>), dim3(a.slots), dim3(kThreads), 0, s, a);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || a.part == nullptr) return err;
-  hipLaunchKernelGGL((lin_reduce_kernel<ACT>), dim3(plan::kReduceSlots * kReduceParts),
+  hipLaunchKernelGGL((lin_reduce_kernel<ACT, SN>), dim3(plan::kReduceSlots * kReduceParts),
                      dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
-}  // namespace
-
-namespace lin {
-
-// The kernel's 32-bit byte offsets: the gathered rows from x, 256 buffer rows,
-// and an expert's weights from the tile's base.
-bool big_ok(const LinArgs& a) {
-  const size_t lim = size_t(1) << 32, row = (size_t)a.K * 2;
-  const bool gt = a.act == kActGeglu || a.act == kActSwiglu;
-  const size_t x = (size_t)(a.gather ? a.gT : BM) * row;
-  return x < lim && (size_t)(gt ? 2 : 1) * a.N * row < lim;
-}
-
-size_t big_ws_bytes(const LinArgs& a) { return big_layout(a).bytes; }
-
-hipError_t launch_big(LinArgs a, void* ws, hipStream_t s) {
-  const BigLayout L = big_layout(a);
+template <int SN>
+hipError_t launch_big_sn(LinArgs a, void* ws, hipStream_t s) {
+  const BigLayout L = big_layout<64 * SN>(a);
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.part = L.split ? reinterpret_cast<float*>(base) : nullptr;
   a.slots = L.slots;
   if (a.offsets) {
     a.table = reinterpret_cast<const int4*>(base + L.table);
     const int n = L.slots + plan::kReduceSlots;
-    hipLaunchKernelGGL(lin_plan_kernel, dim3((n + kThreads - 1) / kThreads), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((lin_plan_kernel<64 * SN>), dim3((n + kThreads - 1) / kThreads), dim3(kThreads),
+                       0, s, a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
   switch (a.act) {
-    case kActNone: return run_big<kActNone>(a, s);
-    case kActGelu: return run_big<kActGelu>(a, s);
-    case kActSilu: return run_big<kActSilu>(a, s);
-    case kActGeglu: return run_big<kActGeglu>(a, s);
-    default: return run_big<kActSwiglu>(a, s);
+    case kActNone: return run_big<kActNone, SN>(a, s);
+    case kActGelu: return run_big<kActGelu, SN>(a, s);
+    case kActSilu: return run_big<kActSilu, SN>(a, s);
+    case kActGeglu: return run_big<kActGeglu, SN>(a, s);
+    default: return run_big<kActSwiglu, SN>(a, s);
   }
+}
+
+}  // namespace
+
+namespace lin {
+
+// The kernel's 32-bit byte offsets: 256 buffer rows and an expert's weights from the
+// tile's base, and gathered rows from x.
+constexpr size_t kOffsets = size_t(1) << 32;
+bool big_ok(const LinArgs& a) {
+  const bool gt = a.act == kActGeglu || a.act == kActSwiglu;
+  return std::max((size_t)BM, (size_t)(gt ? 2 : 1) * a.N) * a.K * 2 < kOffsets;
+}
+bool big_gather_ok(const LinArgs& a) { return (size_t)a.gT * a.K * 2 < kOffsets; }
+
+size_t big_ws_bytes(const LinArgs& a, bool half) {
+  return half ? big_layout<128>(a).bytes : big_layout<256>(a).bytes;
+}
+
+hipError_t launch_big(LinArgs a, bool half, void* ws, hipStream_t s) {
+  return half ? launch_big_sn<2>(a, ws, s) : launch_big_sn<4>(a, ws, s);
 }
 
 }  // namespace lin

@@ -25,51 +25,89 @@
 namespace moe {
 namespace {
 
-// VEC consecutive elements at p as fp32, and back with one rounding. 16-byte
-// accesses for VEC > 1 (the host picks VEC = 1 where H leaves rows unaligned).
+// VEC consecutive elements as they lie in memory: 16 bytes at any element's address
+// (rows whose length is no multiple of VEC start unaligned, which global loads and
+// stores take), or one element for rows shorter than that. Loads are issued raw, from
+// addresses clamped into the row, and widened when they are used: a widening next to
+// its load, or a load under a branch, would wait for each load in turn.
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+template <typename T, int VEC>
+struct Raw {
+  u32x4_t q;
+};
+template <typename T>
+struct Raw<T, 1> {
+  T q;
+};
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> load_raw(const T* p) {
+  Raw<T, VEC> r;
+  if constexpr (VEC == 1) r.q = *p;
+  else r.q = *reinterpret_cast<const u32x4_any_t*>(p);
+  return r;
+}
 template <int VEC>
-__device__ __forceinline__ void load_vec(const uint16_t* p, float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    const u32x4_t q = ld16(p);
+__device__ __forceinline__ void widen(const Raw<uint16_t, VEC>& r, float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    v[0] = bf16_to_f32(r.q);
+  } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_to_f32(q[i] & 0xffffu);
-      v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+      v[2 * i] = bf16_to_f32(r.q[i] & 0xffffu);
+      v[2 * i + 1] = __uint_as_float(r.q[i] & 0xffff0000u);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = bf16_to_f32(p[i]);
   }
 }
 template <int VEC>
-__device__ __forceinline__ void load_vec(const float* p, float (&v)[VEC]) {
-  if constexpr (VEC == 4) {
-    const f32x4_t q = *reinterpret_cast<const f32x4_t*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = q[i];
+__device__ __forceinline__ void widen(const Raw<float, VEC>& r, float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    v[0] = r.q;
   } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = p[i];
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r.q[i]);
   }
 }
+// Stores v[skip ..] at p + skip ..
 template <int VEC>
-__device__ __forceinline__ void store_vec(uint16_t* p, const float (&v)[VEC]) {
+__device__ __forceinline__ void store_vec(uint16_t* p, const float (&v)[VEC], int skip) {
   if constexpr (VEC == 8) {
-    st16(p, u32x4_t{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]),
-                    cvt_bf16x2(v[6], v[7])});
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) p[i] = (uint16_t)f32_to_bf16(v[i]);
+    if (skip == 0) {
+      *reinterpret_cast<u32x4_any_t*>(p) = u32x4_t{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
+                                                   cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7])};
+      return;
+    }
   }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j)
+    if (j >= skip) p[j] = (uint16_t)f32_to_bf16(v[j]);
 }
 template <int VEC>
-__device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC]) {
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC], int skip) {
   if constexpr (VEC == 4) {
-    *reinterpret_cast<f32x4_t*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) p[i] = v[i];
+    if (skip == 0) {
+      *reinterpret_cast<u32x4_any_t*>(p) = u32x4_t{__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                                   __float_as_uint(v[2]), __float_as_uint(v[3])};
+      return;
+    }
   }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j)
+    if (j >= skip) p[j] = v[j];
+}
+
+// Vector i of thread t covers the elements [e, e + VEC), e = (i * TR + t) * VEC. The
+// one that would pass the end of the row is loaded at H - VEC instead; its first
+// `skip` elements then belong to the vector before it (all of them past the end) and
+// are neither counted nor stored here. The host takes the fewest vectors NV per thread
+// that hold the row, so those below NV / 2 are whole.
+template <int VEC, int TR, int NV>
+__device__ __forceinline__ int vec_start(int i, int t, int H) {
+  const int e = (i * TR + t) * VEC;
+  return i < NV / 2 ? e : min(e, H - VEC);
+}
+template <int VEC, int TR, int NV>
+__device__ __forceinline__ int vec_skip(int i, int t, int H) {
+  return i < NV / 2 ? 0 : max((i * TR + t) * VEC - (H - VEC), 0);
 }
 
 template <int L>
@@ -98,19 +136,29 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[TR / 64], int& bu
   return v;
 }
 
-// norm of the row held in v (kind MOE_NORM_RMS / MOE_NORM_LAYER). Elements
-// past H are never counted and never stored.
+// The vectors of a row-long array that this thread holds (null: none).
 template <typename T, int VEC, int TR, int NV>
-__device__ __forceinline__ void norm_row(float (&v)[NV][VEC], int kind, const T* w, const T* b,
-                                         int H, float eps, int t,
+struct RowRaw {
+  Raw<T, VEC> r[NV];
+  __device__ __forceinline__ void load(const T* p, int H, int t) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) r[i] = load_raw<T, VEC>(p + vec_start<VEC, TR, NV>(i, t, H));
+  }
+};
+
+// norm of the row held in v (kind kNormRms / kNormLayer), whose weight and bias are
+// on their way in w and b.
+template <typename T, int VEC, int TR, int NV>
+__device__ __forceinline__ void norm_row(float (&v)[NV][VEC], int kind, bool has_w, bool has_b,
+                                         const RowRaw<T, VEC, TR, NV>& w,
+                                         const RowRaw<T, VEC, TR, NV>& b, int H, float eps, int t,
                                          float (*red)[TR / 64], int& buf) {
   if (kind == kNormLayer) {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if ((i * TR + t) * VEC < H)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) s += v[i][j];
+      for (int j = 0; j < VEC; ++j) s += j >= vec_skip<VEC, TR, NV>(i, t, H) ? v[i][j] : 0.0f;
     const float mu = row_sum<TR>(s, red, buf) / (float)H;  // divided: exact for equal elements
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -120,21 +168,22 @@ __device__ __forceinline__ void norm_row(float (&v)[NV][VEC], int kind, const T*
   float q = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if ((i * TR + t) * VEC < H)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) q = fmaf(v[i][j], v[i][j], q);
+    for (int j = 0; j < VEC; ++j) {
+      const float x = j >= vec_skip<VEC, TR, NV>(i, t, H) ? v[i][j] : 0.0f;
+      q = fmaf(x, x, q);
+    }
   const float r = 1.0f / sqrtf(row_sum<TR>(q, red, buf) / (float)H + eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = (i * TR + t) * VEC;
     float wv[VEC], bv[VEC];
-    if (w != nullptr && e < H) load_vec<VEC>(w + e, wv);
-    if (b != nullptr && e < H) load_vec<VEC>(b + e, bv);
+    widen<VEC>(w.r[i], wv);
+    widen<VEC>(b.r[i], bv);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
       float o = v[i][j] * r;
-      if (w != nullptr) o *= wv[j];
-      if (b != nullptr) o += bv[j];
+      if (has_w) o *= wv[j];
+      if (has_b) o += bv[j];
       v[i][j] = o;
     }
   }
@@ -149,115 +198,107 @@ struct NormArgs {
   float eps, scale;
 };
 
-// TR threads per row, 256 / TR (at least one) rows per workgroup; the
-// workgroups walk the rows with the grid's stride.
+// TR threads per row, 256 / TR (at least one) rows per workgroup. One row each: in
+// a loop over rows the next row's loads wait for this one's stores (16384 x 4096
+// bf16: 2048 workgroups walking the rows 63 us, one row each 53 us).
 template <typename T, int VEC, int TR, int NV, bool RES>
 __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_kernel(NormArgs a) {
   constexpr int RPB = TR < 256 ? 256 / TR : 1;
   static_assert(TR == 64 || RPB == 1, "a row's threads are a wave or a whole workgroup");
+  using Row = RowRaw<T, VEC, TR, NV>;
   __shared__ float red[2][TR / 64];
   int buf = 0;
   const int t = threadIdx.x % TR;
   const int H = a.H;
-  const T* x = static_cast<const T*>(a.x);
+  const int row = blockIdx.x * RPB + threadIdx.x / TR;
+  if (row >= a.rows) return;  // whole waves of a workgroup without barriers
+  const size_t base = (size_t)row * H;
   const T* w = static_cast<const T*>(a.w);
   const T* b = static_cast<const T*>(a.b);
-  T* out = static_cast<T*>(a.out);
-  for (int row = blockIdx.x * RPB + threadIdx.x / TR; row < a.rows; row += gridDim.x * RPB) {
-    const size_t base = (size_t)row * H;
-    float v[NV][VEC], r[RES ? NV : 1][VEC];
+  const T* x = static_cast<const T*>(a.x) + base;
+  // every load of the row first; arrays that are not there read the row itself
+  Row rx, rw, rb;
+  rx.load(x, H, t);
+  float v[NV][VEC];
+  if constexpr (!RES) {
+    rw.load(w != nullptr ? w : x, H, t);
+    rb.load(b != nullptr ? b : x, H, t);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) widen<VEC>(rx.r[i], v[i]);
+    norm_row<T, VEC, TR, NV>(v, a.kind, w != nullptr, b != nullptr, rw, rb, H, a.eps, t, red, buf);
+  } else {
+    const T* gate = static_cast<const T*>(a.gate);
+    const T* nw = static_cast<const T*>(a.nw);
+    const T* nb = static_cast<const T*>(a.nb);
+    const bool gv = a.gate_mode >= kGateChannel;
+    Row rr, rg, rnw, rnb;
+    rr.load(static_cast<const T*>(a.res) + base, H, t);
+    if (w != nullptr) rw.load(w, H, t);
+    if (b != nullptr) rb.load(b, H, t);
+    if (gv) rg.load(a.gate_mode == kGateFull ? gate + base : gate, H, t);
+    constexpr bool kLate = TR == 1024;  // 128 registers a thread: they would spill
+    if (!kLate && nw != nullptr) rnw.load(nw, H, t);
+    if (!kLate && nb != nullptr) rnb.load(nb, H, t);
+    float g1[1] = {1.0f};
+    if (a.gate_mode == kGateToken) widen<1>(load_raw<T, 1>(gate + row), g1);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) widen<VEC>(rx.r[i], v[i]);
+    if (a.kind != kNormNone)
+      norm_row<T, VEC, TR, NV>(v, a.kind, w != nullptr, b != nullptr, rw, rb, H, a.eps, t, red, buf);
+    T* out = static_cast<T*>(a.out) + base;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (i * TR + t) * VEC;
+      float r[VEC], g[VEC];
+      widen<VEC>(rr.r[i], r);
+      if (gv) widen<VEC>(rg.r[i], g);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] = 0.0f;
-      if (e < H) load_vec<VEC>(x + base + e, v[i]);
+      for (int j = 0; j < VEC; ++j) v[i][j] = fmaf(v[i][j] * (gv ? g[j] : g1[0]), a.scale, r[j]);
+      store_vec<VEC>(out + vec_start<VEC, TR, NV>(i, t, H), v[i], vec_skip<VEC, TR, NV>(i, t, H));
     }
-    if constexpr (RES) {
-      const T* res = static_cast<const T*>(a.res);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = (i * TR + t) * VEC;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) r[i][j] = 0.0f;
-        if (e < H) load_vec<VEC>(res + base + e, r[i]);
-      }
-    }
-    if (a.kind != kNormNone) norm_row<T, VEC, TR, NV>(v, a.kind, w, b, H, a.eps, t, red, buf);
-    if constexpr (RES) {
-      const T* gate = static_cast<const T*>(a.gate);
-      const T* g = a.gate_mode == kGateToken ? gate + row
-                   : a.gate_mode == kGateFull ? gate + base : gate;
-      float gt[1] = {1.0f};
-      if (a.gate_mode == kGateToken) load_vec<1>(g, gt);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = (i * TR + t) * VEC;
-        float gv[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) gv[j] = gt[0];
-        if (a.gate_mode >= kGateChannel && e < H) load_vec<VEC>(g + e, gv);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) v[i][j] = fmaf(v[i][j] * gv[j], a.scale, r[i][j]);
-        if (e < H) store_vec<VEC>(out + base + e, v[i]);
-      }
-      if (a.next_kind != kNormNone) {
-        norm_row<T, VEC, TR, NV>(v, a.next_kind, static_cast<const T*>(a.nw),
-                                 static_cast<const T*>(a.nb), H, a.eps, t, red, buf);
-        T* next = static_cast<T*>(a.next);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int e = (i * TR + t) * VEC;
-          if (e < H) store_vec<VEC>(next + base + e, v[i]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = (i * TR + t) * VEC;
-        if (e < H) store_vec<VEC>(out + base + e, v[i]);
-      }
-    }
+    if (a.next_kind == kNormNone) return;
+    if (kLate && nw != nullptr) rnw.load(nw, H, t);
+    if (kLate && nb != nullptr) rnb.load(nb, H, t);
+    norm_row<T, VEC, TR, NV>(v, a.next_kind, nw != nullptr, nb != nullptr, rnw, rnb, H, a.eps, t, red,
+                             buf);
   }
+  T* last = static_cast<T*>(RES ? a.next : a.out) + base;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    store_vec<VEC>(last + vec_start<VEC, TR, NV>(i, t, H), v[i], vec_skip<VEC, TR, NV>(i, t, H));
 }
 
 template <typename T, int VEC, int TR, int NV, bool RES>
 hipError_t run_norm(const NormArgs& a, hipStream_t s) {
   constexpr int RPB = TR < 256 ? 256 / TR : 1;
-  const int blocks = std::min((a.rows + RPB - 1) / RPB, 256 * 8);
-  hipLaunchKernelGGL((norm_kernel<T, VEC, TR, NV, RES>), dim3(blocks), dim3(TR < 256 ? 256 : TR), 0,
-                     s, a);
+  hipLaunchKernelGGL((norm_kernel<T, VEC, TR, NV, RES>), dim3((a.rows + RPB - 1) / RPB),
+                     dim3(TR < 256 ? 256 : TR), 0, s, a);
   return hipGetLastError();
 }
 
-// Vectors per thread: the smallest of 1, 2, 4, 8 that hold the row in TR
-// threads (H <= 16384: TR = 1024 holds it with 16 single elements).
-template <typename T, int VEC, int TR, bool RES>
-hipError_t run_norm_tr(const NormArgs& a, hipStream_t s) {
-  const int n = (a.H + VEC * TR - 1) / (VEC * TR);
-  if (n <= 1) return run_norm<T, VEC, TR, 1, RES>(a, s);
-  if (n <= 2) return run_norm<T, VEC, TR, 2, RES>(a, s);
-  if (n <= 4) return run_norm<T, VEC, TR, 4, RES>(a, s);
-  if (n <= 8) return run_norm<T, VEC, TR, 8, RES>(a, s);
-  if constexpr (VEC == 1) return run_norm<T, VEC, TR, 16, RES>(a, s);
-  return hipErrorInvalidValue;
-}
-
+// Threads per row: a wave up to 2 vectors a lane, 256 threads up to 4, else 1024
+// (16384 elements, the longest row, are 2048 vectors of 8 or 4096 of 4). Vectors per
+// thread: the fewest of 1, 2, 4 that hold the row.
 template <typename T, int VEC, bool RES>
 hipError_t run_norm_vec(const NormArgs& a, hipStream_t s) {
   const int vecs = (a.H + VEC - 1) / VEC;
-  if (vecs <= 64 * 2) return run_norm_tr<T, VEC, 64, RES>(a, s);
-  if constexpr (VEC < 8) {  // 16384 elements are 2048 vectors of 8
-    if (vecs > 256 * 8) return run_norm_tr<T, VEC, 1024, RES>(a, s);
+  if (vecs <= 64) return run_norm<T, VEC, 64, 1, RES>(a, s);
+  if constexpr (VEC > 1) {
+    if (vecs <= 64 * 2) return run_norm<T, VEC, 64, 2, RES>(a, s);
+    if (vecs <= 256) return run_norm<T, VEC, 256, 1, RES>(a, s);
+    if (vecs <= 256 * 2) return run_norm<T, VEC, 256, 2, RES>(a, s);
+    if (vecs <= 256 * 4) return run_norm<T, VEC, 256, 4, RES>(a, s);
+    if (vecs <= 1024 * 2) return run_norm<T, VEC, 1024, 2, RES>(a, s);
+    if constexpr (VEC == 4) {
+      if (vecs <= 1024 * 4) return run_norm<T, VEC, 1024, 4, RES>(a, s);
+    }
   }
-  return run_norm_tr<T, VEC, 256, RES>(a, s);
+  return hipErrorInvalidValue;
 }
 
 template <bool RES>
 hipError_t run_norm_dtype(const NormArgs& a, bool bf16, hipStream_t s) {
-  if (bf16)
-    return a.H % 8 == 0 ? run_norm_vec<uint16_t, 8, RES>(a, s) : run_norm_vec<uint16_t, 1, RES>(a, s);
-  return a.H % 4 == 0 ? run_norm_vec<float, 4, RES>(a, s) : run_norm_vec<float, 1, RES>(a, s);
+  if (bf16) return a.H >= 8 ? run_norm_vec<uint16_t, 8, RES>(a, s) : run_norm_vec<uint16_t, 1, RES>(a, s);
+  return a.H >= 4 ? run_norm_vec<float, 4, RES>(a, s) : run_norm_vec<float, 1, RES>(a, s);
 }
 
 }  // namespace

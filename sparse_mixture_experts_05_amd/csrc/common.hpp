@@ -107,6 +107,22 @@ __device__ __forceinline__ void lds_dma16(const void* g, void* lds_uniform) {
       : "memory");
 }
 
+// 16 x 16 product step on 16-byte fragments: lane l holds row l % 16 of each operand
+// at chunk l / 16 of a 64-byte run of K: 8 bf16 for one MFMA, or 4 fp32 whose element
+// j goes to the j-th of four (both operands in the same order of k). D: lane l holds
+// column l % 16 (row of b) and rows 4 (l / 16) .. + 3 (rows of a).
+template <typename T>
+__device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, f32x4_t c) {
+  if constexpr (sizeof(T) == 2) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[j]), __uint_as_float(b[j]), c, 0, 0, 0);
+    return c;
+  }
+}
+
 // Value of the partner lane of butterfly level L: xor 1, xor 2, the mirror
 // lane within 8, within 16 (DPP), xor 16 (ds_swizzle), xor 32 (bpermute).
 // Each level pairs two groups that the earlier levels already merged.

@@ -66,9 +66,10 @@ __device__ __forceinline__ void scan_segments(const LinArgs& a, SegScan& s) {
 // The tile of this workgroup, BM rows x bnc output columns. Tiles are numbered
 // segment by segment, column tile by column tile, row tile by row tile, and XCD
 // x (workgroups x, x + 8, ...) takes a contiguous run of them: the tiles that
-// share a weight panel run on one XCD at about one time. False: no work.
+// share a weight panel run on one XCD at about one time. M = 0: no work.
 template <int BM>
-__device__ __forceinline__ bool lin_tile(const LinArgs& a, int bnc, LinTile& t) {
+__device__ __forceinline__ LinTile lin_tile(const LinArgs& a, int bnc) {
+  LinTile t{};
   const int ntn = (a.N + bnc - 1) / bnc;
   const int g = blockIdx.x;
   if (a.offsets == nullptr) {
@@ -76,20 +77,21 @@ __device__ __forceinline__ bool lin_tile(const LinArgs& a, int bnc, LinTile& t) 
     const long long total = (long long)nm * ntn;
     const int chunk = (int)((total + 7) / 8);
     const long long q = (long long)(g & 7) * chunk + (g >> 3);
-    if ((g >> 3) >= chunk || q >= total) return false;
+    if ((g >> 3) >= chunk || q >= total) return t;
     t.e = 0;
     t.q = (int)q;
     t.row0 = t.q % nm * BM;
     t.n0 = t.q / nm * bnc;
-    t.M = min(BM, a.M - t.row0);
-    return true;
+    const int left = a.M - t.row0;
+    t.M = left < BM ? left : BM;
+    return t;
   }
   SegScan s;
   scan_segments<BM>(a, s);
   const long long total = (long long)s.total * ntn;
   const int chunk = (int)((total + 7) / 8);
   const long long q = (long long)(g & 7) * chunk + (g >> 3);
-  if ((g >> 3) >= chunk || q >= total) return false;
+  if ((g >> 3) >= chunk || q >= total) return t;
   const int lane = threadIdx.x & 63;
   int excl = s.incl;
 #pragma unroll
@@ -110,22 +112,23 @@ __device__ __forceinline__ bool lin_tile(const LinArgs& a, int bnc, LinTile& t) 
   t.e = e;
   t.q = (int)q;
   t.row0 = off + m * BM;
-  t.M = min(BM, cnt - m * BM);
+  const int left = cnt - m * BM;
+  t.M = left < BM ? left : BM;
   t.n0 = local / nb * bnc;
-  return true;
+  return t;
 }
 
-// ----------------------------------------------------------------- bf16 tiles
+// ----------------------------------------------------------------- 64 x 64 tiles
 
 // Tiles of 64 rows x 64 weight rows (64 output columns, or 32 of a gated
-// product) by 4 waves in a 2 x 2 grid. Operand rows are copied global -> LDS with
-// global_load_lds (8 rows of 128 bytes an instruction) into a ring of NS stages
-// of 64 k; 16-byte chunk c of row r sits at slot c ^ ((r >> 1) & 7), so the 16
-// lanes of a fragment read (16 consecutive rows, one chunk) touch 16 distinct
-// 4-bank groups. v_mfma_f32_16x16x32_bf16 takes the weights as A and the rows as
-// B: lane l ends with 4 consecutive weight rows of row l % 16 of x. In a gated
-// product the first half of a wave's weight sub-tiles holds gate rows, the second
-// the up rows of the same columns.
+// product) by 4 waves in a 2 x 2 grid, bf16 or fp32. Operand rows are copied
+// global -> LDS with global_load_lds (8 rows of 128 bytes an instruction) into a
+// ring of NS stages of 128 bytes of K; 16-byte chunk c of row r sits at slot
+// c ^ ((r >> 1) & 7), so the 16 lanes of a fragment read (16 consecutive rows, one
+// chunk) touch 16 distinct 4-bank groups. The weights are the MFMA's A and the rows
+// its B: lane l ends with 4 consecutive weight rows of row l % 16 of x. In a gated
+// product the first half of a wave's weight sub-tiles holds gate rows, the second the up rows
+// of the same columns.
 //
 // blockIdx.y of gridDim.y: a K slice. With several, a slice writes its
 // accumulators to a.part and lin_tile_reduce_kernel finishes the tile.
@@ -142,6 +145,7 @@ __device__ __forceinline__ int tile_col(int wn, int j, bool gt) {  // first colu
 }
 
 // Epilogue of a wave's accumulators, straight to memory.
+template <typename T>
 __device__ __forceinline__ void tile_store(const LinArgs& a, const LinTile& t,
                                            const f32x4_t (&acc)[Tile64::TM][Tile64::TN]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -155,7 +159,7 @@ __device__ __forceinline__ void tile_store(const LinArgs& a, const LinTile& t,
     for (int j = 0; j < Tile64::TN; ++j) {
       if (gt && j >= Tile64::TN / 2) continue;
       const int c = t.n0 + tile_col(wn, j, gt) + (lane >> 4) * 4;
-      if (c < a.N) store4(a, t.e, (size_t)(t.row0 + r), c, acc[i][j], acc[i][(j + Tile64::TN / 2) % Tile64::TN]);
+      if (c < a.N) store4<T>(a, t.e, (size_t)(t.row0 + r), c, acc[i][j], acc[i][(j + Tile64::TN / 2) % Tile64::TN]);
     }
   }
 }
@@ -167,32 +171,34 @@ __device__ __forceinline__ float* tile_part(const LinArgs& a, const LinTile& t, 
          ((size_t)(i * Tile64::TN + j) * kThreads + threadIdx.x) * 4;
 }
 
-__device__ __forceinline__ bool find(const LinArgs& a, LinTile& t) {
-  return lin_tile<Tile64::BM>(a, gated(a.act) ? Tile64::BN / 2 : Tile64::BN, t);
+__device__ __forceinline__ LinTile find(const LinArgs& a) {
+  return lin_tile<Tile64::BM>(a, gated(a.act) ? Tile64::BN / 2 : Tile64::BN);
 }
 
+template <typename T>
 __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
   constexpr int BM = Tile64::BM, BN = Tile64::BN, NS = Tile64::NS, STAGE = Tile64::STAGE, NI = Tile64::NI;
   constexpr int TM = Tile64::TM, TN = Tile64::TN;
   __shared__ __attribute__((aligned(16))) uint8_t smem[NS * STAGE];
-  LinTile t;
-  if (!find(a, t)) return;
+  const LinTile t = find(a);
+  if (t.M == 0) return;
   const bool gt = gated(a.act);
   const int N = a.N, K = a.K;
-  const uint16_t* x = static_cast<const uint16_t*>(a.x);
-  const uint16_t* w = static_cast<const uint16_t*>(a.w) + (size_t)t.e * (gt ? 2 : 1) * N * K;
+  const T* x = static_cast<const T*>(a.x);
+  const T* w = static_cast<const T*>(a.w) + (size_t)t.e * (gt ? 2 : 1) * N * K;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 1, wn = wave & 1;
-  const int KT0 = K / 64;
+  constexpr int BK = 128 / sizeof(T), EC = 16 / sizeof(T);  // elements of a stage, of a chunk
+  const int KT0 = K / BK;
   const int kbase = (int)((long long)blockIdx.y * KT0 / gridDim.y);
   const int KT = (int)((long long)(blockIdx.y + 1) * KT0 / gridDim.y) - kbase;
 
-  const uint16_t* src[NI];
+  const T* src[NI];
 #pragma unroll
   for (int q = 0; q < NI; ++q) {
     const int r = 8 * (wave * NI + q) + (lane >> 3);
     const int chunk = (lane & 7) ^ ((r >> 1) & 7);
-    const uint16_t* row;
+    const T* row;
     if (r < BM) {
       row = x + x_row(a, t.row0 + min(r, t.M - 1)) * K;  // rows past the end: its last
     } else {
@@ -201,12 +207,12 @@ __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
       const int c = t.n0 + tile_col(b / (BN / 2), j - half * (TN / 2), gt) + b % 16;
       row = w + ((size_t)half * N + min(c, N - 1)) * K;  // columns past the end: its last
     }
-    src[q] = row + kbase * 64 + chunk * 8;
+    src[q] = row + (size_t)kbase * BK + chunk * EC;
   }
   auto issue = [&](int kt) {
     uint8_t* base = smem + (kt % NS) * STAGE;
 #pragma unroll
-    for (int q = 0; q < NI; ++q) lds_dma16(src[q] + kt * 64, base + (wave * NI + q) * 1024);
+    for (int q = 0; q < NI; ++q) lds_dma16(src[q] + (size_t)kt * BK, base + (wave * NI + q) * 1024);
   };
   f32x4_t acc[TM][TN];
 #pragma unroll
@@ -238,13 +244,11 @@ __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wf[j]), as_bf16x8(xf[i]),
-                                                              acc[i][j], 0, 0, 0);
+        for (int j = 0; j < TN; ++j) acc[i][j] = mma16<T>(wf[j], xf[i], acc[i][j]);
     }
   }
   if (gridDim.y == 1) {
-    tile_store(a, t, acc);
+    tile_store<T>(a, t, acc);
     return;
   }
 #pragma unroll
@@ -260,9 +264,10 @@ __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
 // tiles still has many.
 constexpr int kMaxSlices = 16;
 
+template <typename T>
 __global__ __launch_bounds__(kThreads) void lin_tile_reduce_kernel(LinArgs a, int nks) {
-  LinTile t;
-  if (!find(a, t)) return;
+  const LinTile t = find(a);
+  if (t.M == 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const bool gt = gated(a.act);
   const int i = blockIdx.y;
@@ -285,7 +290,7 @@ __global__ __launch_bounds__(kThreads) void lin_tile_reduce_kernel(LinArgs a, in
   for (int j = 0; j < Tile64::TN; ++j) {
     if (gt && j >= Tile64::TN / 2) continue;
     const int c = t.n0 + tile_col(wave & 1, j, gt) + (lane >> 4) * 4;
-    if (c < a.N) store4(a, t.e, (size_t)(t.row0 + r), c, acc[j], acc[(j + Tile64::TN / 2) % Tile64::TN]);
+    if (c < a.N) store4<T>(a, t.e, (size_t)(t.row0 + r), c, acc[j], acc[(j + Tile64::TN / 2) % Tile64::TN]);
   }
 }
 
@@ -305,8 +310,8 @@ template <bool GT>
 __global__ __launch_bounds__(kThreads) void lin_rows_kernel(LinArgs a) {
   constexpr int KQ = 4, U = 4, H = GT ? 2 : 1;
   __shared__ f32x4_t red[KQ][H][64];
-  LinTile t;
-  if (!lin_tile<16>(a, 16, t)) return;
+  const LinTile t = lin_tile<16>(a, 16);
+  if (t.M == 0) return;
   const int N = a.N, K = a.K;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int S = K / 32;
@@ -371,77 +376,7 @@ __global__ __launch_bounds__(kThreads) void lin_rows_kernel(LinArgs a) {
 #pragma unroll
     for (int h = 0; h < H; ++h) acc[h] += red[q][h][lane];
   const int r = lane & 15;
-  if (r < t.M) store4(a, t.e, (size_t)(t.row0 + r), t.n0 + (lane >> 4) * 4, acc[0], acc[H - 1]);
-}
-
-// ----------------------------------------------------------------- fp32
-
-// Weight row of row r of a tile of interleaved gate and up rows whose first
-// output column is n0: rows 4q, 4q+1 are the gate rows of columns n0 + 2q,
-// n0 + 2q + 1 and rows 4q+2, 4q+3 their up rows, so the 4 consecutive rows of a
-// thread hold both factors of 2 outputs.
-__device__ __forceinline__ int gated_row(int r, int n0, int N) {
-  return ((r >> 1) & 1) * N + n0 + (r >> 2) * 2 + (r & 1);
-}
-
-// 64 x 64 tiles of plain FMA (small fp32 layers).
-__global__ __launch_bounds__(kThreads) void lin_f32_kernel(LinArgs a) {
-  constexpr int BM = 64, BN = 64, BK = 16;
-  __shared__ float As[BK][BM + 4];
-  __shared__ float Bs[BK][BN + 4];
-  const bool gt = gated(a.act);
-  LinTile t;
-  if (!lin_tile<BM>(a, gt ? BN / 2 : BN, t)) return;
-  const int N = a.N, K = a.K;
-  const float* w = static_cast<const float*>(a.w) + (size_t)t.e * (gt ? 2 : 1) * N * K;
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const int lr = tid >> 2, lk = (tid & 3) * 4;  // loader: row, first k of a float4
-  const float* ga = static_cast<const float*>(a.x) + x_row(a, t.row0 + min(lr, t.M - 1)) * K + lk;
-  const float* gb = w + (size_t)(gt ? gated_row(lr, t.n0, N) : t.n0 + lr) * K + lk;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += BK) {
-    const float4 va = *reinterpret_cast<const float4*>(ga + k0);
-    const float4 vb = *reinterpret_cast<const float4*>(gb + k0);
-    As[lk + 0][lr] = va.x, As[lk + 1][lr] = va.y, As[lk + 2][lr] = va.z, As[lk + 3][lr] = va.w;
-    Bs[lk + 0][lr] = vb.x, Bs[lk + 1][lr] = vb.y, Bs[lk + 2][lr] = vb.z, Bs[lk + 3][lr] = vb.w;
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < BK; ++kk) {
-      float fa[4], fb[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) fa[i] = As[kk][ty * 4 + i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) fb[j] = Bs[kk][tx * 4 + j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(fa[i], fb[j], acc[i][j]);
-    }
-    __syncthreads();
-  }
-  const float* bias = a.bias == nullptr ? nullptr
-                          : static_cast<const float*>(a.bias) + (size_t)t.e * (gt ? 2 : 1) * N;
-  const float* res = static_cast<const float*>(a.res);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (ty * 4 + i >= t.M) continue;
-    const size_t row = (size_t)(t.row0 + ty * 4 + i) * N;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (gt && j >= 2) continue;
-      const int c = t.n0 + (gt ? tx * 2 : tx * 4) + j;
-      float g = acc[i][j];
-      if (bias != nullptr) g += bias[c];
-      float o = activate<false>(a.act, g);
-      if (gt) {
-        float u = acc[i][j ^ 2];
-        if (bias != nullptr) u += bias[N + c];
-        o *= u;
-      }
-      if (res != nullptr) o += res[row + c];
-      static_cast<float*>(a.y)[row + c] = o;
-    }
-  }
+  if (r < t.M) store4<uint16_t>(a, t.e, (size_t)(t.row0 + r), t.n0 + (lane >> 4) * 4, acc[0], acc[H - 1]);
 }
 
 // ----------------------------------------------------------------- host side
@@ -464,6 +399,15 @@ struct LinPlan {
 };
 
 bool host_gated(int act) { return act == kActGeglu || act == kActSwiglu; }
+
+// K slices of an fp32 product, which always takes the 64 x 64 tiles: as many as fill
+// the chip with about two workgroups a CU and leave each 8 stages or more.
+int f32_slices(const LinArgs& a) {
+  const double tiles = (double)lin_tiles(a, 64, host_gated(a.act) ? 32 : 64);
+  int nks = 1;
+  while (nks < kMaxSlices && tiles * nks * 2 <= 512 && a.K / 32 >= 16 * nks) nks *= 2;
+  return nks;
+}
 
 // Path of a bf16 product: the least of the four paths' estimated times, in us. The
 // estimates hold what was measured (graph replay, no act; M x N x K dense, then E
@@ -535,13 +479,14 @@ size_t tile_ws_bytes(const LinArgs& a, int nks) {
          Tile64::BN * sizeof(float);
 }
 
+template <typename T>
 hipError_t run_tile(LinArgs a, int nks, void* ws, hipStream_t s) {
   const unsigned grid = lin_grid(a, Tile64::BM, host_gated(a.act) ? Tile64::BN / 2 : Tile64::BN);
   a.part = static_cast<float*>(ws);
-  hipLaunchKernelGGL((lin_tile_kernel), dim3(grid, nks), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((lin_tile_kernel<T>), dim3(grid, nks), dim3(kThreads), 0, s, a);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || nks <= 1) return err;
-  hipLaunchKernelGGL((lin_tile_reduce_kernel), dim3(grid, Tile64::TM), dim3(kThreads), 0, s, a, nks);
+  hipLaunchKernelGGL((lin_tile_reduce_kernel<T>), dim3(grid, Tile64::TM), dim3(kThreads), 0, s, a, nks);
   return hipGetLastError();
 }
 
@@ -561,9 +506,9 @@ bool linear_fits(int E, int M, int N, int K) {
 }
 
 size_t linear_ws_bytes(int E, int M, int N, int K, int act, bool grouped, bool bf16) {
-  if (!bf16) return 0;
   const int32_t some = 0;
   const LinArgs a = lin_args(nullptr, nullptr, 1, M, grouped ? &some : nullptr, E, M, N, K, act);
+  if (!bf16) return tile_ws_bytes(a, f32_slices(a));
   const LinPlan p = lin_plan(a);
   if (p.path >= kBigHalf) return big_ws_bytes(a, p.path == kBigHalf);
   return p.path == kTile64 ? tile_ws_bytes(a, p.nks) : 0;
@@ -576,10 +521,7 @@ hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
   LinArgs a = lin_args(x, gather, gk, gT, offsets, E, M, N, K, act);
   a.w = w, a.bias = bias, a.res = res, a.y = y;
   const bool gt = host_gated(act);
-  if (!bf16) {
-    hipLaunchKernelGGL(lin_f32_kernel, dim3(lin_grid(a, 64, gt ? 32 : 64)), dim3(kThreads), 0, s, a);
-    return hipGetLastError();
-  }
+  if (!bf16) return run_tile<float>(a, f32_slices(a), ws, s);
   LinPlan p = lin_plan(a);
   // gathered rows past the large tiles' 32-bit offsets: no workspace needed either
   if (p.path >= kBigHalf && gather && !big_gather_ok(a)) p = LinPlan{kTile64, 1};
@@ -590,7 +532,7 @@ hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
       else hipLaunchKernelGGL((lin_rows_kernel<false>), grid, dim3(kThreads), 0, s, a);
       return hipGetLastError();
     }
-    case kTile64: return run_tile(a, p.nks, ws, s);
+    case kTile64: return run_tile<uint16_t>(a, p.nks, ws, s);
     default: return launch_big(a, p.path == kBigHalf, ws, s);
   }
 }

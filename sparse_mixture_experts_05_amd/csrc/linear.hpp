@@ -54,37 +54,50 @@ __device__ __forceinline__ Out4 widen4(uint2 q) {
                bf16_to_f32(q.y & 0xffffu), __uint_as_float(q.y & 0xffff0000u)}};
 }
 
-// act(g + bg) [* (u + bu)] [+ res] of 4 columns, packed to bf16 (no bias: zeros).
-__device__ __forceinline__ uint2 finish4(int act, const f32x4_t& g, const f32x4_t& u,
-                                         const Out4& bg, const Out4& bu, bool has_res,
-                                         const Out4& res) {
-  float o[4];
+// act(g + bg) [* (u + bu)] [+ res] of 4 columns (no bias: zeros).
+template <bool BF16>
+__device__ __forceinline__ Out4 finish4(int act, const f32x4_t& g, const f32x4_t& u, const Out4& bg,
+                                        const Out4& bu, bool has_res, const Out4& res) {
+  Out4 o;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    float x = activate<true>(act, g[c] + bg.v[c]);
+    float x = activate<BF16>(act, g[c] + bg.v[c]);
     if (gated(act)) x *= u[c] + bu.v[c];
     if (has_res) x += res.v[c];
-    o[c] = x;
+    o.v[c] = x;
   }
-  return make_uint2(cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3]));
+  return o;
+}
+__device__ __forceinline__ uint2 pack4(const Out4& o) {
+  return make_uint2(cvt_bf16x2(o.v[0], o.v[1]), cvt_bf16x2(o.v[2], o.v[3]));
+}
+
+// 4 elements of T at p.
+__device__ __forceinline__ Out4 load4(const uint16_t* p) { return widen4(*reinterpret_cast<const uint2*>(p)); }
+__device__ __forceinline__ Out4 load4(const float* p) {
+  const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p);
+  return Out4{{v[0], v[1], v[2], v[3]}};
 }
 
 // Bias and residual of the 4 columns c .. c + 3 of buffer row `row`, then finish4
 // and the store. e: the row's expert.
+template <typename T>
 __device__ __forceinline__ void store4(const LinArgs& a, int e, size_t row, int c,
                                        const f32x4_t& g, const f32x4_t& u) {
+  constexpr bool BF16 = sizeof(T) == 2;
   const bool gt = gated(a.act);
   Out4 bg{}, bu{}, rv{};
   if (a.bias != nullptr) {
-    const uint16_t* b = static_cast<const uint16_t*>(a.bias) + (size_t)e * (gt ? 2 : 1) * a.N + c;
-    bg = widen4(*reinterpret_cast<const uint2*>(b));
-    if (gt) bu = widen4(*reinterpret_cast<const uint2*>(b + a.N));
+    const T* b = static_cast<const T*>(a.bias) + (size_t)e * (gt ? 2 : 1) * a.N + c;
+    bg = load4(b);
+    if (gt) bu = load4(b + a.N);
   }
   const size_t at = row * a.N + c;
-  if (a.res != nullptr)
-    rv = widen4(*reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.res) + at));
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
-      finish4(a.act, g, u, bg, bu, a.res != nullptr, rv);
+  if (a.res != nullptr) rv = load4(static_cast<const T*>(a.res) + at);
+  const Out4 o = finish4<BF16>(a.act, g, u, bg, bu, a.res != nullptr, rv);
+  T* y = static_cast<T*>(a.y) + at;
+  if constexpr (BF16) *reinterpret_cast<uint2*>(y) = pack4(o);
+  else *reinterpret_cast<f32x4_t*>(y) = f32x4_t{o.v[0], o.v[1], o.v[2], o.v[3]};
 }
 
 // Big-tile path (linear_big.hip): 256 rows x 256 weight rows, or half as many

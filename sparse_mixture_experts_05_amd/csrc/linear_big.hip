@@ -400,9 +400,9 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
       if constexpr (GT) asm volatile("" : "+a"(acc[i][j + SN / 2]));
       const f32x16_t& g = acc[i][j];
       const f32x16_t& u = acc[i][GT ? j + SN / 2 : j];
-      const uint2 o = finish4(ACT, f32x4_t{g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]},
+      const uint2 o = pack4(finish4<true>(ACT, f32x4_t{g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]},
                                    f32x4_t{u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]},
-                                   bg, bu, RES, rv[i]);
+                                   bg, bu, RES, rv[i]));
       const int row = lr + i * 32;
       *reinterpret_cast<uint2*>(smem + row * CROWB + (((col >> 3) ^ (row & SWZ)) << 4) + khalf * 8) = o;
     }
@@ -463,7 +463,7 @@ __global__ __launch_bounds__(kThreads) void lin_reduce_kernel(LinArgs a) {
         g += vg[ks];
         if constexpr (GT) u += vu[ks];
       }
-    store4(a, t.e, (size_t)(t.row0 + row), n0 + col, g, u);
+    store4<uint16_t>(a, t.e, (size_t)(t.row0 + row), n0 + col, g, u);
   }
 }
 

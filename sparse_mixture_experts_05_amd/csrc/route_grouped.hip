@@ -37,18 +37,14 @@ struct GroupArgs {
 
 __device__ __forceinline__ float sigmoidf(float s) { return 1.0f / (1.0f + expf(-s)); }
 
-// LDS of the group stage of BT tokens, behind the score tile.
-template <int BT>
-struct GroupLds {
-  float gs[BT][kMaxGroups];        // group scores
-  unsigned long long mask[BT];     // chosen groups
-  float top[BT], rz[BT];           // softmax: largest score, 1 / sum
-};
+// exp by the hardware's exp2 (relative error about |x| * 6e-8 and an ulp): the choice
+// evaluates all E experts of a token, and its values carry the scores' own error of
+// that size. The k weights take expf.
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
-// Value that the choice is made on: v, or with no bias at all the score.
-// NaN and -inf leave the expert off.
-__device__ __forceinline__ float prob_of(const GroupArgs& a, float s, float top, float rz) {
-  return a.softmax ? expf(s - top) * rz : sigmoidf(s);
+// p of a score: sigmoid, or softmax with the largest score and 1 / sum.
+__device__ __forceinline__ float prob_fast(const GroupArgs& a, float s, float top, float rz) {
+  return a.softmax ? exp_fast(s - top) * rz : __builtin_amdgcn_rcpf(1.0f + exp_fast(-s));
 }
 
 template <int L, int G>
@@ -57,12 +53,27 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
+// LDS writes of this wave are seen by its later reads (the LDS serves a wave in order;
+// this keeps the compiler from moving them).
+__device__ __forceinline__ void wave_lds_fence() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// LDS of the group stage of BT tokens: the values v and the group scores.
+template <int BT, int NW>
+struct GroupLds {
+  float v[BT * tile_stride<BT, NW>()];
+  float gs[BT][kMaxGroups + 1];
+};
+
 // Chooses for the BT tokens whose scores are in the LDS tile sc (row stride
-// tile_stride<BT, NW>(), no bias in them). Lanes as in topk_tokens: G = 64 *
-// NW / BT lanes a token, lane g reads the experts g, g + G, ...
+// tile_stride<BT, NW>(), no bias in them). Lanes as in topk_tokens: G = 64 * NW / BT
+// lanes a token, all in one wave, so nothing here needs a barrier; lane g has the
+// experts g, g + G, ... A token's time is instructions: its E values p + b are worked
+// out once, by the hardware's exp2 and reciprocal, and kept in LDS for the group
+// scores (one lane a group reads its group). Work on scores in place of values, and a
+// workgroup's barriers between the stages, took 31 us for 4096 tokens of 256 experts.
 template <int BT, int KP, int EPX, int NW>
-__device__ __forceinline__ void grouped_tokens(float* sc, GroupLds<BT>& L, const GroupArgs& a,
-                                               int t0, int T, int E, int k,
+__device__ __forceinline__ void grouped_tokens(const float* sc, GroupLds<BT, NW>& L,
+                                               const GroupArgs& a, int t0, int T, int E, int k,
                                                int32_t* __restrict__ topk_idx,
                                                float* __restrict__ topk_w) {
   constexpr int NT = NW * 64, G = NT / BT, S = tile_stride<BT, NW>();
@@ -74,58 +85,72 @@ __device__ __forceinline__ void grouped_tokens(float* sc, GroupLds<BT>& L, const
   const float* row = sc + t * S;
   const bool limit = a.topk_groups < a.groups;
 
+  float x[NBLK * KP];  // scores, then the keys' values
+#pragma unroll
+  for (int i = 0; i < NBLK * KP; ++i) x[i] = i < NSUB ? row[min(g + G * i, E - 1)] : 0.0f;
   float top = 0.0f, rz = 1.0f;
   if (a.softmax) {
     float m = -INFINITY, z = 0.0f;
-    for (int e = g; e < E; e += G) m = fmaxf(m, row[e]);  // fmaxf drops a NaN
+#pragma unroll
+    for (int i = 0; i < NSUB; ++i) m = fmaxf(m, x[i]);  // fmaxf drops a NaN
     top = group_max<0, G>(m);
-    for (int e = g; e < E; e += G) {
-      const float d = row[e] - top;
-      z += d == d ? expf(d) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NSUB; ++i) {
+      const float d = x[i] - top;
+      z += d == d && g + G * i < E ? exp_fast(d) : 0.0f;
     }
     rz = 1.0f / group_sum<0, G>(z);
-    if (g == 0) {
-      L.top[t] = top;
-      L.rz[t] = rz;
+  }
+  if (a.bias != nullptr || limit) {
+#pragma unroll
+    for (int i = 0; i < NSUB; ++i) {
+      const int e = g + G * i, ec = min(e, E - 1);
+      float v = prob_fast(a, x[i], top, rz);
+      if (a.bias != nullptr) v += a.bias[ec];
+      if (limit && e < E) L.v[t * S + e] = v;
+      if (a.bias != nullptr) x[i] = v;
     }
   }
+  unsigned long long mask = ~0ull;
   if (limit) {
-    if (g == 0) L.mask[t] = 0;
-    __syncthreads();
-    // one thread per (token, group); each starts at another expert of its
-    // group, which spreads the LDS banks when groups are a power of two wide
-    for (int q = threadIdx.x; q < BT * a.groups; q += NT) {
-      const int qt = q / a.groups, qg = q - qt * a.groups;
-      const float* r = sc + qt * S + qg * a.per;
-      const float* b = a.bias != nullptr ? a.bias + qg * a.per : nullptr;
-      const float tm = a.softmax ? L.top[qt] : 0.0f, z = a.softmax ? L.rz[qt] : 1.0f;
-      float b1 = -INFINITY, b2 = -INFINITY;
-      int i = qg % a.per;
-      for (int n = 0; n < a.per; ++n) {
-        float v = prob_of(a, r[i], tm, z);
-        if (b != nullptr) v += b[i];
-        v = fmaxf(v, -INFINITY);
-        b2 = fmaxf(b2, fminf(b1, v));
-        b1 = fmaxf(b1, v);
-        i = i + 1 == a.per ? 0 : i + 1;
+    wave_lds_fence();
+    // one lane a group; each starts at another expert of its group, which spreads the
+    // LDS banks when groups are a power of two wide
+    for (int gb = 0; gb < a.groups; gb += G) {
+      const int q = gb + g;
+      if (q < a.groups) {
+        const float* r = L.v + t * S + q * a.per;
+        float b1 = -INFINITY, b2 = -INFINITY;
+        int i = q % a.per;
+        for (int n = 0; n < a.per; ++n) {
+          const float v = fmaxf(r[i], -INFINITY);
+          b2 = fmaxf(b2, fminf(b1, v));
+          b1 = fmaxf(b1, v);
+          i = i + 1 == a.per ? 0 : i + 1;
+        }
+        // the second counts only if it is on
+        L.gs[t][q] = a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
       }
-      // the second counts only if it is on
-      L.gs[qt][qg] = a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
     }
-    __syncthreads();
-    for (int q = threadIdx.x; q < BT * a.groups; q += NT) {
-      const int qt = q / a.groups, qg = q - qt * a.groups;
-      const float own = L.gs[qt][qg];
-      int rank = 0;
-      for (int o = 0; o < a.groups; ++o) {
-        const float v = L.gs[qt][o];
-        rank += v > own || (v == own && o < qg);
+    wave_lds_fence();
+    mask = 0;
+    for (int gb = 0; gb < a.groups; gb += G) {
+      const int q = gb + g;
+      bool in = false;
+      if (q < a.groups) {
+        const float own = L.gs[t][q];
+        int rank = 0;
+        for (int o = 0; o < a.groups; ++o) {
+          const float v = L.gs[t][o];
+          rank += v > own || (v == own && o < q);
+        }
+        in = rank < a.topk_groups;
       }
-      if (rank < a.topk_groups) atomicOr(&L.mask[qt], 1ull << qg);
+      unsigned long long bits = __ballot(in);
+      if constexpr (G < 64) bits = (bits >> ((threadIdx.x & 63) / G * G)) & ((1ull << (G & 63)) - 1);
+      mask |= bits << gb;
     }
-    __syncthreads();
   }
-  const unsigned long long mask = limit ? L.mask[t] : ~0ull;
 
   uint64_t list[KP];
 #pragma unroll
@@ -134,11 +159,8 @@ __device__ __forceinline__ void grouped_tokens(float* sc, GroupLds<BT>& L, const
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
       const int e = g + G * (b * KP + i);
-      const int ec = min(e, E - 1);
-      float v = row[ec];
-      if (a.bias != nullptr) v = prob_of(a, v, top, rz) + a.bias[ec];
-      const bool in = e < E && ((mask >> ((ec * a.magic) >> 16)) & 1);
-      blk[i] = topk_key(v, e) & (uint64_t)(-(int64_t)in);
+      const bool in = e < E && ((mask >> ((min(e, E - 1) * a.magic) >> 16)) & 1);
+      blk[i] = topk_key(x[b * KP + i], e) & (uint64_t)(-(int64_t)in);
     }
     bitonic_sort<KP>(blk);
     if (b == 0) {
@@ -167,9 +189,9 @@ __device__ __forceinline__ void grouped_tokens(float* sc, GroupLds<BT>& L, const
   for (int j = 0; j < KP; ++j) {
     p[j] = 0.0f;
     if (j < k && sj[j] > -INFINITY) {
-      if (!a.renorm) p[j] = prob_of(a, sj[j], top, rz);
-      else if (a.softmax) p[j] = expf(sj[j] - m);
-      else p[j] = sj[j] > 0.0f ? sigmoidf(sj[j]) : expf(sj[j] - m) / (1.0f + expf(sj[j]));
+      if (a.softmax) p[j] = a.renorm ? expf(sj[j] - m) : expf(sj[j] - top) * rz;
+      else if (!a.renorm || sj[j] > 0.0f) p[j] = sigmoidf(sj[j]);
+      else p[j] = expf(sj[j] - m) / (1.0f + expf(sj[j]));
     }
     sum += p[j];
   }
@@ -185,8 +207,8 @@ __device__ __forceinline__ void grouped_tokens(float* sc, GroupLds<BT>& L, const
 }
 
 template <int BT, int EPX, int NW = 4>
-__device__ __forceinline__ void grouped_phase(float* sc, GroupLds<BT>& L, const GroupArgs& a,
-                                              int t0, int T, int E, int k,
+__device__ __forceinline__ void grouped_phase(const float* sc, GroupLds<BT, NW>& L,
+                                              const GroupArgs& a, int t0, int T, int E, int k,
                                               int32_t* __restrict__ idx, float* __restrict__ w) {
   if (k <= 1) grouped_tokens<BT, 1, EPX, NW>(sc, L, a, t0, T, E, k, idx, w);
   else if (k <= 2) grouped_tokens<BT, 2, EPX, NW>(sc, L, a, t0, T, E, k, idx, w);
@@ -200,7 +222,7 @@ __global__ __launch_bounds__(NW * 64) void grouped_bf16_kernel(
     const uint16_t* __restrict__ x, const uint16_t* __restrict__ wg, GroupArgs a, int T, int H,
     int E, int k, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
   using C = RouteTile<BT, EP, NW>;
-  constexpr int NEED = C::SC_BYTES + (int)sizeof(GroupLds<BT>);
+  constexpr int NEED = C::SC_BYTES + (int)sizeof(GroupLds<BT, NW>);
   constexpr int LDS = C::LDS > NEED ? C::LDS : NEED;
   static_assert(LDS <= 160 * 1024 && C::SC_BYTES % 8 == 0, "score tile and group stage in LDS");
   __shared__ __align__(16) uint8_t smem[LDS];
@@ -209,7 +231,7 @@ __global__ __launch_bounds__(NW * 64) void grouped_bf16_kernel(
   score_tile<BT, EP, NW>(smem, x, wg, t0, T, 0, E, H, 0, H / 64, acc);
   scores_to_lds<BT, EP, NW>(smem, E, nullptr, acc);
   grouped_phase<BT, EP, NW>(reinterpret_cast<float*>(smem),
-                            *reinterpret_cast<GroupLds<BT>*>(smem + C::SC_BYTES), a, t0, T, E, k,
+                            *reinterpret_cast<GroupLds<BT, NW>*>(smem + C::SC_BYTES), a, t0, T, E, k,
                             topk_idx, topk_w);
 }
 
@@ -220,62 +242,32 @@ __global__ __launch_bounds__(kThreads) void grouped_select_kernel(const float* _
                                                                   GroupArgs a, int T, int E, int k,
                                                                   int32_t* __restrict__ topk_idx,
                                                                   float* __restrict__ topk_w) {
-  constexpr int S = tile_stride<BT>();
+  constexpr int S = tile_stride<BT>(), G = kThreads / BT, NSUB = (EPX + G - 1) / G;
   __shared__ float sc[BT * S];
-  __shared__ GroupLds<BT> L;
+  __shared__ GroupLds<BT, 4> L;
   const int t0 = blockIdx.x * BT;
-  // about 32 loads in flight per thread, from addresses clamped into the buffer
-  constexpr int PER = NKS >= 8 ? 32 / NKS : 8;
-  const int nval = min(BT, T - t0) * E;
-  for (int p0 = threadIdx.x; p0 < nval; p0 += PER * kThreads) {
+  // each lane sums the experts that it will choose from; about 32 loads in flight, from
+  // addresses clamped into the buffer
+  constexpr int PER = NKS >= 16 ? 2 : 32 / NKS < NSUB ? 32 / NKS : NSUB;
+  const int t = threadIdx.x / G, g = threadIdx.x % G;
+  const float* src = ws + (size_t)min(t0 + t, T - 1) * E;
+#pragma unroll
+  for (int i0 = 0; i0 < NSUB; i0 += PER) {
     float v[PER][NKS];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int p = p0 + i * kThreads;
-      const int tt = min(t0 + p / E, T - 1), e = p % E;
+    for (int i = 0; i < PER; ++i)
 #pragma unroll
-      for (int q = 0; q < NKS; ++q) v[i][q] = ws[((size_t)q * T + tt) * E + e];
-    }
+      for (int q = 0; q < NKS; ++q) v[i][q] = src[(size_t)q * T * E + min(g + G * (i0 + i), E - 1)];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int p = p0 + i * kThreads;
-      if (p < nval) {
-        float s = 0.0f;
+      float s = 0.0f;
 #pragma unroll
-        for (int q = 0; q < NKS; ++q) s += v[i][q];
-        sc[p / E * S + p % E] = s;
-      }
+      for (int q = 0; q < NKS; ++q) s += v[i][q];
+      if (g + G * (i0 + i) < E) sc[t * S + g + G * (i0 + i)] = s;
     }
   }
-  __syncthreads();
+  wave_lds_fence();
   grouped_phase<BT, EPX>(sc, L, a, t0, T, E, k, topk_idx, topk_w);
-}
-
-// fp32 scores with plain dot products (small fp32 layers).
-__global__ __launch_bounds__(kThreads) void grouped_f32_kernel(
-    const float* __restrict__ x, const float* __restrict__ wg, GroupArgs a, int T, int H, int E,
-    int k, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
-  constexpr int BT = 16;
-  constexpr int S = tile_stride<BT>();
-  __shared__ float sc[BT * S];
-  __shared__ GroupLds<BT> L;
-  const int t0 = blockIdx.x * BT;
-  for (int p = threadIdx.x; p < BT * E; p += kThreads) {
-    const int t = p / E, e = p % E;
-    const float4* xr = reinterpret_cast<const float4*>(x + (size_t)min(t0 + t, T - 1) * H);
-    const float4* wr = reinterpret_cast<const float4*>(wg + (size_t)e * H);
-    float s = 0.0f;
-    for (int h = 0; h < H / 4; ++h) {
-      const float4 u = xr[h], b = wr[h];
-      s = fmaf(u.x, b.x, s);
-      s = fmaf(u.y, b.y, s);
-      s = fmaf(u.z, b.z, s);
-      s = fmaf(u.w, b.w, s);
-    }
-    sc[t * S + e] = s;
-  }
-  __syncthreads();
-  grouped_phase<BT, kMaxE>(sc, L, a, t0, T, E, k, topk_idx, topk_w);
 }
 
 template <int BT, int EPX>
@@ -320,10 +312,40 @@ hipError_t launch_bf16_bt(const void* x, const void* wg, const GroupArgs& a, int
   return launch_bf16<BT, 256, route_waves<BT, 256>()>(x, wg, a, T, H, E, k, idx, w, s);
 }
 
+// fp32 scores always take two launches: 16 x 64 tiles for few tokens, else 64 x 128.
+// bf16 calls take the paths of moe_route.
+bool f32_big(int T) { return T >= 512; }
+
+// K slices of the fp32 paths: a power of two that divides the panels (32 k), about 512
+// workgroups, at least 4 panels each.
+int f32_kslices(int T, int H, int E) {
+  const bool big = f32_big(T);
+  const int tiles = big ? ((T + 63) / 64) * ((E + 127) / 128) : ((T + 15) / 16) * ((E + 63) / 64);
+  int ks = 1;
+  while (ks * 2 * tiles <= 512 && (H / 32) % (ks * 8) == 0 && ks * 2 <= kMaxSlices) ks *= 2;
+  return ks;
+}
+
+hipError_t launch_partial_f32(const void* x, const void* wg, int T, int H, int E, float* sp,
+                              hipStream_t s) {
+  const int nks = f32_kslices(T, H, E), kps = H / 32 / nks;
+  const float* xp = static_cast<const float*>(x);
+  const float* wp = static_cast<const float*>(wg);
+  if (f32_big(T))
+    hipLaunchKernelGGL((route_partial_kernel<64, 128, 4, float>), dim3((T + 63) / 64, (E + 127) / 128, nks),
+                       dim3(256), 0, s, xp, wp, T, H, E, kps, sp);
+  else
+    hipLaunchKernelGGL((route_partial_kernel<kPartBT, kPartEP, 4, float>),
+                       dim3((T + kPartBT - 1) / kPartBT, (E + kPartEP - 1) / kPartEP, nks), dim3(256), 0,
+                       s, xp, wp, T, H, E, kps, sp);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 size_t route_grouped_ws_bytes(int T, int H, int E, bool bf16) {
-  return scores_ws_bytes(T, H, E, bf16);
+  return bf16 ? scores_ws_bytes(T, H, E, true)
+              : align256((size_t)f32_kslices(T, H, E) * T * E * sizeof(float));
 }
 
 hipError_t launch_route_grouped(const void* x, const void* wg, const float* bias, int T, int H,
@@ -340,20 +362,15 @@ hipError_t launch_route_grouped(const void* x, const void* wg, const float* bias
   a.softmax = softmax;
   a.renorm = renorm;
   a.scale = scale;
-  if (route_mode(T, E, bf16) != kOneLaunch) {
-    const int nks = route_kslices(T, H, E);
-    const hipError_t err = launch_partial(x, wg, T, H, E, static_cast<float*>(ws), s);
+  if (!bf16 || route_mode(T, E, true) != kOneLaunch) {
+    float* sp = static_cast<float*>(ws);
+    const int nks = bf16 ? route_kslices(T, H, E) : f32_kslices(T, H, E);
+    const hipError_t err = bf16 ? launch_partial(x, wg, T, H, E, sp, s)
+                                : launch_partial_f32(x, wg, T, H, E, sp, s);
     if (err != hipSuccess) return err;
-    const float* wsf = static_cast<const float*>(ws);
     return select_tokens_per_block(T) == 16
-               ? launch_select<16>(nks, wsf, a, T, E, k, topk_idx, topk_w, s)
-               : launch_select<4>(nks, wsf, a, T, E, k, topk_idx, topk_w, s);
-  }
-  if (!bf16) {
-    hipLaunchKernelGGL(grouped_f32_kernel, dim3((T + 15) / 16), dim3(kThreads), 0, s,
-                       static_cast<const float*>(x), static_cast<const float*>(wg), a, T, H, E, k,
-                       topk_idx, topk_w);
-    return hipGetLastError();
+               ? launch_select<16>(nks, sp, a, T, E, k, topk_idx, topk_w, s)
+               : launch_select<4>(nks, sp, a, T, E, k, topk_idx, topk_w, s);
   }
   switch (bf16_tokens_per_block(T)) {
     case 64: return launch_bf16_bt<64>(x, wg, a, T, H, E, k, topk_idx, topk_w, s);

@@ -140,11 +140,12 @@ struct RouteTile {
   static_assert(LDS <= 160 * 1024, "LDS budget");
 };
 
-// The K loop of one tile; returns with every wave's accumulators complete and
+// The K loop of one tile (T: bf16 bits or fp32; a panel is 128 bytes of a row, the
+// K range in panels); returns with every wave's accumulators complete and
 // the LDS free for reuse (after a barrier).
-template <int BT, int EP, int NW = 4>
-__device__ __forceinline__ void score_tile(uint8_t* smem, const uint16_t* __restrict__ x,
-                                           const uint16_t* __restrict__ wg, int t0, int T, int e0,
+template <int BT, int EP, int NW = 4, typename T_ = uint16_t>
+__device__ __forceinline__ void score_tile(uint8_t* smem, const T_* __restrict__ x,
+                                           const T_* __restrict__ wg, int t0, int T, int e0,
                                            int E, int H, int kp0, int kp1,
                                            f32x4_t (&acc)[RouteTile<BT, EP, NW>::MC][RouteTile<BT, EP, NW>::NC]) {
   using C = RouteTile<BT, EP, NW>;
@@ -152,7 +153,7 @@ __device__ __forceinline__ void score_tile(uint8_t* smem, const uint16_t* __rest
   const int NST = (kp1 - kp0 + C::PPS - 1) / C::PPS;  // stages
 
   // DMA plan of this lane: instruction q copies rows [8g, 8g+8) of panel pq[q].
-  const uint16_t* src[C::NI];
+  const T_* src[C::NI];
   int pq[C::NI], dst[C::NI];
 #pragma unroll
   for (int q = 0; q < C::NI; ++q) {
@@ -160,9 +161,9 @@ __device__ __forceinline__ void score_tile(uint8_t* smem, const uint16_t* __rest
     const int p = j / (C::R / 8), g = j % (C::R / 8);
     const int r = 8 * g + (lane >> 3);
     const int chunk = (lane & 7) ^ ((r >> 1) & 7);
-    const uint16_t* row = r < BT ? x + (size_t)min(t0 + r, T - 1) * H
+    const T_* row = r < BT ? x + (size_t)min(t0 + r, T - 1) * H
                                  : wg + (size_t)min(e0 + r - BT, E - 1) * H;
-    src[q] = row + chunk * 8;
+    src[q] = row + chunk * (int)(16 / sizeof(T_));
     pq[q] = p;
     dst[q] = p * C::PB + g * 1024;
   }
@@ -170,7 +171,7 @@ __device__ __forceinline__ void score_tile(uint8_t* smem, const uint16_t* __rest
     uint8_t* base = smem + (st % C::NS) * C::SB;
 #pragma unroll
     for (int q = 0; q < C::NI; ++q)
-      lds_dma16(src[q] + (size_t)min(kp0 + st * C::PPS + pq[q], kp1 - 1) * 64, base + dst[q]);
+      lds_dma16(src[q] + (size_t)min(kp0 + st * C::PPS + pq[q], kp1 - 1) * (128 / sizeof(T_)), base + dst[q]);
   };
 
 #pragma unroll
@@ -211,8 +212,7 @@ __device__ __forceinline__ void score_tile(uint8_t* smem, const uint16_t* __rest
         for (int m = 0; m < C::MC; ++m)
 #pragma unroll
           for (int n = 0; n < C::NC; ++n)
-            acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[m]), as_bf16x8(b[n]),
-                                                                acc[m][n], 0, 0, 0);
+            acc[m][n] = mma16<T_>(a[m], b[n], acc[m][n]);
       }
     }
   }
@@ -270,9 +270,9 @@ __device__ __forceinline__ void scores_to_lds(uint8_t* smem, int ncol, const flo
 // block, K slice) stores its BT x EP tile to ws[ks][t][e] (no bias).
 constexpr int kPartBT = 16, kPartEP = 64, kMaxSlices = 16;
 
-template <int BT, int EP, int NW = 4>
-__global__ __launch_bounds__(NW * 64) void route_partial_kernel(const uint16_t* __restrict__ x,
-                                                                const uint16_t* __restrict__ wg,
+template <int BT, int EP, int NW = 4, typename T_ = uint16_t>
+__global__ __launch_bounds__(NW * 64) void route_partial_kernel(const T_* __restrict__ x,
+                                                                const T_* __restrict__ wg,
                                                                 int T, int H, int E, int kps,
                                                                 float* __restrict__ ws) {
   using C = RouteTile<BT, EP, NW>;
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(NW * 64) void route_partial_kernel(const uint16_t* 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int t0 = blockIdx.x * BT, e0 = blockIdx.y * EP, ks = blockIdx.z;
   f32x4_t acc[C::MC][C::NC];
-  score_tile<BT, EP, NW>(smem, x, wg, t0, T, e0, E, H, ks * kps, (ks + 1) * kps, acc);
+  score_tile<BT, EP, NW, T_>(smem, x, wg, t0, T, e0, E, H, ks * kps, (ks + 1) * kps, acc);
   // D layout of 16x16: lane holds column lane%16, rows (lane/16)*4 + v
 #pragma unroll
   for (int m = 0; m < C::MC; ++m)

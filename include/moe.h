@@ -355,7 +355,8 @@ typedef enum {
  * weight, bias, next_weight, next_bias [H] dtype or NULL: device, read; NULL
  *   with the kind MOE_NORM_NONE
  * res_out, next_out [rows,H] dtype: device, written. res_out may be res itself
- *   and next_out may be y itself; no other overlap. next_out NULL with
+ *   and next_out may be y itself; any other overlap of the outputs with each
+ *   other, y or res is MOE_ERR_INVALID_ARG. next_out NULL with
  *   next_kind MOE_NORM_NONE.
  * scale: finite. eps, H, alignment and arithmetic as moe_norm.
  */
@@ -390,7 +391,7 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
  * x [T,H], wg [E,H] dtype, bias [E] fp32 or NULL: device, read
  * topk_idx [T,k] int32, topk_w [T,k] fp32: device, written
  * 1 <= groups <= 64, E % groups == 0, 1 <= topk_groups <= groups,
- * k <= topk_groups * E / groups, scale finite; else MOE_ERR_UNSUPPORTED (or
+ * k <= topk_groups * E / groups, T <= 2^27, scale finite; else MOE_ERR_UNSUPPORTED (or
  * MOE_ERR_INVALID_ARG for non-positive sizes and unknown enums).
  * ws / ws_bytes: device workspace of at least
  *   moe_route_grouped_workspace_bytes(T,H,E,k,dtype) (NULL allowed when that is 0)
@@ -420,7 +421,9 @@ typedef enum {
  * x [M,K], w [N,K] or [2,N,K], bias [N] or [2,N] or NULL, residual [M,N] or NULL,
  * all dtype: device, read; y [M,N] dtype: device, written. y may be residual
  * itself, and overlaps no other input.
- * K % 64 == 0, N % 64 == 0, any M >= 1.
+ * K % 64 == 0, N % 64 == 0, any M >= 1 whose tiles fit a launch (about M * N <
+ * 2^36; else MOE_ERR_UNSUPPORTED). An output that overlaps x, or residual other
+ * than being it, is MOE_ERR_INVALID_ARG.
  * ws / ws_bytes: device workspace of at least
  *   moe_linear_workspace_bytes(M,N,K,act,dtype) (NULL allowed when that is 0)
  */

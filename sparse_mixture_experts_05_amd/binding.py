@@ -550,6 +550,11 @@ class MoELayerGraph:
 
 
 # ---------------------------------------------------------------- around the layer
+#
+# Forward only, like the layer: no gradients flow through these calls. A call runs on
+# the given stream, or the current stream of the tensors' device; outputs and
+# workspaces that it allocates belong to that stream. Tensors made on another stream
+# are the caller's to order.
 
 NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -571,15 +576,15 @@ def _ptr(t, name: str, shape, dtype, device):
         return None
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch tensor")
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _ws(nbytes: int, device, ws):
@@ -836,8 +841,8 @@ def moe_block_forward(h, wg, w_up, w_down, k: int, x=None, norm_weight=None, nor
     offsets, perm, inv, out."""
     if (ws_up is None) != (ws_down is None):
         raise ValueError("the shared expert needs ws_up and ws_down")
-    dev = _dims(h, "h", 2) and h.device
-    other = _other_stream(dev, stream)
+    _dims(h, "h", 2)
+    other = _other_stream(h.device, stream)
     if other is not None:
         with torch.cuda.stream(other):
             return moe_block_forward(h, wg, w_up, w_down, k, x, norm_weight, norm_bias, norm, eps,
@@ -894,6 +899,8 @@ class MoEBlockGraph:
 
     def run(self, h):
         """Copy h into the static input and replay; returns (res, next)."""
+        if h.shape != self.h.shape:  # copy_ would broadcast
+            raise ValueError(f"h has shape {tuple(h.shape)}, expected {tuple(self.h.shape)}")
         self.h.copy_(h)
         self.graph.replay()
         return self.state["res"], self.state["next"]

@@ -58,7 +58,7 @@ hipError_t launch_route_grouped(const void* x, const void* wg, const float* bias
                                 int32_t* topk_idx, float* topk_w, void* ws, hipStream_t s);
 
 // Whether every launch of the shape fits one grid.
-bool linear_fits(int E, int M, int N, int K);
+bool linear_fits(int E, int M, int N, int K, int act, bool grouped, bool bf16);
 size_t linear_ws_bytes(int E, int M, int N, int K, int act, bool grouped, bool bf16);
 hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
                          const int32_t* offsets, int E, int M, int N, int K, const void* w,

@@ -500,9 +500,14 @@ LinArgs lin_args(const void* x, const int32_t* gather, int gk, int gT, const int
 
 }  // namespace
 
-bool linear_fits(int E, int M, int N, int K) {
+bool linear_fits(int E, int M, int N, int K, int act, bool grouped, bool bf16) {
   const int32_t some = 0;  // only tested for null
-  return lin_tiles(lin_args(nullptr, nullptr, 1, M, &some, E, M, N, K, 0), 16, 16) < (1LL << 31) - 8;
+  const LinArgs a = lin_args(nullptr, nullptr, 1, M, grouped ? &some : nullptr, E, M, N, K, act);
+  // a grid dimension holds less than 2^32 threads; every path but the few-row one has at
+  // most the workgroups of the 64 x 64 tiles
+  const int bnc = host_gated(act) ? 32 : 64;
+  const bool rows = bf16 && lin_plan(a).path == kRows;
+  return lin_tiles(a, rows ? 16 : 64, rows ? 16 : bnc) + 8 < (1LL << 32) / kThreads;
 }
 
 size_t linear_ws_bytes(int E, int M, int N, int K, int act, bool grouped, bool bf16) {

@@ -215,6 +215,7 @@ int moe_bias_update(const int32_t* counts, int E, float gamma, float* bias, floa
 namespace {
 
 constexpr int kMaxNormH = 16384;
+constexpr int kMaxGroupedT = 1 << 27;  // 16 threads a token in one grid dimension
 
 bool norm_kind_ok(int kind) { return kind >= MOE_NORM_NONE && kind <= MOE_NORM_LAYER; }
 bool aligned_or_null(const void* p) { return !p || aligned16(p); }
@@ -233,22 +234,23 @@ int check_norm(int rows, int H, float eps, int dtype) {
   return H > kMaxNormH ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-int check_grouped(int E, int k, int score, int groups, int topk_groups, int group_top, int renorm,
+int check_grouped(int T, int E, int k, int score, int groups, int topk_groups, int group_top, int renorm,
                   float scale) {
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
   if (groups < 1 || topk_groups < 1 || (group_top != 1 && group_top != 2) ||
       (renorm != 0 && renorm != 1) || !std::isfinite(scale))
     return MOE_ERR_INVALID_ARG;
-  if (groups > 64 || E % groups != 0 || topk_groups > groups) return MOE_ERR_UNSUPPORTED;
+  if (groups > 64 || E % groups != 0 || topk_groups > groups || T > kMaxGroupedT)
+    return MOE_ERR_UNSUPPORTED;
   return k > topk_groups * (E / groups) ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-int check_linear(int E, int M, int N, int K, int act, int dtype) {
+int check_linear(int E, int M, int N, int K, int act, bool grouped, int dtype) {
   if (E < 1 || M < 1 || N < 1 || K < 1 || !dtype_ok(dtype) || act < MOE_ACT_NONE ||
       act > MOE_ACT_SWIGLU)
     return MOE_ERR_INVALID_ARG;
   if (E > kMaxExperts || N % 64 != 0 || K % 64 != 0) return MOE_ERR_UNSUPPORTED;
-  return moe::linear_fits(E, M, N, K) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+  return moe::linear_fits(E, M, N, K, act, grouped, dtype == MOE_BF16) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
 int run_linear(const void* x, const int32_t* perm, int k, int T, const int32_t* offsets, int E,
@@ -323,7 +325,7 @@ int moe_route_grouped(const void* x, const void* wg, const float* bias, int T, i
   if (!aligned16(x) || !aligned16(wg) || !aligned_or_null(ws)) return MOE_ERR_INVALID_ARG;
   int st = check_tokens(T, H, E, k);
   if (st != MOE_OK) return st;
-  st = check_grouped(E, k, score, groups, topk_groups, group_top, renorm, scale);
+  st = check_grouped(T, E, k, score, groups, topk_groups, group_top, renorm, scale);
   if (st != MOE_OK) return st;
   const size_t need = moe::route_grouped_ws_bytes(T, H, E, dtype == MOE_BF16);
   if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
@@ -334,21 +336,21 @@ int moe_route_grouped(const void* x, const void* wg, const float* bias, int T, i
 }
 
 size_t moe_linear_workspace_bytes(int M, int N, int K, int act, int dtype) {
-  if (check_linear(1, M, N, K, act, dtype) != MOE_OK) return 0;
+  if (check_linear(1, M, N, K, act, false, dtype) != MOE_OK) return 0;
   return moe::linear_ws_bytes(1, M, N, K, act, false, dtype == MOE_BF16);
 }
 
 int moe_linear(const void* x, const void* w, const void* bias, int act, const void* residual,
                int M, int N, int K, int dtype, void* y, void* ws, size_t ws_bytes, void* stream) {
   if (!x || !w || !y) return MOE_ERR_INVALID_ARG;
-  const int st = check_linear(1, M, N, K, act, dtype);
+  const int st = check_linear(1, M, N, K, act, false, dtype);
   if (st != MOE_OK) return st;
   return run_linear(x, nullptr, 1, M, nullptr, 1, M, w, bias, act, residual, N, K, dtype, y, ws,
                     ws_bytes, stream);
 }
 
 size_t moe_linear_grouped_workspace_bytes(int E, int rows, int N, int K, int act, int dtype) {
-  if (check_linear(E, rows, N, K, act, dtype) != MOE_OK) return 0;
+  if (check_linear(E, rows, N, K, act, true, dtype) != MOE_OK) return 0;
   return moe::linear_ws_bytes(E, rows, N, K, act, true, dtype == MOE_BF16);
 }
 
@@ -357,7 +359,7 @@ int moe_linear_grouped(const void* x, const int32_t* perm, int k, int T, const i
                        const void* residual, int N, int K, int dtype, void* y, void* ws,
                        size_t ws_bytes, void* stream) {
   if (!x || !offsets || !w || !y) return MOE_ERR_INVALID_ARG;
-  const int st = check_linear(E, rows, N, K, act, dtype);
+  const int st = check_linear(E, rows, N, K, act, true, dtype);
   if (st != MOE_OK) return st;
   if (perm) {
     if (T < 1 || k < 1) return MOE_ERR_INVALID_ARG;

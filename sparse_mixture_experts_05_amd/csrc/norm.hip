@@ -210,8 +210,8 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_kernel(NormArgs a) {
   int buf = 0;
   const int t = threadIdx.x % TR;
   const int H = a.H;
-  const int row = blockIdx.x * RPB + threadIdx.x / TR;
-  if (row >= a.rows) return;  // whole waves of a workgroup without barriers
+  const long long row = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * RPB + threadIdx.x / TR;
+  if (row >= a.rows) return;  // whole workgroups, or whole waves where there is no barrier
   const size_t base = (size_t)row * H;
   const T* w = static_cast<const T*>(a.w);
   const T* b = static_cast<const T*>(a.b);
@@ -270,7 +270,9 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_kernel(NormArgs a) {
 template <typename T, int VEC, int TR, int NV, bool RES>
 hipError_t run_norm(const NormArgs& a, hipStream_t s) {
   constexpr int RPB = TR < 256 ? 256 / TR : 1;
-  hipLaunchKernelGGL((norm_kernel<T, VEC, TR, NV, RES>), dim3((a.rows + RPB - 1) / RPB),
+  // a grid dimension holds less than 2^32 threads: a second one for very many rows
+  const unsigned blocks = ((unsigned)a.rows + RPB - 1) / RPB, nx = std::min(blocks, 1u << 20);
+  hipLaunchKernelGGL((norm_kernel<T, VEC, TR, NV, RES>), dim3(nx, (blocks + nx - 1) / nx),
                      dim3(TR < 256 ? 256 : TR), 0, s, a);
   return hipGetLastError();
 }

@@ -140,6 +140,8 @@ def test_block_graphs(T):
     p = params(16, H, 128, 64, dtype)
     kw = {n: v for n, v in {**p, **KW}.items() if n not in ("wg", "w_up", "w_down", "k")}
     graphs = [moe.MoEBlockGraph(T, p["wg"], p["w_up"], p["w_down"], KW["k"], **kw) for _ in range(2)]
+    with pytest.raises(ValueError, match="h has shape"):
+        graphs[0].run(torch.zeros((1, 1), dtype=dtype, device="cuda"))
     for rep in range(4):
         hs = [stream_rows(T, H, dtype, p, 10 * rep + i) for i in range(2)]
         outs = [g.run(h) for g, h in zip(graphs, hs)]

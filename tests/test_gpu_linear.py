@@ -185,6 +185,32 @@ def test_bad_offsets_and_perm_stay_inside():
         torch.cuda.synchronize()
 
 
+def test_operands_past_4_gib():
+    """Row buffers past 32-bit offsets: gathered rows from the far end of x, and a
+    buffer with many row tiles."""
+    print("\n[gpu] linear past 4 GiB", flush=True)
+    T, K, N, E, k = 600_000, 4096, 2048, 4, 1
+    x = torch.empty((T, K), dtype=torch.bfloat16, device="cuda").normal_()
+    w = randn((E, N, K), torch.bfloat16, 2, K ** -0.5)
+    for rows in (40, 4000):
+        # many rows would take the large tiles, whose offsets into x are 32-bit
+        need = moe.moe_linear_grouped_workspace_bytes(E, rows, N, K, "none", 1)
+        assert (need > 0) == (rows == 4000)
+        perm = torch.arange(T - 1, T - 1 - rows, -1, dtype=torch.int32, device="cuda")
+        off = torch.tensor([0, rows // 3, rows // 3, rows - 7, rows], dtype=torch.int32, device="cuda")
+        got = moe.moe_linear_grouped(x, off, w, perm=perm, k=k, rows=rows)
+        for e in range(E):
+            lo, hi = int(off[e]), int(off[e + 1])
+            if hi > lo:
+                near(got[lo:hi], *product64(x[perm[lo:hi].long()], w[e], None, "none", None, torch.bfloat16),
+                     torch.bfloat16, f"rows {rows} expert {e}")
+    w1 = w[1, :64].contiguous()
+    got = moe.moe_linear(x, w1)
+    for lo in (0, 524_280, T - 300):
+        near(got[lo:lo + 300], *product64(x[lo:lo + 300], w1, None, "none", None, torch.bfloat16),
+             torch.bfloat16, f"row {lo}")
+
+
 def test_nan_rows_stay_alone():
     """A NaN or infinite row reaches only its own outputs."""
     print("\n[gpu] linear nan rows", flush=True)

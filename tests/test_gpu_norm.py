@@ -132,6 +132,19 @@ def test_rows_do_not_touch_each_other(kind, dtype):
         assert (moe.moe_norm(z + 2.0, kind=kind) == 0).all()
 
 
+def test_very_many_rows():
+    """More workgroups than one grid dimension takes here (2^20), to the last row."""
+    print("\n[gpu] norm many rows", flush=True)
+    T, H = 4 * (1 << 20) + 5, 12
+    x = torch.randn((T, H), device="cuda").bfloat16()
+    got = moe.moe_norm(x)
+    for lo in (0, 2 ** 20 - 3, T // 2, T - 9):
+        part = x[lo:lo + 9]
+        near(got[lo:lo + 9], *norm64(part.cpu().double(), "rms", None, None, 1e-6), torch.bfloat16, lo)
+    r, n = moe.moe_norm_residual(x, x.clone(), kind="none", scale=0.0, next_kind="rms")
+    assert torch.equal(r, x) and torch.equal(n, got)
+
+
 def test_other_stream_and_graph():
     print("\n[gpu] norm stream and graph", flush=True)
     x, res = draw((64, 4096), torch.bfloat16, 1).cuda(), draw((64, 4096), torch.bfloat16, 2).cuda()

@@ -38,8 +38,9 @@ def oracle(s, bias, k, score, groups, topk_groups, group_top, renorm, scale):
     ids, w, gap = np.zeros((T, k), np.int32), np.zeros((T, k)), np.inf
 
     def nearest(a):
+        a = a[np.isfinite(a)]
         d = -np.diff(a)
-        d = d[np.isfinite(d) & (d > 0)]
+        d = d[d > 0]
         return d.min() if d.size else np.inf
 
     for t in range(T):

@@ -64,7 +64,7 @@ def grouped(x=P[0], wg=P[1], bias=P[2], T=32, H=64, E=64, k=4, score=1, groups=8
     (dict(k=0), -1), (dict(score=2), -1), (dict(score=-1), -1), (dict(groups=0), -1),
     (dict(tg=0), -1), (dict(gt=0), -1), (dict(gt=3), -1), (dict(rn=2), -1), (dict(scale=NAN), -1),
     (dict(scale=INF), -1), (dict(groups=7), -2), (dict(tg=9), -2), (dict(E=256, groups=128), -2),
-    (dict(E=16, tg=1, k=4), -2), (dict(E=257), -2), (dict(k=9), -2), (dict(H=96), -2),
+    (dict(E=16, tg=1, k=4), -2), (dict(E=257), -2), (dict(k=9), -2), (dict(H=96), -2), (dict(T=(1 << 27) + 1, k=1), -2),
     (dict(ws=None), -3), (dict(wsn=16), -3),
 ])
 def test_route_grouped_refusals(kw, status):
@@ -87,7 +87,7 @@ def linear(x=P[0], w=P[1], b=P[2], act=2, res=P[3], M=32, N=64, K=64, dt=1, y=P[
     (dict(act=-1), -1), (dict(M=0), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(dt=4), -1),
     (dict(x=ODD), -1), (dict(w=ODD), -1), (dict(b=ODD), -1), (dict(res=ODD), -1), (dict(y=ODD), -1),
     (dict(ws=ODD), -1), (dict(N=96), -2), (dict(K=32), -2),
-    (dict(M=2 ** 31 - 1, N=1 << 20, y=ctypes.c_void_p(1 << 62)), -2),
+    (dict(M=2 ** 31 - 1, N=1 << 20), -2), (dict(M=1 << 22, N=1 << 14), -2),
     (dict(y=P[0]), -1), (dict(y=ctypes.c_void_p(P[0].value + 16)), -1),
     (dict(y=ctypes.c_void_p(P[3].value + 16)), -1),
 ])

@@ -308,12 +308,24 @@ hipError_t launch_bf16_bt(const void* x, const void* wg, const GroupArgs& a, int
   if (E <= 16) return launch_bf16<BT, 16>(x, wg, a, T, H, E, k, idx, w, s);
   if (E <= 32) return launch_bf16<BT, 32>(x, wg, a, T, H, E, k, idx, w, s);
   if (E <= 64) return launch_bf16<BT, 64>(x, wg, a, T, H, E, k, idx, w, s);
-  if (E <= 128) return launch_bf16<BT, 128, route_waves<BT, 128>()>(x, wg, a, T, H, E, k, idx, w, s);
-  return launch_bf16<BT, 256, route_waves<BT, 256>()>(x, wg, a, T, H, E, k, idx, w, s);
+  if constexpr (BT != 32) {  // 8192 to 16383 tokens and E > 64 take two launches
+    if (E <= 128) return launch_bf16<BT, 128, route_waves<BT, 128>()>(x, wg, a, T, H, E, k, idx, w, s);
+    return launch_bf16<BT, 256, route_waves<BT, 256>()>(x, wg, a, T, H, E, k, idx, w, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+// bf16 calls take the paths of moe_route, except that few tokens with a small Wg (256 KB)
+// take one launch too: a workgroup of 16 tokens reads all of it at about 60 GB/s, which
+// costs the GPU 0 to 3 us more than two launches (H 2048, E 60, T 16: 12.2 against 8.8;
+// T 1777: 12.3 against 11.2; H 1024, E 16: 5.9 against 7.9) and saves the host the second
+// one and the workspace (5 us). At 512 KB one launch takes up to twice as long.
+bool one_launch(int T, int H, int E, bool bf16) {
+  return bf16 && (route_mode(T, E, true) == kOneLaunch ||
+                  (T < 2048 && (long long)E * H <= 128 * 1024));
 }
 
 // fp32 scores always take two launches: 16 x 64 tiles for few tokens, else 64 x 128.
-// bf16 calls take the paths of moe_route.
 bool f32_big(int T) { return T >= 512; }
 
 // K slices of the fp32 paths: a power of two that divides the panels (32 k), about 512
@@ -344,6 +356,7 @@ hipError_t launch_partial_f32(const void* x, const void* wg, int T, int H, int E
 }  // namespace
 
 size_t route_grouped_ws_bytes(int T, int H, int E, bool bf16) {
+  if (one_launch(T, H, E, bf16)) return 0;
   return bf16 ? scores_ws_bytes(T, H, E, true)
               : align256((size_t)f32_kslices(T, H, E) * T * E * sizeof(float));
 }
@@ -362,7 +375,7 @@ hipError_t launch_route_grouped(const void* x, const void* wg, const float* bias
   a.softmax = softmax;
   a.renorm = renorm;
   a.scale = scale;
-  if (!bf16 || route_mode(T, E, true) != kOneLaunch) {
+  if (!one_launch(T, H, E, bf16)) {
     float* sp = static_cast<float*>(ws);
     const int nks = bf16 ? route_kslices(T, H, E) : f32_kslices(T, H, E);
     const hipError_t err = bf16 ? launch_partial(x, wg, T, H, E, sp, s)

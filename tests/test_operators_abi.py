@@ -65,7 +65,8 @@ def grouped(x=P[0], wg=P[1], bias=P[2], T=32, H=64, E=64, k=4, score=1, groups=8
     (dict(tg=0), -1), (dict(gt=0), -1), (dict(gt=3), -1), (dict(rn=2), -1), (dict(scale=NAN), -1),
     (dict(scale=INF), -1), (dict(groups=7), -2), (dict(tg=9), -2), (dict(E=256, groups=128), -2),
     (dict(E=16, tg=1, k=4), -2), (dict(E=257), -2), (dict(k=9), -2), (dict(H=96), -2), (dict(T=(1 << 27) + 1, k=1), -2),
-    (dict(ws=None), -3), (dict(wsn=16), -3),
+    (dict(H=4096, ws=None), -3), (dict(H=4096, wsn=16), -3),
+    (dict(dt=0, ws=None), -3), (dict(dt=0, wsn=16), -3),
 ])
 def test_route_grouped_refusals(kw, status):
     assert grouped(**kw) == status
@@ -75,6 +76,7 @@ def test_route_grouped_workspace():
     L = moe.lib()
     assert L.moe_route_grouped_workspace_bytes(16, 4096, 128, 8, 1) >= 16 * 128 * 4
     assert L.moe_route_grouped_workspace_bytes(16, 4096, 257, 8, 1) == 0
+    assert L.moe_route_grouped_workspace_bytes(16, 1024, 64, 8, 1) == 0  # one launch
 
 
 def linear(x=P[0], w=P[1], b=P[2], act=2, res=P[3], M=32, N=64, K=64, dt=1, y=P[4], ws=P[5],

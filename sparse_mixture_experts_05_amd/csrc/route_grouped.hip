@@ -42,11 +42,6 @@ __device__ __forceinline__ float sigmoidf(float s) { return 1.0f / (1.0f + expf(
 // that size. The k weights take expf.
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
-// p of a score: sigmoid, or softmax with the largest score and 1 / sum.
-__device__ __forceinline__ float prob_fast(const GroupArgs& a, float s, float top, float rz) {
-  return a.softmax ? exp_fast(s - top) * rz : __builtin_amdgcn_rcpf(1.0f + exp_fast(-s));
-}
-
 template <int L, int G>
 __device__ __forceinline__ float group_max(float v) {
   if constexpr ((1 << L) < G) return group_max<L + 1, G>(fmaxf(v, __uint_as_float(partner<L>(__float_as_uint(v)))));
@@ -102,13 +97,29 @@ __device__ __forceinline__ void grouped_tokens(const float* sc, GroupLds<BT, NW>
     rz = 1.0f / group_sum<0, G>(z);
   }
   if (a.bias != nullptr || limit) {
+    // branch free in the experts (a load or a write under a branch would wait for each in
+    // turn); columns from E up hold values that nobody reads
+    float v[NSUB], b[NSUB];
 #pragma unroll
-    for (int i = 0; i < NSUB; ++i) {
-      const int e = g + G * i, ec = min(e, E - 1);
-      float v = prob_fast(a, x[i], top, rz);
-      if (a.bias != nullptr) v += a.bias[ec];
-      if (limit && e < E) L.v[t * S + e] = v;
-      if (a.bias != nullptr) x[i] = v;
+    for (int i = 0; i < NSUB; ++i) b[i] = 0.0f;
+    if (a.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NSUB; ++i) b[i] = a.bias[min(g + G * i, E - 1)];
+    }
+    if (a.softmax) {
+#pragma unroll
+      for (int i = 0; i < NSUB; ++i) v[i] = fmaf(exp_fast(x[i] - top), rz, b[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NSUB; ++i) v[i] = __builtin_amdgcn_rcpf(1.0f + exp_fast(-x[i])) + b[i];
+    }
+    if (limit) {
+#pragma unroll
+      for (int i = 0; i < NSUB; ++i) L.v[t * S + g + G * i] = v[i];
+    }
+    if (a.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NSUB; ++i) x[i] = v[i];
     }
   }
   unsigned long long mask = ~0ull;
@@ -122,11 +133,18 @@ __device__ __forceinline__ void grouped_tokens(const float* sc, GroupLds<BT, NW>
         const float* r = L.v + t * S + q * a.per;
         float b1 = -INFINITY, b2 = -INFINITY;
         int i = q % a.per;
-        for (int n = 0; n < a.per; ++n) {
-          const float v = fmaxf(r[i], -INFINITY);
-          b2 = fmaxf(b2, fminf(b1, v));
-          b1 = fmaxf(b1, v);
-          i = i + 1 == a.per ? 0 : i + 1;
+        for (int n = 0; n < a.per; n += 4) {
+          float v[4];  // past the end: nothing
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            v[u] = n + u < a.per ? fmaxf(r[i], -INFINITY) : -INFINITY;
+            i = i + 1 == a.per ? 0 : i + 1;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            b2 = fmaxf(b2, fminf(b1, v[u]));
+            b1 = fmaxf(b1, v[u]);
+          }
         }
         // the second counts only if it is on
         L.gs[t][q] = a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
@@ -263,7 +281,7 @@ __global__ __launch_bounds__(kThreads) void grouped_select_kernel(const float* _
       float s = 0.0f;
 #pragma unroll
       for (int q = 0; q < NKS; ++q) s += v[i][q];
-      if (g + G * (i0 + i) < E) sc[t * S + g + G * (i0 + i)] = s;
+      sc[t * S + g + G * (i0 + i)] = s;  // columns from E up: read by nobody
     }
   }
   wave_lds_fence();

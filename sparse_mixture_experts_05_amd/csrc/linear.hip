@@ -120,7 +120,7 @@ __device__ __forceinline__ LinTile lin_tile(const LinArgs& a, int bnc) {
 
 // ----------------------------------------------------------------- 64 x 64 tiles
 
-// Tiles of 64 rows x 64 weight rows (64 output columns, or 32 of a gated
+// Tiles of BM rows x 64 weight rows (64 output columns, or 32 of a gated
 // product) by 4 waves in a 2 x 2 grid, bf16 or fp32. Operand rows are copied
 // global -> LDS with global_load_lds (8 rows of 128 bytes an instruction) into a
 // ring of NS stages of 128 bytes of K; 16-byte chunk c of row r sits at slot
@@ -132,55 +132,59 @@ __device__ __forceinline__ LinTile lin_tile(const LinArgs& a, int bnc) {
 //
 // blockIdx.y of gridDim.y: a K slice. With several, a slice writes its
 // accumulators to a.part and lin_tile_reduce_kernel finishes the tile.
-struct Tile64 {
-  static constexpr int BM = 64, BN = 64, NS = 3;
+template <int BM_>
+struct TileShape {
+  static constexpr int BM = BM_, BN = 64, NS = 3;
   static constexpr int TM = BM / 2 / 16, TN = BN / 2 / 16;  // sub-tiles of a wave
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int NI = (BM + BN) / 8 / 4;  // copies per wave per stage
 };
 
 __device__ __forceinline__ int tile_col(int wn, int j, bool gt) {  // first column of a sub-tile
-  constexpr int W = Tile64::BN / 2;
+  constexpr int W = 64 / 2;
   return gt ? wn * (W / 2) + j * 16 : wn * W + j * 16;
 }
 
 // Epilogue of a wave's accumulators, straight to memory.
-template <typename T>
+template <typename T, typename Sh>
 __device__ __forceinline__ void tile_store(const LinArgs& a, const LinTile& t,
-                                           const f32x4_t (&acc)[Tile64::TM][Tile64::TN]) {
+                                           const f32x4_t (&acc)[Sh::TM][Sh::TN]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 1, wn = wave & 1;
   const bool gt = gated(a.act);
 #pragma unroll
-  for (int i = 0; i < Tile64::TM; ++i) {
-    const int r = wm * (Tile64::BM / 2) + i * 16 + (lane & 15);
+  for (int i = 0; i < Sh::TM; ++i) {
+    const int r = wm * (Sh::BM / 2) + i * 16 + (lane & 15);
     if (r >= t.M) continue;
 #pragma unroll
-    for (int j = 0; j < Tile64::TN; ++j) {
-      if (gt && j >= Tile64::TN / 2) continue;
+    for (int j = 0; j < Sh::TN; ++j) {
+      if (gt && j >= Sh::TN / 2) continue;
       const int c = t.n0 + tile_col(wn, j, gt) + (lane >> 4) * 4;
-      if (c < a.N) store4<T>(a, t.e, (size_t)(t.row0 + r), c, acc[i][j], acc[i][(j + Tile64::TN / 2) % Tile64::TN]);
+      if (c < a.N) store4<T>(a, t.e, (size_t)(t.row0 + r), c, acc[i][j], acc[i][(j + Sh::TN / 2) % Sh::TN]);
     }
   }
 }
 
 // Accumulator (i, j) of this thread in slice ks of a tile's partials.
+template <typename Sh>
 __device__ __forceinline__ float* tile_part(const LinArgs& a, const LinTile& t, int ks, int nks,
                                             int i, int j) {
-  return a.part + ((size_t)t.q * nks + ks) * Tile64::BM * Tile64::BN +
-         ((size_t)(i * Tile64::TN + j) * kThreads + threadIdx.x) * 4;
+  return a.part + ((size_t)t.q * nks + ks) * Sh::BM * Sh::BN +
+         ((size_t)(i * Sh::TN + j) * kThreads + threadIdx.x) * 4;
 }
 
+template <typename Sh>
 __device__ __forceinline__ LinTile find(const LinArgs& a) {
-  return lin_tile<Tile64::BM>(a, gated(a.act) ? Tile64::BN / 2 : Tile64::BN);
+  return lin_tile<Sh::BM>(a, gated(a.act) ? Sh::BN / 2 : Sh::BN);
 }
 
-template <typename T>
+template <typename T, int BM_>
 __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
-  constexpr int BM = Tile64::BM, BN = Tile64::BN, NS = Tile64::NS, STAGE = Tile64::STAGE, NI = Tile64::NI;
-  constexpr int TM = Tile64::TM, TN = Tile64::TN;
+  using Sh = TileShape<BM_>;
+  constexpr int BM = Sh::BM, BN = Sh::BN, NS = Sh::NS, STAGE = Sh::STAGE, NI = Sh::NI;
+  constexpr int TM = Sh::TM, TN = Sh::TN;
   __shared__ __attribute__((aligned(16))) uint8_t smem[NS * STAGE];
-  const LinTile t = find(a);
+  const LinTile t = find<Sh>(a);
   if (t.M == 0) return;
   const bool gt = gated(a.act);
   const int N = a.N, K = a.K;
@@ -248,7 +252,7 @@ __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
     }
   }
   if (gridDim.y == 1) {
-    tile_store<T>(a, t, acc);
+    tile_store<T, Sh>(a, t, acc);
     return;
   }
 #pragma unroll
@@ -256,7 +260,7 @@ __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
     if (wm * (BM / 2) + i * 16 < t.M)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        *reinterpret_cast<f32x4_t*>(tile_part(a, t, blockIdx.y, gridDim.y, i, j)) = acc[i][j];
+        *reinterpret_cast<f32x4_t*>(tile_part<Sh>(a, t, blockIdx.y, gridDim.y, i, j)) = acc[i][j];
 }
 
 // Sums the nks K slices of each tile in slice order, then the epilogue. One
@@ -264,22 +268,23 @@ __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
 // tiles still has many.
 constexpr int kMaxSlices = 16;
 
-template <typename T>
+template <typename T, int BM_>
 __global__ __launch_bounds__(kThreads) void lin_tile_reduce_kernel(LinArgs a, int nks) {
-  const LinTile t = find(a);
+  using Sh = TileShape<BM_>;
+  const LinTile t = find<Sh>(a);
   if (t.M == 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const bool gt = gated(a.act);
   const int i = blockIdx.y;
-  const int r = (wave >> 1) * (Tile64::BM / 2) + i * 16 + (lane & 15);
-  f32x4_t acc[Tile64::TN];
-  if ((wave >> 1) * (Tile64::BM / 2) + i * 16 >= t.M) return;
+  const int r = (wave >> 1) * (Sh::BM / 2) + i * 16 + (lane & 15);
+  f32x4_t acc[Sh::TN];
+  if ((wave >> 1) * (Sh::BM / 2) + i * 16 >= t.M) return;
 #pragma unroll
-  for (int j = 0; j < Tile64::TN; ++j) {
+  for (int j = 0; j < Sh::TN; ++j) {
     f32x4_t v[kMaxSlices];
 #pragma unroll
     for (int s = 0; s < kMaxSlices; ++s)  // all loads first, from clamped slices
-      v[s] = *reinterpret_cast<const f32x4_t*>(tile_part(a, t, min(s, nks - 1), nks, i, j));
+      v[s] = *reinterpret_cast<const f32x4_t*>(tile_part<Sh>(a, t, min(s, nks - 1), nks, i, j));
     acc[j] = v[0];
 #pragma unroll
     for (int s = 1; s < kMaxSlices; ++s)
@@ -287,10 +292,10 @@ __global__ __launch_bounds__(kThreads) void lin_tile_reduce_kernel(LinArgs a, in
   }
   if (r >= t.M) return;
 #pragma unroll
-  for (int j = 0; j < Tile64::TN; ++j) {
-    if (gt && j >= Tile64::TN / 2) continue;
+  for (int j = 0; j < Sh::TN; ++j) {
+    if (gt && j >= Sh::TN / 2) continue;
     const int c = t.n0 + tile_col(wave & 1, j, gt) + (lane >> 4) * 4;
-    if (c < a.N) store4<T>(a, t.e, (size_t)(t.row0 + r), c, acc[j], acc[(j + Tile64::TN / 2) % Tile64::TN]);
+    if (c < a.N) store4<T>(a, t.e, (size_t)(t.row0 + r), c, acc[j], acc[(j + Sh::TN / 2) % Sh::TN]);
   }
 }
 
@@ -400,10 +405,15 @@ struct LinPlan {
 
 bool host_gated(int act) { return act == kActGeglu || act == kActSwiglu; }
 
-// K slices of an fp32 product, which always takes the 64 x 64 tiles: as many as fill
-// the chip with about two workgroups a CU and leave each 8 stages or more.
+// fp32 products always take these tiles, bound by the fp32 MFMA rate (a sixteenth of
+// bf16's): of 32 rows where 64 would leave CUs without one (64 x 512 x 256: 9.8 to 6.8
+// us), and as many K slices as fill the chip with about two workgroups a CU and
+// leave each 8 stages or more.
+int f32_rows(const LinArgs& a) {
+  return lin_tiles(a, 64, host_gated(a.act) ? 32 : 64) < 256 ? 32 : 64;
+}
 int f32_slices(const LinArgs& a) {
-  const double tiles = (double)lin_tiles(a, 64, host_gated(a.act) ? 32 : 64);
+  const double tiles = (double)lin_tiles(a, f32_rows(a), host_gated(a.act) ? 32 : 64);
   int nks = 1;
   while (nks < kMaxSlices && tiles * nks * 2 <= 512 && a.K / 32 >= 16 * nks) nks *= 2;
   return nks;
@@ -431,10 +441,11 @@ int f32_slices(const LinArgs& a) {
 // A stage is 64 k. Few-row kernel: every block of 16 rows x 16 columns reads both
 // operands from the caches (8.5 TB/s), and a wave walks a quarter of K (1 us per
 // 1000). 64x64 tiles: 0.36 us a stage while fewer than 1.75 workgroups share a CU,
-// then in proportion, a fifth of which does not hide behind the weights' stream;
-// slices add a launch (3 us) and their partials' round trip. The large tiles run one
+// then in proportion, and a third of the time in which every column tile reads its rows
+// from L2 (8 TB/s) does not hide; slices add a launch (3 us) and their partials' round trip. The large tiles run one
 // workgroup a CU: 0.55 or 0.94 us a stage on an idle chip, 0.9 or 1.5 when every CU
-// runs one (power and cache traffic).
+// runs one (power and cache traffic). Of the lesser of work and weight stream a tenth
+// does not hide behind the other.
 LinPlan lin_plan(const LinArgs& a) {
   const double h = host_gated(a.act) ? 2.0 : 1.0, cols = h * a.N;  // weight rows of an expert
   // experts with rows, as if each row drew its expert
@@ -460,33 +471,35 @@ LinPlan lin_plan(const LinArgs& a) {
     if (us < t) t = us, best = LinPlan{path, nks};
   };
   const double tiles = row_tiles(64) * std::ceil(cols / 64);
+  const double rows_l2 = 0.3 * 2.0 * a.M * a.K * std::ceil(cols / 64) / 8e6;
   for (int nks = 1; nks <= 16; nks *= 2) {
     if (nks > 1 && (a.K / 64 < 2 * nks || tiles * nks > 2048)) break;
     double us = 4.4 + std::ceil(stages / nks) * 0.36 * std::max(1.0, tiles * nks / 448);
     if (nks > 1) us += 3.0 + 8.0 * a.M * cols * nks / 5e6;
-    take(kTile64, nks, std::max(us, 3.0 + hbm) + 0.2 * std::min(us, hbm));
+    take(kTile64, nks, std::max(us, 3.0 + hbm) + 0.1 * std::min(us, hbm) + rows_l2);
   }
   if (big_ok(a)) {
-    take(kBigHalf, 1, std::max(big(128, 0.55, 0.9), 8.0 + 1.1 * hbm));
-    take(kBig, 1, std::max(big(256, 0.94, 1.5), 8.0 + hbm));
+    const double half = big(128, 0.55, 0.9), whole = big(256, 0.94, 1.5);
+    take(kBigHalf, 1, std::max(half, 8.0 + 1.1 * hbm) + 0.1 * std::min(half, hbm));
+    take(kBig, 1, std::max(whole, 8.0 + hbm) + 0.1 * std::min(whole, hbm));
   }
   return best;
 }
 
-size_t tile_ws_bytes(const LinArgs& a, int nks) {
+size_t tile_ws_bytes(const LinArgs& a, int bm, int nks) {
   if (nks <= 1) return 0;
-  return (size_t)lin_tiles(a, Tile64::BM, host_gated(a.act) ? Tile64::BN / 2 : Tile64::BN) * nks * Tile64::BM *
-         Tile64::BN * sizeof(float);
+  return (size_t)lin_tiles(a, bm, host_gated(a.act) ? 32 : 64) * nks * bm * 64 * sizeof(float);
 }
 
-template <typename T>
+template <typename T, int BM>
 hipError_t run_tile(LinArgs a, int nks, void* ws, hipStream_t s) {
-  const unsigned grid = lin_grid(a, Tile64::BM, host_gated(a.act) ? Tile64::BN / 2 : Tile64::BN);
+  const unsigned grid = lin_grid(a, BM, host_gated(a.act) ? 32 : 64);
   a.part = static_cast<float*>(ws);
-  hipLaunchKernelGGL((lin_tile_kernel<T>), dim3(grid, nks), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((lin_tile_kernel<T, BM>), dim3(grid, nks), dim3(kThreads), 0, s, a);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || nks <= 1) return err;
-  hipLaunchKernelGGL((lin_tile_reduce_kernel<T>), dim3(grid, Tile64::TM), dim3(kThreads), 0, s, a, nks);
+  hipLaunchKernelGGL((lin_tile_reduce_kernel<T, BM>), dim3(grid, TileShape<BM>::TM), dim3(kThreads), 0,
+                     s, a, nks);
   return hipGetLastError();
 }
 
@@ -505,6 +518,7 @@ bool linear_fits(int E, int M, int N, int K, int act, bool grouped, bool bf16) {
   const LinArgs a = lin_args(nullptr, nullptr, 1, M, grouped ? &some : nullptr, E, M, N, K, act);
   // a grid dimension holds less than 2^32 threads; every path but the few-row one has at
   // most the workgroups of the 64 x 64 tiles
+  // (fp32 tiles of 32 rows are a few hundred at most)
   const int bnc = host_gated(act) ? 32 : 64;
   const bool rows = bf16 && lin_plan(a).path == kRows;
   return lin_tiles(a, rows ? 16 : 64, rows ? 16 : bnc) + 8 < (1LL << 32) / kThreads;
@@ -513,10 +527,10 @@ bool linear_fits(int E, int M, int N, int K, int act, bool grouped, bool bf16) {
 size_t linear_ws_bytes(int E, int M, int N, int K, int act, bool grouped, bool bf16) {
   const int32_t some = 0;
   const LinArgs a = lin_args(nullptr, nullptr, 1, M, grouped ? &some : nullptr, E, M, N, K, act);
-  if (!bf16) return tile_ws_bytes(a, f32_slices(a));
+  if (!bf16) return tile_ws_bytes(a, f32_rows(a), f32_slices(a));
   const LinPlan p = lin_plan(a);
   if (p.path >= kBigHalf) return big_ws_bytes(a, p.path == kBigHalf);
-  return p.path == kTile64 ? tile_ws_bytes(a, p.nks) : 0;
+  return p.path == kTile64 ? tile_ws_bytes(a, 64, p.nks) : 0;
 }
 
 hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
@@ -526,7 +540,9 @@ hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
   LinArgs a = lin_args(x, gather, gk, gT, offsets, E, M, N, K, act);
   a.w = w, a.bias = bias, a.res = res, a.y = y;
   const bool gt = host_gated(act);
-  if (!bf16) return run_tile<float>(a, f32_slices(a), ws, s);
+  if (!bf16)
+    return f32_rows(a) == 32 ? run_tile<float, 32>(a, f32_slices(a), ws, s)
+                             : run_tile<float, 64>(a, f32_slices(a), ws, s);
   LinPlan p = lin_plan(a);
   // gathered rows past the large tiles' 32-bit offsets: no workspace needed either
   if (p.path >= kBigHalf && gather && !big_gather_ok(a)) p = LinPlan{kTile64, 1};
@@ -537,7 +553,7 @@ hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
       else hipLaunchKernelGGL((lin_rows_kernel<false>), grid, dim3(kThreads), 0, s, a);
       return hipGetLastError();
     }
-    case kTile64: return run_tile<uint16_t>(a, p.nks, ws, s);
+    case kTile64: return run_tile<uint16_t, 64>(a, p.nks, ws, s);
     default: return launch_big(a, p.path == kBigHalf, ws, s);
   }
 }

@@ -884,6 +884,7 @@ class MoEBlockGraph:
         if dev.type != "cuda":
             raise ValueError("wg must be a GPU tensor")
         self.h = torch.zeros((T, wg.shape[1]), dtype=wg.dtype, device=dev)
+        self.weights = (wg, w_up, w_down, kw)  # the graph reads them: kept alive with it
         call = lambda: moe_block_forward(self.h, wg, w_up, w_down, k, **kw)  # noqa: E731
         with torch.cuda.device(dev):
             side = torch.cuda.Stream()

@@ -88,7 +88,9 @@ __device__ __forceinline__ LinTile lin_tile(const LinArgs& a, int bnc) {
   }
   SegScan s;
   scan_segments<BM>(a, s);
-  const long long total = (long long)s.total * ntn;
+  // offsets that overlap could name more tiles than the launch has room for: the rest is
+  // left out
+  const long long total = min((long long)s.total * ntn, (long long)a.tiles);
   const int chunk = (int)((total + 7) / 8);
   const long long q = (long long)(g & 7) * chunk + (g >> 3);
   if ((g >> 3) >= chunk || q >= total) return t;
@@ -493,7 +495,9 @@ size_t tile_ws_bytes(const LinArgs& a, int bm, int nks) {
 
 template <typename T, int BM>
 hipError_t run_tile(LinArgs a, int nks, void* ws, hipStream_t s) {
-  const unsigned grid = lin_grid(a, BM, host_gated(a.act) ? 32 : 64);
+  const int bnc = host_gated(a.act) ? 32 : 64;
+  const unsigned grid = lin_grid(a, BM, bnc);
+  a.tiles = (int)lin_tiles(a, BM, bnc);
   a.part = static_cast<float*>(ws);
   hipLaunchKernelGGL((lin_tile_kernel<T, BM>), dim3(grid, nks), dim3(kThreads), 0, s, a);
   const hipError_t err = hipGetLastError();
@@ -549,6 +553,7 @@ hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
   switch (p.path) {
     case kRows: {
       const dim3 grid(lin_grid(a, 16, 16));
+      a.tiles = (int)lin_tiles(a, 16, 16);
       if (gt) hipLaunchKernelGGL((lin_rows_kernel<true>), grid, dim3(kThreads), 0, s, a);
       else hipLaunchKernelGGL((lin_rows_kernel<false>), grid, dim3(kThreads), 0, s, a);
       return hipGetLastError();

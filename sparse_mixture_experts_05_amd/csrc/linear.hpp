@@ -19,6 +19,7 @@ struct LinArgs {
   int E, M, N, K;
   int act;
   float* part;        // split-K partial tiles, or null
+  int tiles;          // 64 x 64 and few-row tiles: at most this many (sizes the partials)
   const int4* table;  // big tiles of a grouped launch: tile descriptors (plan.hpp entries)
   int slots;          // big tiles: workgroups of the launch
 };

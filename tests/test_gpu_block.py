@@ -139,7 +139,12 @@ def test_block_graphs(T):
     H, dtype = 256, torch.bfloat16
     p = params(16, H, 128, 64, dtype)
     kw = {n: v for n, v in {**p, **KW}.items() if n not in ("wg", "w_up", "w_down", "k")}
-    graphs = [moe.MoEBlockGraph(T, p["wg"], p["w_up"], p["w_down"], KW["k"], **kw) for _ in range(2)]
+    graphs = [moe.MoEBlockGraph(T, p["wg"], p["w_up"], p["w_down"], KW["k"], **kw)]
+    copies = {n: v.clone() for n, v in p.items()}
+    kw2 = {n: copies.get(n, v) for n, v in kw.items()}
+    graphs.append(moe.MoEBlockGraph(T, copies["wg"], copies["w_up"], copies["w_down"], KW["k"], **kw2))
+    del copies, kw2  # a graph keeps the weights that it reads
+    junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(8)]
     with pytest.raises(ValueError, match="h has shape"):
         graphs[0].run(torch.zeros((1, 1), dtype=dtype, device="cuda"))
     for rep in range(4):
@@ -150,3 +155,4 @@ def test_block_graphs(T):
             torch.cuda.synchronize()
             assert torch.equal(res, want["res"]) and torch.equal(nxt, want["next"]), rep
             check(h, p, g.state, dtype)
+    del junk

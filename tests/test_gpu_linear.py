@@ -185,6 +185,24 @@ def test_bad_offsets_and_perm_stay_inside():
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dtype", BOTH, ids=ID)
+def test_overlapping_offsets_stay_in_the_workspace(dtype):
+    """Offsets that go back and forth name more tiles than rows can have; no K slice's
+    partial tile may land past the workspace."""
+    print(f"\n[gpu] grouped overlapping offsets {dtype}", flush=True)
+    E, rows, N, K = 16, 96, 192, 8192
+    x, w = randn((rows, K), dtype, 1), randn((E, N, K), dtype, 2, K ** -0.5)
+    off = torch.tensor([0, rows] * (E // 2) + [rows], dtype=torch.int32, device="cuda")
+    need = moe.moe_linear_grouped_workspace_bytes(E, rows, N, K, "none", int(dtype == torch.bfloat16))
+    buf = torch.full((need + (8 << 20),), 77, dtype=torch.uint8, device="cuda")
+    y = torch.full((rows + 64, N), 3.0, dtype=dtype, device="cuda")
+    moe.moe_linear_grouped(x, off, w, y=y[:rows], ws=buf[:max(need, 16)])
+    torch.cuda.synchronize()
+    assert (buf[need:] == 77).all() and (y[rows:] == 3.0).all()
+    if dtype == torch.float32:
+        assert need > 0
+
+
 def test_operands_past_4_gib():
     """Row buffers past 32-bit offsets: gathered rows from the far end of x, and a
     buffer with many row tiles."""

@@ -556,6 +556,13 @@ class MoELayerGraph:
 # workspaces that it allocates belong to that stream. Tensors made on another stream
 # are the caller's to order.
 
+# Handle of a device's current stream, and the current device. The public
+# torch.cuda.current_stream() builds a Stream object, 2.8 us of a call that takes 7;
+# torch's own generated code takes these.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
 ACTS = {"none": 0, "gelu": 1, "silu": 2, "geglu": 3, "swiglu": 4}
@@ -567,6 +574,12 @@ def _enum(table, value, name: str) -> int:
     if code is None:
         raise ValueError(f"{name} must be one of {', '.join(map(repr, table))}, got {value!r}")
     return code
+
+
+def _shape(t, name: str, ndim: int):
+    if isinstance(t, torch.Tensor) and t.dim() == ndim:
+        return t.shape
+    return _dims(t, name, ndim)  # raises
 
 
 def _ptr(t, name: str, shape, dtype, device):
@@ -609,17 +622,10 @@ def _other_stream(device, stream):
     if device.type != "cuda":
         raise ValueError(f"the tensors must be GPU tensors, got {device}")
     if stream is None:
-        return None if device.index == torch.cuda.current_device() else torch.cuda.current_stream(device)
+        return None if device.index == _current_device() else torch.cuda.current_stream(device)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     return None if stream == torch.cuda.current_stream() else stream
-
-
-# Handle of a device's current stream. The public torch.cuda.current_stream() builds
-# a Stream object for it, 2.8 us of a call that takes 7; torch's own generated code
-# takes this one.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def moe_norm(x, weight=None, bias=None, eps: float = 1e-6, kind: str = "rms", out=None,
@@ -627,7 +633,7 @@ def moe_norm(x, weight=None, bias=None, eps: float = 1e-6, kind: str = "rms", ou
     """Norm of every row of x [T,H]: "rms" or "layer", times weight, plus bias.
 
     bf16 or fp32, any H up to 16384; ``out`` may be x itself. Returns out."""
-    T, H = _dims(x, "x", 2)
+    T, H = _shape(x, "x", 2)
     dev, dtype = x.device, x.dtype
     dt, code = _dtype_code(x), _enum(NORM_KINDS, kind, "kind")
     xp = _ptr(x, "x", (T, H), dtype, dev)
@@ -653,7 +659,7 @@ def moe_norm_residual(y, res, weight=None, bias=None, gate=None, scale: float = 
     y, res [T,H]; kind / next_kind "none", "rms" or "layer"; gate None, [T,1]
     (one value a row), [H] or [T,H]. Returns (h, norm of h or None). res_out may
     be res itself, next_out y itself."""
-    T, H = _dims(y, "y", 2)
+    T, H = _shape(y, "y", 2)
     dev, dtype, row = y.device, y.dtype, (H,)
     dt = _dtype_code(y)
     code, ncode = _enum(NORM_KINDS, kind, "kind"), _enum(NORM_KINDS, next_kind, "next_kind")
@@ -705,8 +711,8 @@ def moe_route_grouped(x, wg, bias, k: int, score: str = "sigmoid", groups: int =
     moves the choice only, and the choice limited to the topk_groups best of
     ``groups`` groups of experts (by their ``group_top`` largest biased scores).
     Returns (topk_idx int32 [T,k], topk_w fp32 [T,k])."""
-    T, H = _dims(x, "x", 2)
-    E = _dims(wg, "wg", 2)[0]
+    T, H = _shape(x, "x", 2)
+    E = _shape(wg, "wg", 2)[0]
     dev, dtype = x.device, x.dtype
     dt, code = _dtype_code(x), _enum(SCORES, score, "score")
     xp, wp = _ptr(x, "x", (T, H), dtype, dev), _ptr(wg, "wg", (E, H), dtype, dev)
@@ -743,10 +749,10 @@ def moe_linear(x, w, bias=None, act: str = "none", residual=None, y=None, ws=Non
     fp32); act "none", "gelu" (erf) or "silu". Gated: act "geglu" or "swiglu"
     with w [2,N,K] and bias [2,N], y = act(gate half) * other half + residual.
     y may be residual itself. Returns y."""
-    M, K = _dims(x, "x", 2)
+    M, K = _shape(x, "x", 2)
     code = _enum(ACTS, act, "act")
     two = (2,) if code >= 3 else ()
-    N = _dims(w, "w", 2 + len(two))[-2]
+    N = _shape(w, "w", 2 + len(two))[-2]
     dev, dtype = x.device, x.dtype
     dt = _dtype_code(x)
     xp, wp = _ptr(x, "x", (M, K), dtype, dev), _ptr(w, "w", (*two, N, K), dtype, dev)
@@ -759,7 +765,7 @@ def moe_linear(x, w, bias=None, act: str = "none", residual=None, y=None, ws=Non
     L = lib()
     wsp, wsn, ws = _ws(L.moe_linear_workspace_bytes(M, N, K, code, dt), dev, ws)
     if y is None:
-        y = torch.empty((M, N), dtype=dtype, device=dev)
+        y = x.new_empty((M, N))
         yp = y.data_ptr()
     _check("moe_linear", L.moe_linear(xp, wp, bp, code, rp, M, N, K, dt, yp, wsp, wsn,
                                       _raw_stream(dev.index)))
@@ -782,10 +788,10 @@ def moe_linear_grouped(x, offsets, w, bias=None, act: str = "none", residual=Non
     the token rows [T,K] and row p reads x[perm[p] // k]. rows (default: all of the
     buffer, T*k with perm) is an upper bound of offsets[E]; rows of y past
     offsets[E] are left as they were. Returns y [rows,N]."""
-    T, K = _dims(x, "x", 2)
+    T, K = _shape(x, "x", 2)
     code = _enum(ACTS, act, "act")
     two = (2,) if code >= 3 else ()
-    dims = _dims(w, "w", 3 + len(two))
+    dims = _shape(w, "w", 3 + len(two))
     E, N = dims[0], dims[-2]
     dev, dtype = x.device, x.dtype
     dt = _dtype_code(x)
@@ -794,7 +800,7 @@ def moe_linear_grouped(x, offsets, w, bias=None, act: str = "none", residual=Non
         rows = most
     if not 1 <= rows <= most:
         raise ValueError(f"rows {rows} outside [1, {most}]")
-    if perm is not None and _dims(perm, "perm", 1)[0] < rows:
+    if perm is not None and _shape(perm, "perm", 1)[0] < rows:
         raise ValueError(f"perm must have at least rows = {rows} entries")
     xp, wp = _ptr(x, "x", (T, K), dtype, dev), _ptr(w, "w", (E, *two, N, K), dtype, dev)
     fp = _ptr(offsets, "offsets", (E + 1,), torch.int32, dev)
@@ -808,7 +814,7 @@ def moe_linear_grouped(x, offsets, w, bias=None, act: str = "none", residual=Non
     L = lib()
     wsp, wsn, ws = _ws(L.moe_linear_grouped_workspace_bytes(E, rows, N, K, code, dt), dev, ws)
     if y is None:
-        y = torch.empty((rows, N), dtype=dtype, device=dev)
+        y = x.new_empty((rows, N))
         yp = y.data_ptr()
     _check("moe_linear_grouped", L.moe_linear_grouped(
         xp, pp, k, T, fp, E, rows, wp, bp, code, rp, N, K, dt, yp, wsp, wsn,

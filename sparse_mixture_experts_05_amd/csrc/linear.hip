@@ -466,11 +466,16 @@ LinPlan lin_plan(const LinArgs& a) {
                                                    : std::max(idle, full * rest / 256)));
   };
   const double hbm = 2.0 * ((double)a.M * a.K + live * cols * a.K) / 5.3e6;
+  // What a call costs its caller: the GPU's time, but in a run of calls no less than the
+  // host's for its launches (9 us for one, 13 for two and a workspace); a tenth of the
+  // GPU's own time decides between equals.
+  auto cost = [](double us, bool two) { return std::max(us, two ? 13.0 : 9.0) + 0.1 * us; };
   LinPlan best{kRows, 1};
-  double t = 3.2 + std::max({1.1 * hbm, a.K / 1000.0,
-                             row_tiles(16) * (a.N / 16) * (16 * h + std::min(16.0, a.M / live)) * a.K * 2 / 8.5e6});
+  double t = cost(3.2 + std::max({1.1 * hbm, a.K / 1000.0,
+                             row_tiles(16) * (a.N / 16) * (16 * h + std::min(16.0, a.M / live)) * a.K * 2 / 8.5e6}), false);
   auto take = [&](LinPath path, int nks, double us) {
-    if (us < t) t = us, best = LinPlan{path, nks};
+    const double c = cost(us, nks > 1 || (path >= kBigHalf && a.offsets));
+    if (c < t) t = c, best = LinPlan{path, nks};
   };
   const double tiles = row_tiles(64) * std::ceil(cols / 64);
   const double rows_l2 = 0.3 * 2.0 * a.M * a.K * std::ceil(cols / 64) / 8e6;

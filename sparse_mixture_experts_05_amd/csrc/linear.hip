@@ -426,26 +426,27 @@ int f32_slices(const LinArgs& a) {
 // experts with evenly drawn rows):
 //                        rows    64x64 (slices)   256x128   256x256
 //   1 x 4096 x 4096       8.7     11.7 (8)           41        44
-//   64 x 4096 x 4096              14.2 (4)           41        50
-//   256 x 4096 x 4096             23.8 (2)           44        69
-//   512 x 4096 x 4096             32.9 (1)           44        70
-//   1024 x 4096 x 4096            60.2 (1)           45        70
-//   2048 x 4096 x 4096           139   (1)           60        74
-//   4096 x 4096 x 4096           309   (1)          117       105
+//   64 x 4096 x 4096              14.0 (4)           43        51
+//   256 x 4096 x 4096             23.7 (2)           44        73
+//   512 x 4096 x 4096             33.9 (1)           45        73
+//   1024 x 4096 x 4096            61.7 (1)           47        73
+//   2048 x 4096 x 4096           140   (1)           58        75
+//   3000 x 4096 x 4096           219   (1)           97        81
+//   4096 x 4096 x 4096           305   (1)          114        96
 //   64 x 1024 x 1024      5.0      8.1 (8)           15        19
-//   2048 x 512 x 4096             27.7 (1)           42        68
+//   2048 x 512 x 4096             26.4 (1)           44        73
 //   E 8, 64 rows, 1024 x 1024    7.1     10.0 (1)    15        18
-//   E 8, 512 rows, 4096 x 4096           60.8 (1)    62        76
-//   E 8, 1024 rows, 4096 x 4096         101   (1)    68        83
-//   E 8, 8192 rows, 4096 x 4096         530   (1)   285       274
-//   E 128, 1024 rows, 1024 x 4096       190   (1)   229       188
-//   E 64, 16384 rows, 1024 x 1024        85   (1)    65        58
+//   E 8, 512 rows, 4096 x 4096           61.4 (1)    68        77
+//   E 8, 1024 rows, 4096 x 4096          93   (1)    72        88
+//   E 8, 8192 rows, 4096 x 4096         525   (1)   273       257
+//   E 128, 1024 rows, 1024 x 4096       184   (1)   246       191
+//   E 64, 16384 rows, 1024 x 1024        81   (1)    65        57
 // A stage is 64 k. Few-row kernel: every block of 16 rows x 16 columns reads both
 // operands from the caches (8.5 TB/s), and a wave walks a quarter of K (1 us per
 // 1000). 64x64 tiles: 0.36 us a stage while fewer than 1.75 workgroups share a CU,
 // then in proportion, and a third of the time in which every column tile reads its rows
 // from L2 (8 TB/s) does not hide; slices add a launch (3 us) and their partials' round trip. The large tiles run one
-// workgroup a CU: 0.55 or 0.94 us a stage on an idle chip, 0.9 or 1.5 when every CU
+// workgroup a CU: 0.56 or 1 us a stage on an idle chip, 0.83 or 1.38 when every CU
 // runs one (power and cache traffic). Of the lesser of work and weight stream a tenth
 // does not hide behind the other.
 LinPlan lin_plan(const LinArgs& a) {
@@ -486,7 +487,7 @@ LinPlan lin_plan(const LinArgs& a) {
     take(kTile64, nks, std::max(us, 3.0 + hbm) + 0.1 * std::min(us, hbm) + rows_l2);
   }
   if (big_ok(a)) {
-    const double half = big(128, 0.55, 0.9), whole = big(256, 0.94, 1.5);
+    const double half = big(128, 0.56, 0.83), whole = big(256, 1.0, 1.38);
     take(kBigHalf, 1, std::max(half, 8.0 + 1.1 * hbm) + 0.1 * std::min(half, hbm));
     take(kBig, 1, std::max(whole, 8.0 + hbm) + 0.1 * std::min(whole, hbm));
   }

@@ -3,18 +3,22 @@
 //
 // A workgroup of 4 waves (one per SIMD) computes 256 rows x 256 weight rows;
 // wave w the 128 x 128 block (rows (w / 2) * 128, weight rows (w % 2) * 128) as
-// 4 x 4 accumulators of v_mfma_f32_32x32x16_bf16 (all 256 accumulation
-// registers). The weights are the MFMA's A operand and the rows its B, so a lane
+// 8 x 8 accumulators of v_mfma_f32_16x16x32_bf16 (all 256 accumulation
+// registers). Of the two shapes of this rate it is the one that draws less power: on
+// random data, registers only, it holds 1790-1850 TFLOP/s where v_mfma_f32_32x32x16
+// holds 1500-1600 (both 2235 on zeros), and large products run at that limit: a
+// 64-deep stage of 256 tiles takes 1.37 us on random data and 0.97 on zeros (1.53 and
+// 0.91 with 32x32x16). The weights are the MFMA's A operand and the rows its B, so a lane
 // ends with runs of 4 consecutive output columns of one row: bias and residual
 // come and the result goes 8 bytes at a time, with no exchange between lanes.
-// A gated product gives each wave the gate rows of 64 columns in its first two
-// weight sub-tiles and their up rows in the other two: both factors of an output
+// A gated product gives each wave the gate rows of 64 columns in its first four
+// weight sub-tiles and their up rows in the other four: both factors of an output
 // meet in one lane, and the tile has 128 output columns.
 //
 // With one wave per SIMD nothing else feeds the matrix core, so the stage is
-// hand-ordered: the 8 fragment reads of the next 16-deep k slice and the LDS
+// hand-ordered: the 16 fragment reads of the next 32-deep k slice and the LDS
 // copies of the stage after the next (global_load_lds, the rows in two stage
-// buffers, the weights in three) sit between the slice's 16 MFMAs, held there by
+// buffers, the weights in three) sit between the slice's 64 MFMAs, held there by
 // sched_barrier.
 //
 // Tile order and the split of a long K in the last round are plan.hpp's. A
@@ -139,24 +143,24 @@ __device__ __forceinline__ bool tile_of(const LinArgs& a, bool gt, int i, bool r
   return kind == 0;
 }
 
-// Weight row of row r of a tile of 64 SN weight rows: the expert's row n0 + r, or
-// for a gated product (n0, N in output columns) wave half r / (32 SN), sub-tile
-// (r / 32) % SN: half of them gate rows, then the up rows of the same columns.
-template <bool GT, int SN>
+// Weight row of row r of a tile of 32 TN weight rows: the expert's row n0 + r, or
+// for a gated product (n0, N in output columns) wave half r / (16 TN), sub-tile
+// (r / 16) % TN: half of them gate rows, then the up rows of the same columns.
+template <bool GT, int TN>
 __device__ __forceinline__ size_t tile_weight_row(int r, int n0, int N) {
   if constexpr (!GT) return (size_t)min(n0 + r, N - 1);
-  constexpr int HS = SN / 2;
-  const int j = (r >> 5) % SN;
-  return (size_t)(j / HS) * N + min(n0 + r / (32 * SN) * (32 * HS) + j % HS * 32 + (r & 31), N - 1);
+  constexpr int HS = TN / 2;
+  const int j = (r >> 4) % TN;
+  return (size_t)(j / HS) * N + min(n0 + r / (16 * TN) * (16 * HS) + j % HS * 16 + (r & 15), N - 1);
 }
 
-template <int ACT, bool RES, int SN>
+template <int ACT, bool RES, int TN>
 __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
   constexpr bool GT = ACT == kActGeglu || ACT == kActSwiglu;
   constexpr int NW = 4, BK = 64;
   constexpr int ROWB = BK * 2;                 // 128 bytes = 8 chunks of 16
-  constexpr int SM = 4;                        // 32 x 32 sub-tiles of a wave: 4 x SN
-  constexpr int BN = 64 * SN;                  // weight rows of a tile
+  constexpr int TM = 8;                        // 16 x 16 sub-tiles of a wave: 8 x TN
+  constexpr int BN = 32 * TN;                  // weight rows of a tile
   constexpr int RPI = 8;                       // rows per copy instruction
   constexpr int A_INST = BM / RPI / NW, B_INST = BN / RPI / NW;  // copies per wave per stage
   constexpr int A_STAGE = BM * ROWB, B_STAGE = BN * ROWB;
@@ -197,7 +201,7 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
   for (int q = 0; q < B_INST; ++q) {
     const int r = (wave * B_INST + q) * RPI + lrow;
     const int c = (lane & 7) ^ ((r >> 1) & 7);
-    ov[A_INST + q] = (uint32_t)((tile_weight_row<GT, SN>(r, n0, N) * K + c * 8) * 2);
+    ov[A_INST + q] = (uint32_t)((tile_weight_row<GT, TN>(r, n0, N) * K + c * 8) * 2);
   }
   const int KT0 = K / BK;
   const int kbase = t.ks * KT0 / t.spl;
@@ -209,13 +213,13 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
   const uint8_t* B8 = reinterpret_cast<const uint8_t*>(wb);
   auto a_buf = [&](int kt) { return smem + (kt & 1) * A_STAGE; };
   auto b_buf = [&](int slot) { return smem + 2 * A_STAGE + slot * B_STAGE; };
-  // copy q of stage kt (q < 8: rows into row buffer kt & 1; else weights into
-  // weight buffer bslot)
-  auto copy = [&](int kt, int bslot, int q) {
+  // copy q of stage kt: rows (q < 8) into row buffer slot, else weights into weight
+  // buffer slot
+  auto copy = [&](int kt, int slot, int q) {
     const size_t kb = (size_t)(kbase + kt) * (BK * 2);
     const uint32_t m0 =
-        q < A_INST ? lds0 + (uint32_t)((kt & 1) * A_STAGE + (wv * A_INST + q) * RPI * ROWB)
-                   : lds0 + (uint32_t)(2 * A_STAGE + bslot * B_STAGE +
+        q < A_INST ? lds0 + (uint32_t)(slot * A_STAGE + (wv * A_INST + q) * RPI * ROWB)
+                   : lds0 + (uint32_t)(2 * A_STAGE + slot * B_STAGE +
                                        (wv * B_INST + q - A_INST) * RPI * ROWB);
     const uint8_t* base = (q < A_INST ? A8 : B8) + kb;
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
@@ -224,71 +228,66 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
                  : "memory");
   };
 
-  f32x16_t acc[SM][SN];  // [row sub-tile][weight sub-tile]
+  f32x4_t acc[TM][TN];  // [row sub-tile][weight sub-tile]
 #pragma unroll
-  for (int i = 0; i < SM; ++i)
+  for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < SN; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // Every fragment row of this lane is lane % 32 of a 32-row sub-tile: one LDS
-  // offset per operand, the sub-tiles 32 rows apart (a constant of the read).
-  const int fa0 = (wm * 128 + (lane & 31)) * ROWB;
-  const int fb0 = (wn * (BN / 2) + (lane & 31)) * ROWB;
+  // Every fragment row of this lane is lane % 16 of a 16-row sub-tile: one LDS offset
+  // per operand, the sub-tiles 16 rows apart (a constant of the read).
+  const int fa0 = (wm * 128 + (lane & 15)) * ROWB;
+  const int fb0 = (wn * (BN / 2) + (lane & 15)) * ROWB;
   const int sw = (lane >> 1) & 7;
-  const int khalf = lane >> 5;
-  // row sub-tiles of this wave that hold data: all of them except in a segment's
-  // last, partial row tile (a wave-uniform count)
-  const int nsub = __builtin_amdgcn_readfirstlane(min(SM, max(0, (M - wm * 128 + 31) / 32)));
+  const int kq = lane >> 4;
+  // pairs of row sub-tiles of this wave that hold data: all of them except in a
+  // segment's last, partial row tile (a wave-uniform count)
+  const int nsub = __builtin_amdgcn_readfirstlane(min(TM / 2, max(0, (M - wm * 128 + 31) / 32)));
 
-  u32x4_t ca[SM], cb[SN], na[SM], nb[SN];
-  constexpr int NM = SM * SN, NR = SM + SN;  // MFMAs, fragment reads of a k slice
-  static_assert(NR <= NM, "a read after each of the first MFMAs");
+  u32x4_t ca[TM], cb[TN], na[TM], nb[TN];
+  constexpr int NM = TM * TN, NR = TM + TN;  // MFMAs, fragment reads of a k slice
   // fragment read r of k slice ks: b0, a0, the other b, the other a (the order of
   // first use)
-  auto read_r = [&](const uint8_t* sa, const uint8_t* sb, int ks, int r, u32x4_t (&fa_)[SM],
-                    u32x4_t (&fb_)[SN]) {
-    const int off = ((ks * 2 + khalf) ^ sw) << 4;
+  auto read_r = [&](const uint8_t* sa, const uint8_t* sb, int ks, int r, u32x4_t (&fa_)[TM],
+                    u32x4_t (&fb_)[TN]) {
+    const int off = ((ks * 4 + kq) ^ sw) << 4;
     if (r == 0) fb_[0] = ld16(sb + fb0 + off);
     else if (r == 1) fa_[0] = ld16(sa + fa0 + off);
-    else if (r <= SN) fb_[r - 1] = ld16(sb + fb0 + (r - 1) * 32 * ROWB + off);
-    else fa_[r - SN] = ld16(sa + fa0 + (r - SN) * 32 * ROWB + off);
+    else if (r <= TN) fb_[r - 1] = ld16(sb + fb0 + (r - 1) * 16 * ROWB + off);
+    else fa_[r - TN] = ld16(sa + fa0 + (r - TN) * 16 * ROWB + off);
   };
   // NS: row sub-tiles with data, a compile-time count, so that a partial tile's
   // loop has no branch between its MFMAs (its empty sub-tiles are skipped)
   auto main_loop = [&](auto ns_tag) {
     constexpr int NS = decltype(ns_tag)::value;
-    // one k slice: NM MFMAs on (fa_, fb_); after each of the first NR a read of
-    // slice rks of the buffers (rsa, rsb) into (ra_, rb_); copies q0 .. q1-1
-    // spread evenly over them (rows of stage akt for q < 8, weights of stage
-    // bkt into slot bslot for q >= 8)
-    auto slice = [&](const u32x4_t (&fa_)[SM], const u32x4_t (&fb_)[SN], const uint8_t* rsa,
-                     const uint8_t* rsb, int rks, u32x4_t (&ra_)[SM], u32x4_t (&rb_)[SN],
-                     auto q0c, auto q1c, int akt, int bkt, int bslot) {
+    // one k slice: NM MFMAs on (fa_, fb_); over the first half of them the
+    // reads of slice rks of the buffers (rsa, rsb) into (ra_, rb_); copies q0 .. q1-1
+    // (of stage ckt into slot) spread evenly
+    auto slice = [&](const u32x4_t (&fa_)[TM], const u32x4_t (&fb_)[TN], const uint8_t* rsa,
+                     const uint8_t* rsb, int rks, u32x4_t (&ra_)[TM], u32x4_t (&rb_)[TN],
+                     auto q0c, auto q1c, int ckt, int slot) {
       constexpr int q0 = decltype(q0c)::value, nq = decltype(q1c)::value - q0;
       static_for<NM>([&](auto mc) {
-        constexpr int m = decltype(mc)::value, i = m / SN, j = m % SN;
-        if constexpr (i < NS)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(fb_[j]), as_bf16x8(fa_[i]),
-                                                              acc[i][j], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (m < NR) {
-          read_r(rsa, rsb, rks, m, ra_, rb_);
+        constexpr int m = decltype(mc)::value, i = m / TN, j = m % TN;
+        if constexpr (i < NS) acc[i][j] = mma16<uint16_t>(fb_[j], fa_[i], acc[i][j]);
+        constexpr int r = (m * NR * 2 + NM - 1) / NM;  // the first read not before m
+        constexpr bool reads = r < NR && r * NM / (NR * 2) == m;
+        constexpr bool copies = (m * nq) / NM != ((m + 1) * nq) / NM;
+        if constexpr (reads || copies || m % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+        if constexpr (reads) {
+          read_r(rsa, rsb, rks, r, ra_, rb_);
           __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (nq > 0 && (m * nq) / NM != ((m + 1) * nq) / NM) {
+        if constexpr (copies) {
           constexpr int q = q0 + (m * nq) / NM;
-          copy(q < A_INST ? akt : bkt, bslot, q);
+          copy(ckt, slot, q);
           __builtin_amdgcn_sched_barrier(0);
         }
       });
     };
-    using Q0 = std::integral_constant<int, 0>;  // copies: rows, then weights in three parts
+    using Q0 = std::integral_constant<int, 0>;  // copies: rows, then weights
     using Q1 = std::integral_constant<int, A_INST>;
-    using Q2 = std::integral_constant<int, A_INST + (B_INST * 3 + 7) / 8>;
-    using Q3 = std::integral_constant<int, A_INST + (B_INST * 6 + 7) / 8>;
-    using Q4 = std::integral_constant<int, A_INST + B_INST>;
+    using Q2 = std::integral_constant<int, A_INST + B_INST>;
     // prologue: stages 0 and 1 and the weights of stage 2 in flight, in the order
     // the waits count them; stage 0 landed everywhere
     static_for<A_INST + B_INST>([&](auto q) { copy(0, 0, decltype(q)::value); });
@@ -305,50 +304,43 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
       const int bs1 = bs == 2 ? 0 : bs + 1;
       const int bsp = bs == 0 ? 2 : bs - 1;  // slot of stage kt-1 = stage kt+2
       const int k2 = min(kt + 2, last);
-      const uint8_t* sa = a_buf(kt);
-      const uint8_t* sb = b_buf(bs);
-      slice(ca, cb, sa, sb, 1, na, nb, Q1{}, Q2{}, 0, k2, bsp);
-      slice(na, nb, sa, sb, 2, ca, cb, Q2{}, Q3{}, 0, k2, bsp);
-      slice(ca, cb, sa, sb, 3, na, nb, Q3{}, Q4{}, 0, k2, bsp);
+      slice(ca, cb, a_buf(kt), b_buf(bs), 1, na, nb, Q1{}, Q2{}, k2, bsp);
       // stage kt+1 landed for this wave (only the weights of stage kt+2 issued
       // above may still be in flight), then for everyone; stage kt fully read, so
       // row buffer kt & 1 is free
       wait_vmcnt<B_INST>();
       lds_barrier();
-      slice(na, nb, a_buf(kt + 1), b_buf(bs1), 0, ca, cb, Q0{}, Q1{}, k2, 0, 0);
+      slice(na, nb, a_buf(kt + 1), b_buf(bs1), 0, ca, cb, Q0{}, Q1{}, k2, kt & 1);
       bs = bs1;
     }
     wait_vmcnt<0>();
     // every accumulator leaves each variant in its accumulation registers, so the
     // variants meet the epilogue with one register assignment
 #pragma unroll
-    for (int i = 0; i < SM; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int j = 0; j < SN; ++j) asm volatile("" : "+a"(acc[i][j]));
+      for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[i][j]));
   };
   switch (nsub) {
-    case 4: main_loop(std::integral_constant<int, 4>{}); break;
-    case 3: main_loop(std::integral_constant<int, 3>{}); break;
-    case 2: main_loop(std::integral_constant<int, 2>{}); break;
-    case 1: main_loop(std::integral_constant<int, 1>{}); break;
+    case 4: main_loop(std::integral_constant<int, 8>{}); break;
+    case 3: main_loop(std::integral_constant<int, 6>{}); break;
+    case 2: main_loop(std::integral_constant<int, 4>{}); break;
+    case 1: main_loop(std::integral_constant<int, 2>{}); break;
     default: main_loop(std::integral_constant<int, 0>{}); break;
   }
 
-  // 32x32 D layout: lane holds row lane % 32 of x (column of D) and the weight
-  // rows (v / 4) * 8 + (lane / 32) * 4 + v % 4 of each sub-tile.
+  // 16x16 D layout: lane holds row lane % 16 of x (column of D) and the weight rows
+  // 4 (lane / 16) .. + 3 of each sub-tile.
   if (t.unit0 >= 0) {
     // one K slice of a split tile: 16 bytes per lane in accumulator order; the
     // reduce launch sums the slices and runs the epilogue
     float* P = a.part + (size_t)(t.unit0 + t.ks) * BM * BN + wave * (BM * BN / 4) + lane * 4;
 #pragma unroll
-    for (int i = 0; i < SM; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int j = 0; j < SN; ++j) {
+      for (int j = 0; j < TN; ++j) {
         asm volatile("" : "+a"(acc[i][j]));
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<f32x4_t*>(P + ((i * SN + j) * 4 + q) * 256) =
-              f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        *reinterpret_cast<f32x4_t*>(P + (i * TN + j) * 256) = acc[i][j];
       }
     return;
   }
@@ -359,10 +351,10 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
   constexpr int SWZ = (CROWB / 16 < 16 ? CROWB / 16 : 16) - 1;
   const uint16_t* bias = static_cast<const uint16_t*>(a.bias);
   const uint16_t* res = static_cast<const uint16_t*>(a.res);
-  const int lr = wm * 128 + (lane & 31);            // first row of this lane in the tile
-  const int lc = wn * (BC / 2) + khalf * 4;         // first column
-  constexpr int STEPS = (GT ? SN / 2 : SN) * 4;     // (weight sub-tile, 4-column run) pairs
-  // the bias of every run up front (a branch in every step would have the
+  const int lr = wm * 128 + (lane & 15);            // first row of this lane in the tile
+  const int lc = wn * (BC / 2) + kq * 4;            // first column
+  constexpr int STEPS = GT ? TN / 2 : TN;           // weight sub-tiles that give outputs
+  // the bias of every sub-tile up front (a branch in every step would have the
   // compiler spill accumulators)
   uint2 bgs[STEPS], bus[GT ? STEPS : 1];
 #pragma unroll
@@ -374,7 +366,7 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
     bias += (size_t)t.e * (GT ? 2 : 1) * N + n0;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-      const int cc = min(lc + (s >> 2) * 32 + (s & 3) * 8, nvalid - 4);
+      const int cc = min(lc + s * 16, nvalid - 4);
       bgs[s] = *reinterpret_cast<const uint2*>(bias + cc);
       if constexpr (GT) bus[s] = *reinterpret_cast<const uint2*>(bias + N + cc);
     }
@@ -382,29 +374,27 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
   if constexpr (RES) res += (size_t)t.row0 * N + n0;
   lds_barrier();  // every wave has read the last stage
   static_for<STEPS>([&](auto sc) {
-    constexpr int s = decltype(sc)::value, j = s >> 2, q = s & 3;
-    const int col = lc + j * 32 + q * 8;
-    const Out4 bg = widen4(bgs[s]), bu = widen4(bus[GT ? s : 0]);
-    Out4 rv[SM] = {};
+    constexpr int j = decltype(sc)::value;
+    const int col = lc + j * 16;
+    const Out4 bg = widen4(bgs[j]), bu = widen4(bus[GT ? j : 0]);
+    uint2 rv[TM];
     if constexpr (RES) {
 #pragma unroll
-      for (int i = 0; i < SM; ++i)
-        rv[i] = widen4(*reinterpret_cast<const uint2*>(res + (size_t)min(lr + i * 32, M - 1) * N +
-                                                       min(col, nvalid - 4)));
+      for (int i = 0; i < TM; ++i)
+        rv[i] = *reinterpret_cast<const uint2*>(res + (size_t)min(lr + i * 16, M - 1) * N +
+                                                min(col, nvalid - 4));
     }
 #pragma unroll
-    for (int i = 0; i < SM; ++i) {
+    for (int i = 0; i < TM; ++i) {
       // pinned to the accumulation registers up to here: without this the compiler
       // reads all of them out before the first branch of the epilogue, and spills
       asm volatile("" : "+a"(acc[i][j]));
-      if constexpr (GT) asm volatile("" : "+a"(acc[i][j + SN / 2]));
-      const f32x16_t& g = acc[i][j];
-      const f32x16_t& u = acc[i][GT ? j + SN / 2 : j];
-      const uint2 o = pack4(finish4<true>(ACT, f32x4_t{g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]},
-                                   f32x4_t{u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]},
-                                   bg, bu, RES, rv[i]));
-      const int row = lr + i * 32;
-      *reinterpret_cast<uint2*>(smem + row * CROWB + (((col >> 3) ^ (row & SWZ)) << 4) + khalf * 8) = o;
+      if constexpr (GT) asm volatile("" : "+a"(acc[i][j + TN / 2]));
+      Out4 r{};
+      if constexpr (RES) r = widen4(rv[i]);
+      const uint2 o = pack4(finish4<true>(ACT, acc[i][j], acc[i][GT ? j + TN / 2 : j], bg, bu, RES, r));
+      const int row = lr + i * 16;
+      *reinterpret_cast<uint2*>(smem + row * CROWB + (((col >> 3) ^ (row & SWZ)) << 4) + (kq & 1) * 8) = o;
     }
     __builtin_amdgcn_sched_barrier(0);
   });
@@ -426,10 +416,10 @@ __global__ __launch_bounds__(256, 1) void lin_big_kernel(LinArgs a) {
 // them), so the partials stream through many CUs.
 constexpr int kReduceParts = 8;
 
-template <int ACT, int SN>
+template <int ACT, int TN>
 __global__ __launch_bounds__(kThreads) void lin_reduce_kernel(LinArgs a) {
   constexpr bool GT = ACT == kActGeglu || ACT == kActSwiglu;
-  constexpr int BN = 64 * SN;
+  constexpr int BN = 32 * TN;
   __shared__ plan::Tables L;
   plan::Tile t;
   if (!tile_of<BN>(a, GT, blockIdx.x / kReduceParts, true, L, t)) return;
@@ -438,15 +428,15 @@ __global__ __launch_bounds__(kThreads) void lin_reduce_kernel(LinArgs a) {
   const int nvalid = N - n0;
   const float* P = a.part + (size_t)t.unit0 * BM * BN;
   const int spl = t.spl;
-  constexpr int JS = GT ? SN / 2 : SN;  // weight sub-tiles that give outputs
-  constexpr int RUNS = 4 * 4 * JS * 4 * 64;  // runs of 4 columns in a tile
+  constexpr int JS = GT ? TN / 2 : TN;  // weight sub-tiles that give outputs
+  constexpr int RUNS = 4 * 8 * JS * 64;  // runs of 4 columns in a tile
   for (int e = (blockIdx.x % kReduceParts) * kThreads + threadIdx.x; e < RUNS;
        e += kReduceParts * kThreads) {
-    // e = (((wave * 4 + i) * JS + j) * 4 + q) * 64 + lane, the partials' order
-    const int lane = e & 63, q = (e >> 6) & 3, j = (e >> 8) % JS, wi = (e >> 8) / JS;
-    const int wave = wi >> 2, i = wi & 3;
-    const int row = (wave >> 1) * 128 + i * 32 + (lane & 31);
-    const int col = (wave & 1) * (JS * 32) + j * 32 + q * 8 + (lane >> 5) * 4;
+    // e = ((wave * 8 + i) * JS + j) * 64 + lane, the partials' order
+    const int lane = e & 63, j = (e >> 6) % JS, wi = (e >> 6) / JS;
+    const int wave = wi >> 3, i = wi & 7;
+    const int row = (wave >> 1) * 128 + i * 16 + (lane & 15);
+    const int col = (wave & 1) * (JS * 16) + j * 16 + (lane >> 4) * 4;
     if (row >= t.M || col >= nvalid) continue;
     const float* src = P + (size_t)wave * (BM * BN / 4) + lane * 4;
     f32x4_t g{}, u{};
@@ -454,8 +444,8 @@ __global__ __launch_bounds__(kThreads) void lin_reduce_kernel(LinArgs a) {
 #pragma unroll
     for (int ks = 0; ks < plan::kMaxSplit; ++ks) {  // all loads first, from clamped slices
       const float* sl = src + (size_t)min(ks, spl - 1) * BM * BN;
-      vg[ks] = *reinterpret_cast<const f32x4_t*>(sl + ((i * SN + j) * 4 + q) * 256);
-      if constexpr (GT) vu[ks] = *reinterpret_cast<const f32x4_t*>(sl + ((i * SN + j + SN / 2) * 4 + q) * 256);
+      vg[ks] = *reinterpret_cast<const f32x4_t*>(sl + (i * TN + j) * 256);
+      if constexpr (GT) vu[ks] = *reinterpret_cast<const f32x4_t*>(sl + (i * TN + j + TN / 2) * 256);
     }
 #pragma unroll
     for (int ks = 0; ks < plan::kMaxSplit; ++ks)
@@ -488,39 +478,39 @@ BigLayout big_layout(const LinArgs& a) {
   return L;
 }
 
-template <int ACT, int SN>
+template <int ACT, int TN>
 hipError_t run_big(const LinArgs& a, hipStream_t s) {
   if (a.res != nullptr)
-    hipLaunchKernelGGL((lin_big_kernel<ACT, true, SN>), dim3(a.slots), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((lin_big_kernel<ACT, true, TN>), dim3(a.slots), dim3(kThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((lin_big_kernel<ACT, false, SN>), dim3(a.slots), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((lin_big_kernel<ACT, false, TN>), dim3(a.slots), dim3(kThreads), 0, s, a);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || a.part == nullptr) return err;
-  hipLaunchKernelGGL((lin_reduce_kernel<ACT, SN>), dim3(plan::kReduceSlots * kReduceParts),
+  hipLaunchKernelGGL((lin_reduce_kernel<ACT, TN>), dim3(plan::kReduceSlots * kReduceParts),
                      dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
-template <int SN>
-hipError_t launch_big_sn(LinArgs a, void* ws, hipStream_t s) {
-  const BigLayout L = big_layout<64 * SN>(a);
+template <int TN>
+hipError_t launch_big_tn(LinArgs a, void* ws, hipStream_t s) {
+  const BigLayout L = big_layout<32 * TN>(a);
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.part = L.split ? reinterpret_cast<float*>(base) : nullptr;
   a.slots = L.slots;
   if (a.offsets) {
     a.table = reinterpret_cast<const int4*>(base + L.table);
     const int n = L.slots + plan::kReduceSlots;
-    hipLaunchKernelGGL((lin_plan_kernel<64 * SN>), dim3((n + kThreads - 1) / kThreads), dim3(kThreads),
+    hipLaunchKernelGGL((lin_plan_kernel<32 * TN>), dim3((n + kThreads - 1) / kThreads), dim3(kThreads),
                        0, s, a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
   switch (a.act) {
-    case kActNone: return run_big<kActNone, SN>(a, s);
-    case kActGelu: return run_big<kActGelu, SN>(a, s);
-    case kActSilu: return run_big<kActSilu, SN>(a, s);
-    case kActGeglu: return run_big<kActGeglu, SN>(a, s);
-    default: return run_big<kActSwiglu, SN>(a, s);
+    case kActNone: return run_big<kActNone, TN>(a, s);
+    case kActGelu: return run_big<kActGelu, TN>(a, s);
+    case kActSilu: return run_big<kActSilu, TN>(a, s);
+    case kActGeglu: return run_big<kActGeglu, TN>(a, s);
+    default: return run_big<kActSwiglu, TN>(a, s);
   }
 }
 
@@ -542,7 +532,7 @@ size_t big_ws_bytes(const LinArgs& a, bool half) {
 }
 
 hipError_t launch_big(LinArgs a, bool half, void* ws, hipStream_t s) {
-  return half ? launch_big_sn<2>(a, ws, s) : launch_big_sn<4>(a, ws, s);
+  return half ? launch_big_tn<4>(a, ws, s) : launch_big_tn<8>(a, ws, s);
 }
 
 }  // namespace lin

@@ -95,12 +95,15 @@ __device__ __forceinline__ void lds_barrier() {
 // LDS at M0 + 16*i (M0 = the wave-uniform LDS address). Issued through asm so
 // the compiler's wait insertion does not treat every later LDS read as
 // aliasing the in-flight copy (which would drain the prefetch); completion is
-// tracked with explicit vmcnt waits (loads complete in issue order).
+// tracked with explicit vmcnt waits (loads complete in issue order). gfx950 needs an
+// instruction between the write of M0 and the copy that reads it, which the compiler
+// does not add inside asm.
 __device__ __forceinline__ void lds_dma16(const void* g, void* lds_uniform) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)(lds_uniform))));
   asm volatile(
       "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
       "global_load_lds_dwordx4 %0, off"
       :
       : "v"(g), "s"(m0)

@@ -422,8 +422,8 @@ typedef enum {
  * all dtype: device, read; y [M,N] dtype: device, written. y may be residual
  * itself, and overlaps no other input.
  * K % 64 == 0, N % 64 == 0, any M >= 1 whose tiles fit a launch (about M * N <
- * 2^36; else MOE_ERR_UNSUPPORTED). An output that overlaps x, or residual other
- * than being it, is MOE_ERR_INVALID_ARG.
+ * 2^36; else MOE_ERR_UNSUPPORTED). An output or workspace that overlaps another
+ * operand (other than y being residual) is MOE_ERR_INVALID_ARG.
  * ws / ws_bytes: device workspace of at least
  *   moe_linear_workspace_bytes(M,N,K,act,dtype) (NULL allowed when that is 0)
  */

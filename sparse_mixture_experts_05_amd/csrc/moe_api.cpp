@@ -41,7 +41,7 @@ extern "C" {
 const char* moe_status_string(int status) {
   switch (status) {
     case MOE_OK: return "ok";
-    case MOE_ERR_INVALID_ARG: return "invalid argument (null or misaligned pointer, non-positive size or bad dtype)";
+    case MOE_ERR_INVALID_ARG: return "invalid argument (null or misaligned pointer, non-positive size, bad dtype or an output over another operand)";
     case MOE_ERR_UNSUPPORTED: return "unsupported shape (needs 1<=E<=256, 1<=k<=min(E,8), H%64==0, F%64==0, T*k<2^31; norms: H<=16384; moe_route_grouped: E%groups==0, groups<=64, topk_groups<=groups, k<=topk_groups*E/groups; products: N%64==0, K%64==0)";
     case MOE_ERR_WORKSPACE: return "workspace missing or smaller than the size query returned";
     case MOE_ERR_HIP: return "HIP launch failed";
@@ -220,11 +220,22 @@ constexpr int kMaxGroupedT = 1 << 27;  // 16 threads a token in one grid dimensi
 bool norm_kind_ok(int kind) { return kind >= MOE_NORM_NONE && kind <= MOE_NORM_LAYER; }
 bool aligned_or_null(const void* p) { return !p || aligned16(p); }
 
-// Whether the n bytes at p and the m bytes at q share any (null: no).
+// Whether the n bytes at p and the m bytes at q share any (null or none: no).
 bool overlap(const void* p, size_t n, const void* q, size_t m) {
-  if (!p || !q) return false;
+  if (!p || !q || n == 0 || m == 0) return false;
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   return a < b + m && b < a + n;
+}
+// Buffers that a launch reads or writes, and whether the n bytes at p (which it writes)
+// share any with one of them.
+struct Span {
+  const void* p;
+  size_t n;
+};
+bool overlap_any(const void* p, size_t n, std::initializer_list<Span> others) {
+  for (const Span& o : others)
+    if (overlap(p, n, o.p, o.n)) return true;
+  return false;
 }
 size_t elem(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 
@@ -259,13 +270,18 @@ int run_linear(const void* x, const int32_t* perm, int k, int T, const int32_t* 
   if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned_or_null(bias) ||
       !aligned_or_null(residual) || !aligned_or_null(ws))
     return MOE_ERR_INVALID_ARG;
-  const size_t ny = (size_t)M * N * elem(dtype);
-  if (overlap(y, ny, x, (size_t)(perm ? T : M) * K * elem(dtype)) ||
-      (y != residual && overlap(y, ny, residual, ny)))
+  // other tiles still read what a tile's outputs or partials would write over
+  const size_t b = elem(dtype), ny = (size_t)M * N * b;
+  const size_t cols = (size_t)E * (act == MOE_ACT_GEGLU || act == MOE_ACT_SWIGLU ? 2 : 1) * N;
+  const Span sx{x, (size_t)(perm ? T : M) * K * b}, sw{w, cols * K * b}, sb{bias, cols * b};
+  const Span so{offsets, (size_t)(E + 1) * sizeof(int32_t)}, sp{perm, (size_t)M * sizeof(int32_t)};
+  if (overlap_any(y, ny, {sx, sw, sb, so, sp}) || (y != residual && overlap(y, ny, residual, ny)))
     return MOE_ERR_INVALID_ARG;
   const size_t need =
       moe::linear_ws_bytes(E, M, N, K, act, offsets != nullptr, dtype == MOE_BF16);
   if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (overlap_any(ws, need, {sx, sw, sb, so, sp, Span{residual, ny}, Span{y, ny}}))
+    return MOE_ERR_INVALID_ARG;
   return from_hip(moe::launch_linear(x, perm, k, T, offsets, E, M, N, K, w, bias, act, residual,
                                      dtype == MOE_BF16, y, ws, as_stream(stream)));
 }

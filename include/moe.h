@@ -330,7 +330,8 @@ typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_nor
  * x      [rows,H] dtype          device, read
  * weight [H] dtype or NULL       device, read (NULL = 1)
  * bias   [H] dtype or NULL       device, read (NULL = 0)
- * out    [rows,H] dtype          device, written; may be x itself
+ * out    [rows,H] dtype          device, written; may be x itself (any other
+ *                                overlap with an input is MOE_ERR_INVALID_ARG)
  * eps: finite, >= 0. All pointers 16-byte aligned. No workspace.
  */
 int moe_norm(const void* x, const void* weight, const void* bias, int rows, int H, float eps,
@@ -354,9 +355,10 @@ typedef enum {
  *   for MOE_GATE_NONE): device, read
  * weight, bias, next_weight, next_bias [H] dtype or NULL: device, read; NULL
  *   with the kind MOE_NORM_NONE
- * res_out, next_out [rows,H] dtype: device, written. res_out may be res itself
- *   and next_out may be y itself; any other overlap of the outputs with each
- *   other, y or res is MOE_ERR_INVALID_ARG. next_out NULL with
+ * res_out, next_out [rows,H] dtype: device, written. res_out may be res itself,
+ *   next_out may be y itself and either may be a full gate itself; any other
+ *   overlap of an output with the other one or an input is
+ *   MOE_ERR_INVALID_ARG. next_out NULL with
  *   next_kind MOE_NORM_NONE.
  * scale: finite. eps, H, alignment and arithmetic as moe_norm.
  */

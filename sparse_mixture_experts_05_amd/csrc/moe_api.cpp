@@ -295,8 +295,9 @@ int moe_norm(const void* x, const void* weight, const void* bias, int rows, int 
     return MOE_ERR_INVALID_ARG;
   const int st = check_norm(rows, H, eps, dtype);
   if (st != MOE_OK) return st;
-  const size_t n = (size_t)rows * H * elem(dtype);
-  if (out != x && overlap(out, n, x, n)) return MOE_ERR_INVALID_ARG;
+  const size_t n = (size_t)rows * H * elem(dtype), row = (size_t)H * elem(dtype);
+  if ((out != x && overlap(out, n, x, n)) || overlap_any(out, n, {{weight, row}, {bias, row}}))
+    return MOE_ERR_INVALID_ARG;
   return from_hip(moe::launch_norm(x, weight, bias, rows, H, eps, kind, dtype == MOE_BF16, out,
                                    as_stream(stream)));
 }
@@ -322,6 +323,13 @@ int moe_norm_residual(const void* y, int kind, const void* weight, const void* b
   if (overlap(res_out, n, y, n) || overlap(next_out, n, res, n) || overlap(next_out, n, res_out, n) ||
       (res_out != res && overlap(res_out, n, res, n)) || (next_out != y && overlap(next_out, n, y, n)))
     return MOE_ERR_INVALID_ARG;
+  // what other rows still read; a full gate is read where it would be written, like res
+  const size_t b = elem(dtype), row = H * b;
+  const size_t ng = gate_mode == MOE_GATE_FULL ? n : gate_mode == MOE_GATE_TOKEN ? rows * b : row;
+  for (const void* out : {(const void*)res_out, (const void*)next_out})
+    if (overlap_any(out, n, {{weight, row}, {bias, row}, {next_weight, row}, {next_bias, row}}) ||
+        (!(gate_mode == MOE_GATE_FULL && out == gate) && overlap(out, n, gate, ng)))
+      return MOE_ERR_INVALID_ARG;
   return from_hip(moe::launch_norm_residual(y, kind, weight, bias, res, gate, gate_mode, scale,
                                             next_kind, next_weight, next_bias, rows, H, eps,
                                             dtype == MOE_BF16, res_out, next_out,

@@ -56,3 +56,41 @@ def test_linear_workspace_over_an_operand():
     for at in (PERM, OFF):
         assert grouped(ws=at, dt=0, K=4096) == INVALID
         assert grouped(ws=at - need + 16, dt=0, K=4096) == INVALID
+
+
+# ---------------------------------------------------------------- norms
+
+ROWS, H = 4, 96
+NB = ROWS * H * 2  # bytes of bf16 rows
+
+
+def norm(out):
+    return moe.lib().moe_norm(V(X), V(W), V(B), ROWS, H, 1e-6, 1, 1, V(out), None)
+
+
+@pytest.mark.parametrize("at", [W, B])
+def test_norm_output_over_a_parameter(at):
+    assert norm(at + H * 2 - 32) == INVALID
+    assert norm(at - NB + 16) == INVALID
+
+
+GATE, NW, NBIAS, ROUT, NOUT = P[8:13]
+
+
+def residual(rout=ROUT, nout=NOUT, mode=2):
+    return moe.lib().moe_norm_residual(V(X), 1, V(W), V(B), V(RES), V(GATE), mode, 0.5, 2, V(NW), V(NBIAS),
+                                       ROWS, H, 1e-6, 1, V(rout), V(nout), None)
+
+
+@pytest.mark.parametrize("at", [W, B, NW, NBIAS, GATE])
+@pytest.mark.parametrize("which", ["rout", "nout"])
+def test_norm_residual_output_over_a_parameter(at, which):
+    assert residual(**{which: at + H * 2 - 32}) == INVALID
+    assert residual(**{which: at - NB + 16}) == INVALID
+
+
+@pytest.mark.parametrize("which", ["rout", "nout"])
+def test_norm_residual_output_over_the_gate(which):
+    assert residual(**{which: GATE}, mode=1) == INVALID  # a value a row: other rows still read it
+    assert residual(**{which: GATE + 16}, mode=3) == INVALID
+    assert residual(**{which: GATE - 16}, mode=3) == INVALID

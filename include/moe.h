@@ -394,7 +394,8 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
  * topk_idx [T,k] int32, topk_w [T,k] fp32: device, written
  * 1 <= groups <= 64, E % groups == 0, 1 <= topk_groups <= groups,
  * k <= topk_groups * E / groups, T <= 2^27, scale finite; else MOE_ERR_UNSUPPORTED (or
- * MOE_ERR_INVALID_ARG for non-positive sizes and unknown enums).
+ * MOE_ERR_INVALID_ARG for non-positive sizes, unknown enums and outputs or a
+ * workspace that overlap another operand).
  * ws / ws_bytes: device workspace of at least
  *   moe_route_grouped_workspace_bytes(T,H,E,k,dtype) (NULL allowed when that is 0)
  */

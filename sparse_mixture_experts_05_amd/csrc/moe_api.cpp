@@ -351,8 +351,14 @@ int moe_route_grouped(const void* x, const void* wg, const float* bias, int T, i
   if (st != MOE_OK) return st;
   st = check_grouped(T, E, k, score, groups, topk_groups, group_top, renorm, scale);
   if (st != MOE_OK) return st;
+  const Span sx{x, (size_t)T * H * elem(dtype)}, sg{wg, (size_t)E * H * elem(dtype)};
+  const Span sb{bias, E * sizeof(float)};
+  const Span si{topk_idx, (size_t)T * k * sizeof(int32_t)}, sw{topk_w, (size_t)T * k * sizeof(float)};
+  if (overlap_any(si.p, si.n, {sx, sg, sb, sw}) || overlap_any(sw.p, sw.n, {sx, sg, sb}))
+    return MOE_ERR_INVALID_ARG;
   const size_t need = moe::route_grouped_ws_bytes(T, H, E, dtype == MOE_BF16);
   if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (overlap_any(ws, need, {sx, sg, sb, si, sw})) return MOE_ERR_INVALID_ARG;
   return from_hip(moe::launch_route_grouped(x, wg, bias, T, H, E, k, score == MOE_SCORE_SOFTMAX,
                                             groups, topk_groups, group_top, renorm != 0, scale,
                                             dtype == MOE_BF16, topk_idx, topk_w, ws,

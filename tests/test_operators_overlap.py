@@ -94,3 +94,31 @@ def test_norm_residual_output_over_the_gate(which):
     assert residual(**{which: GATE}, mode=1) == INVALID  # a value a row: other rows still read it
     assert residual(**{which: GATE + 16}, mode=3) == INVALID
     assert residual(**{which: GATE - 16}, mode=3) == INVALID
+
+
+# ---------------------------------------------------------------- grouped routing
+
+T, RH, RE, RK = 32, 4096, 128, 8
+IDX, TW = P[13:15]
+
+
+def route(idx=IDX, w=TW, ws=WS):
+    return moe.lib().moe_route_grouped(V(X), V(W), V(B), T, RH, RE, RK, 1, 8, 4, 2, 1, 2.5, 1, V(idx), V(w),
+                                       V(ws), 1 << 40, None)
+
+
+@pytest.mark.parametrize("at,n", [(X, T * RH * 2), (W, RE * RH * 2), (B, RE * 4)])
+@pytest.mark.parametrize("which", ["idx", "w"])
+def test_route_grouped_output_over_an_input(at, n, which):
+    assert route(**{which: at + n - 4}) == INVALID
+    assert route(**{which: at - T * RK * 4 + 4}) == INVALID
+
+
+def test_route_grouped_outputs_and_workspace():
+    assert route(w=IDX) == INVALID
+    assert route(w=IDX + T * RK * 4 - 4) == INVALID
+    need = moe.lib().moe_route_grouped_workspace_bytes(T, RH, RE, RK, 1)
+    assert need > 0
+    for at in (X, W, B, IDX, TW):
+        assert route(ws=at) == INVALID
+        assert route(ws=at - need + 16) == INVALID

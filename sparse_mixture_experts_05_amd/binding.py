@@ -879,9 +879,9 @@ class MoEBlockGraph:
 
     Takes moe_block_forward's arguments after h, by keyword. ``run(h)`` copies h
     into the static input and replays; it returns (res, next), the static outputs,
-    which the next run overwrites; ``state`` holds every step's static result. The
-    weights and biases are read where they are: their owner may update them in
-    place between runs."""
+    which the next run overwrites: runs on several streams are the caller's to order.
+    ``state`` holds every step's static result. The weights and biases are read where
+    they are: their owner may update them in place between runs."""
 
     def __init__(self, T: int, wg, w_up, w_down, k: int, **kw):
         if kw.get("x") is not None or kw.get("stream") is not None:
@@ -905,9 +905,11 @@ class MoEBlockGraph:
             torch.cuda.synchronize()
 
     def run(self, h):
-        """Copy h into the static input and replay; returns (res, next)."""
-        if h.shape != self.h.shape:  # copy_ would broadcast
-            raise ValueError(f"h has shape {tuple(h.shape)}, expected {tuple(self.h.shape)}")
+        """Copy h (of the captured shape and type; host tensors are copied too) into the
+        static input and replay; returns (res, next)."""
+        if not isinstance(h, torch.Tensor):
+            raise ValueError("h must be a torch tensor")
+        _want(h, "h", self.h.shape, self.h.dtype)  # copy_ would broadcast and cast
         self.h.copy_(h)
         self.graph.replay()
         return self.state["res"], self.state["next"]

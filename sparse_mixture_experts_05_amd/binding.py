@@ -600,6 +600,12 @@ def _ptr(t, name: str, shape, dtype, device):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _fits(*sizes):
+    """Refuses sizes that a C int does not hold: ctypes would pass their low 32 bits."""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise ValueError(f"sizes must fit 32 bits, got {max(sizes, key=abs)}")
+
+
 def _ws(nbytes: int, device, ws):
     """(address, bytes) of the workspace: the caller's, or a new one."""
     if ws is None:
@@ -634,6 +640,7 @@ def moe_norm(x, weight=None, bias=None, eps: float = 1e-6, kind: str = "rms", ou
 
     bf16 or fp32, any H up to 16384; ``out`` may be x itself. Returns out."""
     T, H = _shape(x, "x", 2)
+    _fits(T, H)
     dev, dtype = x.device, x.dtype
     dt, code = _dtype_code(x), _enum(NORM_KINDS, kind, "kind")
     xp = _ptr(x, "x", (T, H), dtype, dev)
@@ -660,6 +667,7 @@ def moe_norm_residual(y, res, weight=None, bias=None, gate=None, scale: float = 
     (one value a row), [H] or [T,H]. Returns (h, norm of h or None). res_out may
     be res itself, next_out y itself."""
     T, H = _shape(y, "y", 2)
+    _fits(T, H)
     dev, dtype, row = y.device, y.dtype, (H,)
     dt = _dtype_code(y)
     code, ncode = _enum(NORM_KINDS, kind, "kind"), _enum(NORM_KINDS, next_kind, "next_kind")
@@ -701,6 +709,7 @@ def moe_norm_residual(y, res, weight=None, bias=None, gate=None, scale: float = 
 
 
 def moe_route_grouped_workspace_bytes(T: int, H: int, E: int, k: int, dtype_code: int) -> int:
+    _fits(T, H, E, k)
     return lib().moe_route_grouped_workspace_bytes(T, H, E, k, dtype_code)
 
 
@@ -713,6 +722,7 @@ def moe_route_grouped(x, wg, bias, k: int, score: str = "sigmoid", groups: int =
     Returns (topk_idx int32 [T,k], topk_w fp32 [T,k])."""
     T, H = _shape(x, "x", 2)
     E = _shape(wg, "wg", 2)[0]
+    _fits(T, H, E, k, groups, topk_groups, group_top)
     dev, dtype = x.device, x.dtype
     dt, code = _dtype_code(x), _enum(SCORES, score, "score")
     xp, wp = _ptr(x, "x", (T, H), dtype, dev), _ptr(wg, "wg", (E, H), dtype, dev)
@@ -739,6 +749,7 @@ def moe_route_grouped(x, wg, bias, k: int, score: str = "sigmoid", groups: int =
 
 
 def moe_linear_workspace_bytes(M: int, N: int, K: int, act: str, dtype_code: int) -> int:
+    _fits(M, N, K)
     return lib().moe_linear_workspace_bytes(M, N, K, _enum(ACTS, act, "act"), dtype_code)
 
 
@@ -753,6 +764,7 @@ def moe_linear(x, w, bias=None, act: str = "none", residual=None, y=None, ws=Non
     code = _enum(ACTS, act, "act")
     two = (2,) if code >= 3 else ()
     N = _shape(w, "w", 2 + len(two))[-2]
+    _fits(M, N, K)
     dev, dtype = x.device, x.dtype
     dt = _dtype_code(x)
     xp, wp = _ptr(x, "x", (M, K), dtype, dev), _ptr(w, "w", (*two, N, K), dtype, dev)
@@ -774,6 +786,7 @@ def moe_linear(x, w, bias=None, act: str = "none", residual=None, y=None, ws=Non
 
 def moe_linear_grouped_workspace_bytes(E: int, rows: int, N: int, K: int, act: str,
                                        dtype_code: int) -> int:
+    _fits(E, rows, N, K)
     return lib().moe_linear_grouped_workspace_bytes(E, rows, N, K, _enum(ACTS, act, "act"),
                                                     dtype_code)
 
@@ -798,6 +811,7 @@ def moe_linear_grouped(x, offsets, w, bias=None, act: str = "none", residual=Non
     most = T if perm is None else T * k
     if rows is None:
         rows = most
+    _fits(T, K, E, N, k, rows)
     if not 1 <= rows <= most:
         raise ValueError(f"rows {rows} outside [1, {most}]")
     if perm is not None and _shape(perm, "perm", 1)[0] < rows:

@@ -457,6 +457,24 @@ int moe_linear_grouped(const void* x, const int32_t* perm, int k, int T, const i
                        size_t ws_bytes, void* stream);
 size_t moe_linear_grouped_workspace_bytes(int E, int rows, int N, int K, int act, int dtype);
 
+typedef enum {
+  MOE_PATH_ROWS = 0,     /* few rows: weights straight to registers */
+  MOE_PATH_TILES = 1,    /* tiles of 64 (fp32 also 32) rows x 64 weight rows, K slices */
+  MOE_PATH_256X128 = 2,  /* tiles of 256 rows x 128 weight rows */
+  MOE_PATH_256X256 = 3   /* tiles of 256 rows x 256 weight rows */
+} moe_path;
+
+/*
+ * moe_linear_path - the kernels that a product of these sizes takes (a host
+ * query, for profiles and tests; nothing is launched): a moe_path, or a negative
+ * status. grouped: 0 for moe_linear (E = 1), 1 for moe_linear_grouped.
+ * slices (or NULL) receives the slices of K: of every tile, for the 256-row
+ * tiles those of the last round's; 0 where the offsets decide it (grouped
+ * 256-row tiles of K >= 8192). A grouped product whose gathered x passes 4 GiB
+ * takes MOE_PATH_TILES with one slice in place of the 256-row tiles.
+ */
+int moe_linear_path(int E, int rows, int N, int K, int act, int grouped, int dtype, int* slices);
+
 /* Static, human-readable text for a status code. */
 const char* moe_status_string(int status);
 

@@ -12,7 +12,7 @@ MoEBlockGraph. Every step runs in the HIP kernels; this package only marshals te
 """
 from .binding import (MoEBlockGraph, MoEError, MoELayerGraph, lib, moe_block_forward, moe_bias_update, moe_capacity, moe_combine,
                       moe_dispatch, moe_dispatch_noalloc, moe_expert_ffn, moe_expert_ffn_gather,
-                      moe_layer_forward, moe_linear, moe_linear_grouped, moe_load_stats,
+                      moe_layer_forward, moe_linear, moe_linear_grouped, moe_linear_path, moe_load_stats,
                       moe_norm, moe_norm_residual, moe_route, moe_route_grouped, moe_status_string,
                       moe_dispatch_workspace_bytes, moe_expert_ffn_workspace_bytes,
                       moe_linear_grouped_workspace_bytes, moe_linear_workspace_bytes,
@@ -24,6 +24,6 @@ __all__ = ["MoEError", "MoELayerGraph", "lib", "moe_route", "moe_dispatch",
            "moe_load_stats", "moe_bias_update", "moe_capacity", "moe_layer_forward", "moe_status_string",
            "moe_dispatch_workspace_bytes", "moe_expert_ffn_workspace_bytes",
            "moe_route_workspace_bytes", "moe_norm", "moe_norm_residual", "moe_route_grouped",
-           "moe_linear", "moe_linear_grouped", "moe_block_forward", "MoEBlockGraph",
+           "moe_linear", "moe_linear_grouped", "moe_linear_path", "moe_block_forward", "MoEBlockGraph",
            "moe_route_grouped_workspace_bytes", "moe_linear_workspace_bytes",
            "moe_linear_grouped_workspace_bytes"]

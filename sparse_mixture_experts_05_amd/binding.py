@@ -51,6 +51,7 @@ SIGNATURES = {
     "moe_linear_grouped": (_i, [_vp, _vp, _i, _i, _vp, _i, _i, _vp, _vp, _i, _vp, _i, _i, _i, _vp,
                                 _vp, _sz, _vp]),
     "moe_linear_grouped_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "moe_linear_path": (_i, [_i, _i, _i, _i, _i, _i, _i, _vp]),
     "moe_status_string": (ctypes.c_char_p, [_i]),
 }
 
@@ -789,6 +790,22 @@ def moe_linear_grouped_workspace_bytes(E: int, rows: int, N: int, K: int, act: s
     _fits(E, rows, N, K)
     return lib().moe_linear_grouped_workspace_bytes(E, rows, N, K, _enum(ACTS, act, "act"),
                                                     dtype_code)
+
+
+LINEAR_PATHS = ("rows", "tiles", "256x128", "256x256")
+
+
+def moe_linear_path(M: int, N: int, K: int, act: str, dtype_code: int, E: int | None = None):
+    """(kernels, K slices) of a product of M rows, or with E of a grouped product of M
+    buffer rows: "rows", "tiles", "256x128" or "256x256", and the slices of K (0 where
+    the offsets decide). A host query; raises MoEError for sizes that are refused."""
+    _fits(M, N, K, E or 1)
+    n = ctypes.c_int(0)
+    path = lib().moe_linear_path(1 if E is None else E, M, N, K, _enum(ACTS, act, "act"),
+                                 int(E is not None), dtype_code, ctypes.byref(n))
+    if path < 0:
+        _check("moe_linear_path", path)
+    return LINEAR_PATHS[path], n.value
 
 
 def moe_linear_grouped(x, offsets, w, bias=None, act: str = "none", residual=None, perm=None,

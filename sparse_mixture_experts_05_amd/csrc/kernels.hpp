@@ -60,6 +60,8 @@ hipError_t launch_route_grouped(const void* x, const void* wg, const float* bias
 // Whether every launch of the shape fits one grid.
 bool linear_fits(int E, int M, int N, int K, int act, bool grouped, bool bf16);
 size_t linear_ws_bytes(int E, int M, int N, int K, int act, bool grouped, bool bf16);
+// The product's moe_path and K slices (0: the offsets decide).
+int linear_path(int E, int M, int N, int K, int act, bool grouped, bool bf16, int* slices);
 hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
                          const int32_t* offsets, int E, int M, int N, int K, const void* w,
                          const void* bias, int act, const void* res, bool bf16, void* y, void* ws,

@@ -399,7 +399,7 @@ unsigned lin_grid(const LinArgs& a, int BM, int bnc) {  // whole rounds of the 8
   return (unsigned)((lin_tiles(a, BM, bnc) + 7) / 8 * 8);
 }
 
-enum LinPath { kRows, kTile64, kBigHalf, kBig };
+enum LinPath { kRows, kTile64, kBigHalf, kBig };  // moe_path
 struct LinPlan {
   LinPath path;
   int nks;  // K slices (64 x 64 tiles)
@@ -541,6 +541,14 @@ size_t linear_ws_bytes(int E, int M, int N, int K, int act, bool grouped, bool b
   const LinPlan p = lin_plan(a);
   if (p.path >= kBigHalf) return big_ws_bytes(a, p.path == kBigHalf);
   return p.path == kTile64 ? tile_ws_bytes(a, 64, p.nks) : 0;
+}
+
+int linear_path(int E, int M, int N, int K, int act, bool grouped, bool bf16, int* slices) {
+  const int32_t some = 0;
+  const LinArgs a = lin_args(nullptr, nullptr, 1, M, grouped ? &some : nullptr, E, M, N, K, act);
+  const LinPlan p = bf16 ? lin_plan(a) : LinPlan{kTile64, f32_slices(a)};
+  *slices = p.path >= kBigHalf ? big_slices(a, p.path == kBigHalf) : p.nks;
+  return p.path;
 }
 
 hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,

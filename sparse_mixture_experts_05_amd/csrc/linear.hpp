@@ -106,6 +106,7 @@ __device__ __forceinline__ void store4(const LinArgs& a, int e, size_t row, int 
 bool big_ok(const LinArgs& a);         // the shape's offsets fit the kernel's addressing
 bool big_gather_ok(const LinArgs& a);  // and those of the gathered rows
 size_t big_ws_bytes(const LinArgs& a, bool half);
+int big_slices(const LinArgs& a, bool half);  // K slices of the last round's tiles (0: by the offsets)
 hipError_t launch_big(LinArgs a, bool half, void* ws, hipStream_t s);
 
 }  // namespace lin

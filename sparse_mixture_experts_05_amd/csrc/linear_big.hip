@@ -531,6 +531,20 @@ size_t big_ws_bytes(const LinArgs& a, bool half) {
   return half ? big_layout<128>(a).bytes : big_layout<256>(a).bytes;
 }
 
+int big_slices(const LinArgs& a, bool half) {
+  LinArgs b = a;
+  b.part = nullptr;
+  b.slots = 0;
+  plan::Shape sh = shape_of(b, a.act == kActGeglu || a.act == kActSwiglu);
+  sh.split = plan::split_ok(sh);
+  if (!sh.split) return 1;
+  if (a.offsets != nullptr) return 0;
+  plan::Tables L;
+  L.pf[0] = L.pa[0] = plan::cdiv(sh.shared_M, BM) * plan::cdiv(sh.shared_N, half ? 128 : 256);
+  L.ps[0] = 0;
+  return plan::finish_schedule(sh, L).spl;
+}
+
 hipError_t launch_big(LinArgs a, bool half, void* ws, hipStream_t s) {
   return half ? launch_big_tn<4>(a, ws, s) : launch_big_tn<8>(a, ws, s);
 }

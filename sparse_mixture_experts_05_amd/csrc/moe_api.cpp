@@ -384,6 +384,16 @@ size_t moe_linear_grouped_workspace_bytes(int E, int rows, int N, int K, int act
   return moe::linear_ws_bytes(E, rows, N, K, act, true, dtype == MOE_BF16);
 }
 
+int moe_linear_path(int E, int rows, int N, int K, int act, int grouped, int dtype, int* slices) {
+  if ((grouped != 0 && grouped != 1) || (grouped == 0 && E != 1)) return MOE_ERR_INVALID_ARG;
+  const int st = check_linear(E, rows, N, K, act, grouped != 0, dtype);
+  if (st != MOE_OK) return st;
+  int n = 1;
+  const int path = moe::linear_path(E, rows, N, K, act, grouped != 0, dtype == MOE_BF16, &n);
+  if (slices) *slices = n;
+  return path;
+}
+
 int moe_linear_grouped(const void* x, const int32_t* perm, int k, int T, const int32_t* offsets,
                        int E, int rows, const void* w, const void* bias, int act,
                        const void* residual, int N, int K, int dtype, void* y, void* ws,

@@ -1,0 +1,53 @@
+"""The host query of a product's path: refusals, and that it agrees with the workspace
+that the product asks for."""
+import ctypes
+
+import pytest
+
+import sparse_mixture_experts_05_amd as moe
+
+
+def query(E=1, rows=32, N=64, K=64, act=0, grouped=0, dt=1, slices=None):
+    return moe.lib().moe_linear_path(E, rows, N, K, act, grouped, dt, slices)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(E=0), -1), (dict(E=2), -1), (dict(rows=0), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(act=5), -1),
+    (dict(act=-1), -1), (dict(grouped=2), -1), (dict(grouped=-1), -1), (dict(dt=2), -1),
+    (dict(N=96), -2), (dict(K=32), -2), (dict(E=257, grouped=1), -2), (dict(rows=1 << 22, N=1 << 14), -2),
+])
+def test_refusals(kw, status):
+    assert query(**kw) == status
+
+
+def test_without_slices():
+    n = ctypes.c_int(-1)
+    assert query() == query(slices=ctypes.byref(n)) >= 0
+    assert n.value == 1
+
+
+def test_binding():
+    assert moe.moe_linear_path(4095, 4096, 4096, "none", 1) == ("256x256", 1)
+    assert moe.moe_linear_path(1024, 4096, 4096, "none", 1) == ("256x128", 1)
+    assert moe.moe_linear_path(1, 4096, 4096, "none", 1) == ("rows", 1)
+    assert moe.moe_linear_path(16, 64, 64, "none", 0)[0] == "tiles"
+    with pytest.raises(moe.MoEError):
+        moe.moe_linear_path(16, 60, 64, "none", 1)
+    with pytest.raises(ValueError, match="act must be one of"):
+        moe.moe_linear_path(16, 64, 64, "tanh", 1)
+
+
+@pytest.mark.parametrize("dt", [0, 1])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("E", [None, 8])
+def test_workspace_agrees(E, act, dt):
+    """No workspace for one slice of the rows or tiles path, one for more; the large
+    tiles need one for a grouped launch's table and for K slices."""
+    for M in (1, 17, 64, 257, 700, 1300, 2600):
+        for N in (64, 192, 1088, 4160):
+            for K in (64, 704, 2048, 4096):
+                path, slices = moe.moe_linear_path(M, N, K, act, dt, E)
+                need = (moe.moe_linear_workspace_bytes(M, N, K, act, dt) if E is None else
+                        moe.moe_linear_grouped_workspace_bytes(E, M, N, K, act, dt))
+                many = slices > 1 or (path.startswith("256") and E is not None)
+                assert (need > 0) == many, (M, N, K, path, slices, need)

@@ -246,7 +246,7 @@ __global__ __launch_bounds__(NW * 64) void grouped_bf16_kernel(
   __shared__ __align__(16) uint8_t smem[LDS];
   const int t0 = blockIdx.x * BT;
   f32x4_t acc[C::MC][C::NC];
-  score_tile<BT, EP, NW>(smem, x, wg, t0, T, 0, E, H, 0, H / 64, acc);
+  score_tile<BT, EP, NW, uint16_t, true>(smem, x, wg, t0, T, 0, E, H, 0, H / 64, acc);
   scores_to_lds<BT, EP, NW>(smem, E, nullptr, acc);
   grouped_phase<BT, EP, NW>(reinterpret_cast<float*>(smem),
                             *reinterpret_cast<GroupLds<BT, NW>*>(smem + C::SC_BYTES), a, t0, T, E, k,
@@ -362,10 +362,10 @@ hipError_t launch_partial_f32(const void* x, const void* wg, int T, int H, int E
   const float* xp = static_cast<const float*>(x);
   const float* wp = static_cast<const float*>(wg);
   if (f32_big(T))
-    hipLaunchKernelGGL((route_partial_kernel<64, 128, 4, float>), dim3((T + 63) / 64, (E + 127) / 128, nks),
+    hipLaunchKernelGGL((route_partial_kernel<64, 128, 4, float, true>), dim3((T + 63) / 64, (E + 127) / 128, nks),
                        dim3(256), 0, s, xp, wp, T, H, E, kps, sp);
   else
-    hipLaunchKernelGGL((route_partial_kernel<kPartBT, kPartEP, 4, float>),
+    hipLaunchKernelGGL((route_partial_kernel<kPartBT, kPartEP, 4, float, true>),
                        dim3((T + kPartBT - 1) / kPartBT, (E + kPartEP - 1) / kPartEP, nks), dim3(256), 0,
                        s, xp, wp, T, H, E, kps, sp);
   return hipGetLastError();
@@ -396,7 +396,7 @@ hipError_t launch_route_grouped(const void* x, const void* wg, const float* bias
   if (!one_launch(T, H, E, bf16)) {
     float* sp = static_cast<float*>(ws);
     const int nks = bf16 ? route_kslices(T, H, E) : f32_kslices(T, H, E);
-    const hipError_t err = bf16 ? launch_partial(x, wg, T, H, E, sp, s)
+    const hipError_t err = bf16 ? launch_partial<true>(x, wg, T, H, E, sp, s)
                                 : launch_partial_f32(x, wg, T, H, E, sp, s);
     if (err != hipSuccess) return err;
     return select_tokens_per_block(T) == 16

@@ -143,7 +143,16 @@ struct RouteTile {
 // The K loop of one tile (T: bf16 bits or fp32; a panel is 128 bytes of a row, the
 // K range in panels); returns with every wave's accumulators complete and
 // the LDS free for reuse (after a barrier).
-template <int BT, int EP, int NW = 4, typename T_ = uint16_t>
+//
+// SUMS: several partial sums per score, one for each half panel of a stage (fp32: two,
+// over every other MFMA), added up behind the loop. In one chain over K every addition
+// rounds a partial sum that grows to the score itself; n sums are n times smaller, and the
+// rounding error falls to about a half with 2, a third with 4, a fifth with 8. Error of
+// softmax weights against float64 where nothing slices K, in u = 2^-24: 64 tokens, E 256,
+// fp32, H 2112 28.9 -> 5.9, H 4032 40.1 -> 8.9 (8 sums); 1024 tokens, E 128, fp32, H 4032
+// 39.0 -> 12.5 (4); 64 tokens, bf16, H 4032 15.4 -> 4.9 (4); 16384 tokens 15.9 -> 8.5 (2).
+// Held in registers that the tiles leave free; times within 3 % of one chain either way.
+template <int BT, int EP, int NW = 4, typename T_ = uint16_t, bool SUMS = false>
 __device__ __forceinline__ void score_tile(uint8_t* smem, const T_* __restrict__ x,
                                            const T_* __restrict__ wg, int t0, int T, int e0,
                                            int E, int H, int kp0, int kp1,
@@ -174,10 +183,18 @@ __device__ __forceinline__ void score_tile(uint8_t* smem, const T_* __restrict__
       lds_dma16(src[q] + (size_t)min(kp0 + st * C::PPS + pq[q], kp1 - 1) * (128 / sizeof(T_)), base + dst[q]);
   };
 
+  // the sums besides acc, by panel of a stage, k step and MFMA
+  constexpr int PS = SUMS && !C::KSPLIT ? C::PPS : 1;
+  constexpr int JS = sizeof(T_) == 4 ? 2 : 1, NSUM = SUMS ? PS * 2 * JS : 1;
+  f32x4_t sum[NSUM][C::MC][C::NC];
 #pragma unroll
   for (int m = 0; m < C::MC; ++m)
 #pragma unroll
-    for (int n = 0; n < C::NC; ++n) acc[m][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < C::NC; ++n) {
+      acc[m][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < NSUM; ++q) sum[q][m][n] = acc[m][n];
+    }
 
   // fragment of a 16-row tile: row lane%16, chunk ks*4 + lane/16 (a 32-deep k step)
   const int fr = (lane & 15) * 128;
@@ -211,10 +228,44 @@ __device__ __forceinline__ void score_tile(uint8_t* smem, const T_* __restrict__
 #pragma unroll
         for (int m = 0; m < C::MC; ++m)
 #pragma unroll
-          for (int n = 0; n < C::NC; ++n)
-            acc[m][n] = mma16<T_>(a[m], b[n], acc[m][n]);
+          for (int n = 0; n < C::NC; ++n) {
+            const int q = (p % PS * 2 + ks) * JS;
+            if constexpr (!SUMS) {
+              acc[m][n] = mma16<T_>(a[m], b[n], acc[m][n]);
+            } else if constexpr (JS == 1) {
+              sum[q][m][n] = mma16<T_>(a[m], b[n], sum[q][m][n]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                sum[q + j % JS][m][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                    __uint_as_float(a[m][j]), __uint_as_float(b[n][j]), sum[q + j % JS][m][n], 0, 0, 0);
+            }
+          }
       }
     }
+    if constexpr (SUMS) {
+      // held in accumulation registers from stage to stage
+#pragma unroll
+      for (int q = 0; q < NSUM; ++q)
+#pragma unroll
+        for (int m = 0; m < C::MC; ++m)
+#pragma unroll
+          for (int n = 0; n < C::NC; ++n) asm volatile("" : "+a"(sum[q][m][n]));
+    }
+  }
+  if constexpr (SUMS) {
+#pragma unroll
+    for (int h = NSUM / 2; h > 0; h /= 2)
+#pragma unroll
+      for (int q = 0; q < h; ++q)
+#pragma unroll
+        for (int m = 0; m < C::MC; ++m)
+#pragma unroll
+          for (int n = 0; n < C::NC; ++n) sum[q][m][n] += sum[q + h][m][n];
+#pragma unroll
+    for (int m = 0; m < C::MC; ++m)
+#pragma unroll
+      for (int n = 0; n < C::NC; ++n) acc[m][n] = sum[0][m][n];
   }
   __syncthreads();  // every wave is done with the stages
 }
@@ -270,8 +321,9 @@ __device__ __forceinline__ void scores_to_lds(uint8_t* smem, int ncol, const flo
 // block, K slice) stores its BT x EP tile to ws[ks][t][e] (no bias).
 constexpr int kPartBT = 16, kPartEP = 64, kMaxSlices = 16;
 
-template <int BT, int EP, int NW = 4, typename T_ = uint16_t>
-__global__ __launch_bounds__(NW * 64) void route_partial_kernel(const T_* __restrict__ x,
+template <int BT, int EP, int NW = 4, typename T_ = uint16_t, bool SUMS = false>
+__global__ __launch_bounds__(NW * 64, SUMS ? 2 : 1)  // two workgroups a CU: at most 256 registers
+void route_partial_kernel(const T_* __restrict__ x,
                                                                 const T_* __restrict__ wg,
                                                                 int T, int H, int E, int kps,
                                                                 float* __restrict__ ws) {
@@ -281,7 +333,7 @@ __global__ __launch_bounds__(NW * 64) void route_partial_kernel(const T_* __rest
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int t0 = blockIdx.x * BT, e0 = blockIdx.y * EP, ks = blockIdx.z;
   f32x4_t acc[C::MC][C::NC];
-  score_tile<BT, EP, NW, T_>(smem, x, wg, t0, T, e0, E, H, ks * kps, (ks + 1) * kps, acc);
+  score_tile<BT, EP, NW, T_, SUMS>(smem, x, wg, t0, T, e0, E, H, ks * kps, (ks + 1) * kps, acc);
   // D layout of 16x16: lane holds column lane%16, rows (lane/16)*4 + v
 #pragma unroll
   for (int m = 0; m < C::MC; ++m)
@@ -346,6 +398,7 @@ int bf16_tokens_per_block(int T) { return T >= 64 * 256 ? 64 : T >= 32 * 256 ? 3
 int select_tokens_per_block(int T) { return T >= 1024 || T <= 4 ? 16 : 4; }
 
 // Score launch of the two-launch paths (route_mode != kOneLaunch).
+template <bool SUMS = false>
 hipError_t launch_partial(const void* x, const void* wg, int T, int H, int E, float* sp,
                           hipStream_t s) {
   const int nks = route_kslices(T, H, E);
@@ -354,16 +407,16 @@ hipError_t launch_partial(const void* x, const void* wg, int T, int H, int E, fl
   const uint16_t* wp = static_cast<const uint16_t*>(wg);
   if (route_mode(T, E, true) == kTwoSmall) {
     const dim3 grid((T + kPartBT - 1) / kPartBT, (E + kPartEP - 1) / kPartEP, nks);
-    hipLaunchKernelGGL((route_partial_kernel<kPartBT, kPartEP>), grid, dim3(kThreads), 0, s, xp,
+    hipLaunchKernelGGL((route_partial_kernel<kPartBT, kPartEP, 4, uint16_t, SUMS>), grid, dim3(kThreads), 0, s, xp,
                        wp, T, H, E, kps, sp);
   } else if (E > 128) {
     const dim3 grid((T + 127) / 128, (E + 255) / 256, nks);
-    hipLaunchKernelGGL((route_partial_kernel<128, 256, route_waves<128, 256>()>), grid,
+    hipLaunchKernelGGL((route_partial_kernel<128, 256, route_waves<128, 256>(), uint16_t, SUMS>), grid,
                        dim3(route_waves<128, 256>() * 64), 0, s, xp, wp, T,
                        H, E, kps, sp);
   } else {
     const dim3 grid((T + 63) / 64, (E + 127) / 128, nks);
-    hipLaunchKernelGGL((route_partial_kernel<64, 128, route_waves<64, 128>()>), grid,
+    hipLaunchKernelGGL((route_partial_kernel<64, 128, route_waves<64, 128>(), uint16_t, SUMS>), grid,
                        dim3(route_waves<64, 128>() * 64), 0, s, xp, wp, T, H,
                        E, kps, sp);
   }

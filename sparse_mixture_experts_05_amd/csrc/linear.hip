@@ -18,6 +18,7 @@
 #include "common.hpp"
 #include "kernels.hpp"
 #include "linear.hpp"
+#include "plan.hpp"
 
 namespace moe {
 namespace {
@@ -435,6 +436,13 @@ int f32_slices(const LinArgs& a) {
 //   4096 x 4096 x 4096           305   (1)          114        96
 //   64 x 1024 x 1024      5.0      8.1 (8)           15        19
 //   2048 x 512 x 4096             26.4 (1)           44        73
+//   1 x 64 x 8192        11.7      9.1 (16)          20        27
+//   64 x 1024 x 8192               10.7 (16)          28        34
+//   256 x 4096 x 8192             38.0 (4)           36        52
+//   512 x 4096 x 8192             62.3 (1)           47        57
+//   2048 x 4096 x 8192           297   (1)          106       117
+//   128 x 512 x 14336             14.9 (16)          31        47
+//   256 x 4096 x 28672           104   (2)           71        85
 //   E 8, 64 rows, 1024 x 1024    7.1     10.0 (1)    15        18
 //   E 8, 512 rows, 4096 x 4096           61.4 (1)    68        77
 //   E 8, 1024 rows, 4096 x 4096          93   (1)    72        88
@@ -447,8 +455,9 @@ int f32_slices(const LinArgs& a) {
 // then in proportion, and a third of the time in which every column tile reads its rows
 // from L2 (8 TB/s) does not hide; slices add a launch (3 us) and their partials' round trip. The large tiles run one
 // workgroup a CU: 0.56 or 1 us a stage on an idle chip, 0.83 or 1.38 when every CU
-// runs one (power and cache traffic). Of the lesser of work and weight stream a tenth
-// does not hide behind the other.
+// runs one (power and cache traffic); the last round's K slices are plan.hpp's, and the
+// launch that adds them up takes 3 us and their bytes at 3.3 TB/s. Of the lesser of work
+// and weight stream a tenth does not hide behind the other.
 LinPlan lin_plan(const LinArgs& a) {
   const double h = host_gated(a.act) ? 2.0 : 1.0, cols = h * a.N;  // weight rows of an expert
   // experts with rows, as if each row drew its expert
@@ -458,13 +467,28 @@ LinPlan lin_plan(const LinArgs& a) {
   auto row_tiles = [&](int bm) {
     return a.offsets ? std::max(live, (double)a.M / bm + live / 2) : std::ceil((double)a.M / bm);
   };
+  struct Large {
+    double us;
+    bool split;  // K slices in the last round, and a launch that adds them up
+  };
   auto big = [&](int bn, double idle, double full) {
     const double tiles = row_tiles(256) * std::ceil(cols / bn);
+    const double start = 8.0 + (a.offsets ? 2.0 : 0.0);
+    if (a.K >= plan::kSplitMinK) {
+      const int each = (int)std::ceil(tiles / plan::kXcds);  // tiles of an XCD
+      const int rounds = each / plan::kSlots, tail = each % plan::kSlots;
+      const int spl = plan::tail_slices(tail, a.K / plan::kStageK);
+      if (spl > 1) {
+        const double last = std::min(tiles, (double)plan::kXcds * each) - 256.0 * rounds;
+        return Large{start + stages * rounds * full +
+                         std::ceil(stages / spl) * std::max(idle, full * tail * spl / plan::kSlots) +
+                         3.0 + last * spl * 256 * bn * 4 / 3.3e6,
+                     true};
+      }
+    }
     const double whole = std::floor(tiles / 256), rest = tiles - 256 * whole;
-    return 8.0 + (a.offsets ? 2.0 : 0.0) +
-           stages * (whole * full + (rest <= 0 ? 0.0
-                                     : a.K >= 8192 ? full * rest / 256  // split over K
-                                                   : std::max(idle, full * rest / 256)));
+    return Large{start + stages * (whole * full + (rest <= 0 ? 0.0 : std::max(idle, full * rest / 256))),
+                 false};
   };
   const double hbm = 2.0 * ((double)a.M * a.K + live * cols * a.K) / 5.3e6;
   // What a call costs its caller: the GPU's time, but in a run of calls no less than the
@@ -474,8 +498,8 @@ LinPlan lin_plan(const LinArgs& a) {
   LinPlan best{kRows, 1};
   double t = cost(3.2 + std::max({1.1 * hbm, a.K / 1000.0,
                              row_tiles(16) * (a.N / 16) * (16 * h + std::min(16.0, a.M / live)) * a.K * 2 / 8.5e6}), false);
-  auto take = [&](LinPath path, int nks, double us) {
-    const double c = cost(us, nks > 1 || (path >= kBigHalf && a.offsets));
+  auto take = [&](LinPath path, int nks, double us, bool two) {
+    const double c = cost(us, two);
     if (c < t) t = c, best = LinPlan{path, nks};
   };
   const double tiles = row_tiles(64) * std::ceil(cols / 64);
@@ -484,12 +508,13 @@ LinPlan lin_plan(const LinArgs& a) {
     if (nks > 1 && (a.K / 64 < 2 * nks || tiles * nks > 2048)) break;
     double us = 4.4 + std::ceil(stages / nks) * 0.36 * std::max(1.0, tiles * nks / 448);
     if (nks > 1) us += 3.0 + 8.0 * a.M * cols * nks / 5e6;
-    take(kTile64, nks, std::max(us, 3.0 + hbm) + 0.1 * std::min(us, hbm) + rows_l2);
+    take(kTile64, nks, std::max(us, 3.0 + hbm) + 0.1 * std::min(us, hbm) + rows_l2, nks > 1);
   }
   if (big_ok(a)) {
-    const double half = big(128, 0.56, 0.83), whole = big(256, 1.0, 1.38);
-    take(kBigHalf, 1, std::max(half, 8.0 + 1.1 * hbm) + 0.1 * std::min(half, hbm));
-    take(kBig, 1, std::max(whole, 8.0 + hbm) + 0.1 * std::min(whole, hbm));
+    const Large half = big(128, 0.56, 0.83), whole = big(256, 1.0, 1.38);
+    const bool table = a.offsets != nullptr;  // written by a launch of its own
+    take(kBigHalf, 1, std::max(half.us, 8.0 + 1.1 * hbm) + 0.1 * std::min(half.us, hbm), table || half.split);
+    take(kBig, 1, std::max(whole.us, 8.0 + hbm) + 0.1 * std::min(whole.us, hbm), table || whole.split);
   }
   return best;
 }

@@ -167,6 +167,13 @@ MOE_HD inline void group_entry(const Shape& s, const int32_t* offsets, int grp, 
   sml = small ? cdiv(cnt, kSBM) * cdiv(s.routed_N, kSBN) : 0;
 }
 
+// K slices of each of the `tail` tiles of an XCD's last round (1: none are cut),
+// with kt K stages to a tile.
+MOE_HD inline int tail_slices(int tail, int kt) {
+  if (tail <= 0 || 2 * tail > kSlots) return 1;
+  return imax(1, imin(imin(kSlots / tail, kMaxSplit), kt / kMinSliceStages));
+}
+
 // The schedule from the completed scans (the same for every workgroup, and
 // for every tile a workgroup runs).
 MOE_HD inline Sched finish_schedule(const Shape& s, const Tables& L) {
@@ -188,10 +195,10 @@ MOE_HD inline Sched finish_schedule(const Shape& s, const Tables& L) {
   S.R = S.CF / kSlots;
   S.tail = S.CF - S.R * kSlots;
   S.spl = 1;
-  if (s.split && S.tail > 0 && 2 * S.tail <= kSlots) {
+  if (s.split) {
     int ktmin = s.routed_K / kStageK;
     if (s.shared_M > 0) ktmin = imin(ktmin, s.shared_K / kStageK);
-    S.spl = imax(1, imin(imin(kSlots / S.tail, kMaxSplit), ktmin / kMinSliceStages));
+    S.spl = tail_slices(S.tail, ktmin);
   }
   return S;
 }

@@ -323,10 +323,8 @@ constexpr int kPartBT = 16, kPartEP = 64, kMaxSlices = 16;
 
 template <int BT, int EP, int NW = 4, typename T_ = uint16_t, bool SUMS = false>
 __global__ __launch_bounds__(NW * 64, SUMS ? 2 : 1)  // two workgroups a CU: at most 256 registers
-void route_partial_kernel(const T_* __restrict__ x,
-                                                                const T_* __restrict__ wg,
-                                                                int T, int H, int E, int kps,
-                                                                float* __restrict__ ws) {
+void route_partial_kernel(const T_* __restrict__ x, const T_* __restrict__ wg, int T, int H, int E,
+                          int kps, float* __restrict__ ws) {
   using C = RouteTile<BT, EP, NW>;
   static_assert(!C::KSPLIT, "each wave owns EP / NW experts");
   __shared__ __align__(16) uint8_t smem[C::NS * C::SB];

@@ -38,6 +38,9 @@ DENSE = [  # (path, slices, M, N, K, acts, type)
     ("tiles", 4, 65, 1344, 2112, GATED, BF16), ("tiles", 8, 1701, 64, 2048, GATED, BF16),
     ("256x128", 1, 1101, 4160, 320, PLAIN, BF16), ("256x128", 1, 1701, 2112, 192, GATED, BF16),
     ("256x256", 1, 2601, 4160, 128, PLAIN, BF16), ("256x256", 1, 1301, 4160, 128, GATED, BF16),
+    ("256x128", 4, 2101, 320, 8192, PLAIN, BF16), ("256x128", 2, 1025, 2112, 8192, PLAIN, BF16),
+    ("256x128", 7, 515, 704, 14336, PLAIN, BF16), ("256x128", 4, 701, 448, 8192, GATED, BF16),
+    ("256x256", 3, 257, 8256, 8192, PLAIN, BF16), ("256x256", 3, 257, 4160, 8192, GATED, BF16),
     ("tiles", 1, 17, 64, 64, PLAIN, FP32), ("tiles", 2, 33, 192, 512, GATED, FP32),
     ("tiles", 4, 17, 64, 1024, PLAIN, FP32), ("tiles", 8, 65, 64, 2112, GATED, FP32),
     ("tiles", 16, 17, 64, 4096, PLAIN, FP32), ("tiles", 1, 1301, 2112, 128, PLAIN, FP32),
@@ -73,6 +76,8 @@ GROUPED = [  # (path, slices, E, rows, N, K, acts, type)
     ("256x128", 1, 3, 901, 4160, 704, PLAIN, BF16), ("256x128", 1, 8, 2601, 2112, 512, PLAIN, BF16),
     ("256x128", 1, 3, 3101, 1088, 320, GATED, BF16), ("256x128", 1, 8, 2601, 960, 512, GATED, BF16),
     ("256x256", 1, 8, 1701, 4160, 320, PLAIN, BF16), ("256x256", 1, 8, 2601, 2112, 192, GATED, BF16),
+    ("256x128", 0, 3, 2101, 320, 8192, PLAIN, BF16), ("256x128", 0, 3, 1701, 192, 8192, GATED, BF16),
+    ("256x256", 0, 3, 515, 2112, 12352, PLAIN, BF16), ("256x256", 0, 3, 515, 1088, 12352, GATED, BF16),
     ("tiles", 1, 8, 17, 64, 64, GATED, FP32), ("tiles", 2, 8, 65, 64, 512, PLAIN, FP32),
     ("tiles", 4, 3, 17, 64, 1024, GATED, FP32), ("tiles", 8, 3, 33, 64, 2048, PLAIN, FP32),
     ("tiles", 16, 3, 17, 64, 4096, GATED, FP32), ("tiles", 1, 8, 1301, 1088, 128, PLAIN, FP32),
@@ -128,6 +133,7 @@ CLAMPED = [  # (path, slices, E, T, k, N, K, act, type)
     ("rows", 1, 4, 32, 2, 128, 128, "none", BF16), ("tiles", 8, 4, 1301, 2, 64, 2048, "none", BF16),
     ("tiles", 1, 4, 2000, 2, 192, 64, "swiglu", BF16), ("256x128", 1, 4, 451, 2, 4160, 704, "none", BF16),
     ("256x256", 1, 4, 1300, 2, 4160, 192, "none", BF16), ("256x256", 1, 4, 1300, 2, 2112, 192, "swiglu", BF16),
+    ("256x128", 0, 4, 1050, 2, 320, 8192, "none", BF16), ("256x256", 0, 4, 258, 2, 2112, 8192, "swiglu", BF16),
     ("tiles", 8, 4, 17, 2, 64, 2048, "none", FP32), ("tiles", 1, 4, 600, 2, 1088, 128, "swiglu", FP32),
 ]
 
@@ -166,6 +172,8 @@ OVERLAPPING = [  # (path, slices, rows, N, K, act, type), 16 experts
     ("tiles", 16, 1300, 64, 4096, "none", BF16), ("tiles", 2, 200, 960, 2048, "none", BF16),
     ("tiles", 8, 900, 64, 4096, "swiglu", BF16), ("256x128", 1, 5000, 1088, 512, "none", BF16),
     ("256x128", 1, 5000, 448, 704, "swiglu", BF16), ("256x256", 1, 5000, 4160, 64, "swiglu", BF16),
+    ("256x128", 0, 4000, 192, 9216, "none", BF16), ("256x128", 0, 4000, 64, 12352, "swiglu", BF16),
+    ("256x256", 0, 4000, 448, 9216, "none", BF16), ("256x256", 0, 515, 1344, 8192, "swiglu", BF16),
 ]
 
 

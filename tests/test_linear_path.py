@@ -51,3 +51,31 @@ def test_workspace_agrees(E, act, dt):
                         moe.moe_linear_grouped_workspace_bytes(E, M, N, K, act, dt))
                 many = slices > 1 or (path.startswith("256") and E is not None)
                 assert (need > 0) == many, (M, N, K, path, slices, need)
+
+
+# (M, N, K, act): a few 256-row tiles whose K slices leave most of the chip idle. The
+# other paths were two to four times as fast, with a workspace of at most a few MiB.
+FEW_TILES = [
+    (1, 64, 8192, "none"), (16, 64, 8192, "none"), (64, 64, 8192, "none"), (256, 64, 8192, "none"),
+    (1024, 64, 8192, "none"), (16, 512, 8192, "none"), (128, 512, 8192, "none"), (256, 512, 8192, "none"),
+    (64, 1024, 8192, "none"), (256, 1024, 8192, "none"), (64, 512, 14336, "none"), (512, 512, 14336, "none"),
+    (128, 1024, 14336, "none"), (256, 64, 28672, "none"), (64, 1024, 28672, "none"), (64, 512, 8192, "swiglu"),
+    (256, 512, 8192, "swiglu"),
+]
+
+
+@pytest.mark.parametrize("M,N,K,act", FEW_TILES)
+def test_long_k_with_few_tiles(M, N, K, act):
+    path, _ = moe.moe_linear_path(M, N, K, act, 1)
+    assert path in ("rows", "tiles")
+    assert moe.moe_linear_workspace_bytes(M, N, K, act, 1) <= 16 << 20
+
+
+@pytest.mark.parametrize("M,N,K,path", [
+    (256, 4096, 8192, "256x128"), (512, 4096, 8192, "256x128"), (1024, 1024, 8192, "256x128"),
+    (2048, 4096, 8192, "256x128"), (256, 4096, 28672, "256x128"), (1024, 512, 28672, "256x128"),
+])
+def test_long_k_with_enough_tiles(M, N, K, path):
+    """Where the large tiles are the fastest, the smaller of the two (their K slices fill
+    the chip with half the rows)."""
+    assert moe.moe_linear_path(M, N, K, "none", 1)[0] == path

@@ -475,11 +475,12 @@ LinPlan lin_plan(const LinArgs& a) {
     const double tiles = row_tiles(256) * std::ceil(cols / bn);
     const double start = 8.0 + (a.offsets ? 2.0 : 0.0);
     if (a.K >= plan::kSplitMinK) {
-      const int each = (int)std::ceil(tiles / plan::kXcds);  // tiles of an XCD
-      const int rounds = each / plan::kSlots, tail = each % plan::kSlots;
+      const long long each = (long long)std::ceil(tiles / plan::kXcds);  // tiles of an XCD
+      const long long rounds = each / plan::kSlots;
+      const int tail = (int)(each % plan::kSlots);
       const int spl = plan::tail_slices(tail, a.K / plan::kStageK);
       if (spl > 1) {
-        const double last = std::min(tiles, (double)plan::kXcds * each) - 256.0 * rounds;
+        const double last = tiles - 256.0 * rounds;
         return Large{start + stages * rounds * full +
                          std::ceil(stages / spl) * std::max(idle, full * tail * spl / plan::kSlots) +
                          3.0 + last * spl * 256 * bn * 4 / 3.3e6,

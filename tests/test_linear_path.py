@@ -79,3 +79,11 @@ def test_long_k_with_enough_tiles(M, N, K, path):
     """Where the large tiles are the fastest, the smaller of the two (their K slices fill
     the chip with half the rows)."""
     assert moe.moe_linear_path(M, N, K, "none", 1)[0] == path
+
+
+def test_refused_sizes_are_refused_whatever_they_would_cost():
+    """Row and column counts whose tiles no int holds, at a K that the large tiles slice."""
+    for rows, N, K in ((2 ** 31 - 1, (1 << 18) - 64, 8192), (2 ** 31 - 1, 1 << 17, 8192), (2 ** 31 - 1, 64, 8192)):
+        for grouped in (0, 1):
+            got = query(E=256 if grouped else 1, rows=rows, N=N, K=K, grouped=grouped)
+            assert got == -2

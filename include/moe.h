@@ -384,7 +384,8 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
  *            groups, descending, equal ones to the lower expert id
  *   topk_w[t,j] = scale * p[t,idx_j] / (renorm ? sum_j' p[t,idx_j'] : 1)
  * Without a bias the experts are ordered by s (the same order as p, kept where
- * p rounds to 0 or 1).
+ * p rounds to 0 or 1). v is worked out with the hardware's exp2 and reciprocal,
+ * as is the softmax's sum (about 2e-7 relative); the weights' p with expf.
  * An expert with a bias of -inf or NaN, or a NaN score, is off: it counts in no
  * group's score (a group with one expert left scores that one alone) and is
  * chosen only when fewer than k experts of the chosen groups are on, then with

@@ -335,8 +335,8 @@ hipError_t launch_bf16_bt(const void* x, const void* wg, const GroupArgs& a, int
 
 // bf16 calls take the paths of moe_route, except that few tokens with a small Wg (256 KB)
 // take one launch too: a workgroup of 16 tokens reads all of it at about 60 GB/s, which
-// costs the GPU 0 to 3 us more than two launches (H 2048, E 60, T 16: 12.2 against 8.8;
-// T 1777: 12.3 against 11.2; H 1024, E 16: 5.9 against 7.9) and saves the host the second
+// costs the GPU 0 to 3 us more than two launches (H 2048, E 60, T 16: 12.6 against 9.4;
+// T 1777: 12.9 against 11.6; H 1024, E 16: 5.1 against 7.3) and saves the host the second
 // one and the workspace (5 us). At 512 KB one launch takes up to twice as long.
 bool one_launch(int T, int H, int E, bool bf16) {
   return bf16 && (route_mode(T, E, true) == kOneLaunch ||

@@ -221,11 +221,18 @@ __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
 #pragma unroll
     for (int q = 0; q < NI; ++q) lds_dma16(src[q] + (size_t)kt * BK, base + (wave * NI + q) * 1024);
   };
-  f32x4_t acc[TM][TN];
+  // fp32: 4 sums per output, for each half of a stage and every other MFMA, added up
+  // behind the loop. One chain over K rounds partial sums as large as the result; 4 are
+  // off by half of it (K 4096 against float64, u = 2^-24: 19.2 -> 9.6 u, with a gate 29.3 -> 14.1; 512 x 4096
+  // x 4096 154.6 and 155.4 us)
+  constexpr int NSUM = sizeof(T) == 4 ? 4 : 1;
+  f32x4_t sum[NSUM][TM][TN];
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+  for (int s = 0; s < NSUM; ++s)
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) sum[s][i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const int fx = (wm * (BM / 2) + (lane & 15)) * 128;
   const int fw = (BM + wn * (BN / 2) + (lane & 15)) * 128;
   const int sw = (lane >> 1) & 7;  // (row >> 1) & 7 of every fragment row of this lane
@@ -251,9 +258,34 @@ __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = mma16<T>(wf[j], xf[i], acc[i][j]);
+        for (int j = 0; j < TN; ++j) {
+          if constexpr (NSUM == 1) {
+            sum[0][i][j] = mma16<T>(wf[j], xf[i], sum[0][i][j]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              sum[ks * 2 + q % 2][i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                  __uint_as_float(wf[j][q]), __uint_as_float(xf[i][q]), sum[ks * 2 + q % 2][i][j], 0, 0, 0);
+          }
+        }
+    }
+    if constexpr (NSUM > 1) {  // held in accumulation registers from stage to stage
+#pragma unroll
+      for (int s = 0; s < NSUM; ++s)
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(sum[s][i][j]));
     }
   }
+  f32x4_t acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      acc[i][j] = sum[0][i][j];
+      if constexpr (NSUM > 1) acc[i][j] = (acc[i][j] + sum[1][i][j]) + (sum[2][i][j] + sum[3][i][j]);
+    }
   if (gridDim.y == 1) {
     tile_store<T, Sh>(a, t, acc);
     return;

@@ -223,8 +223,8 @@ __global__ __launch_bounds__(kThreads) void lin_tile_kernel(LinArgs a) {
   };
   // fp32: 4 sums per output, for each half of a stage and every other MFMA, added up
   // behind the loop. One chain over K rounds partial sums as large as the result; 4 are
-  // off by half of it (K 4096 against float64, u = 2^-24: 19.2 -> 9.6 u, with a gate 29.3 -> 14.1; 512 x 4096
-  // x 4096 154.6 and 155.4 us)
+  // off by half as much (512 x 4096 x 4096 against float64, u = 2^-24: 19.2 -> 9.6 u, with
+  // a gate 29.3 -> 14.1; 154.6 and 155.4 us)
   constexpr int NSUM = sizeof(T) == 4 ? 4 : 1;
   f32x4_t sum[NSUM][TM][TN];
 #pragma unroll

@@ -17,6 +17,9 @@
  *   moe_route_grouped  sigmoid / softmax scores, choice bias, groups, top-k
  *   moe_linear, moe_linear_grouped  product with bias, activation or gate, and
  *                  residual; grouped: over the experts' segments
+ * the same products in 8-bit floating point:
+ *   moe_quantize, moe_quantize_weight  rows and weights to e4m3 with block scales
+ *   moe_linear_fp8, moe_linear_grouped_fp8  products of such operands
  * and, after the layer, the routing-bias feedback of the next step:
  *   moe_bias_update dynamic bias B from the expert counts, load fractions f_i
  *   (the mean router probabilities P_i are an optional output of moe_route)
@@ -477,6 +480,84 @@ typedef enum {
  * takes MOE_PATH_TILES with one slice in place of the 256-row tiles.
  */
 int moe_linear_path(int E, int rows, int N, int K, int act, int grouped, int dtype, int* slices);
+
+/*
+ * moe_quantize - rows to 8-bit floating point (e4m3, the OCP form without
+ * infinities, largest value 448) with one scale for each block of 128 elements:
+ *   amax       = the largest finite |x| of elements 128 b .. 128 b + 127 of row r
+ *   scale[b,r] = the least power of two s with amax / s <= 448, 2^-126 at least;
+ *                1 if amax = 0
+ *   q[r,c]     = x[r,c] / scale[c / 128, r], rounded once (nearest, ties to even);
+ *                NaN for an infinity or NaN, which the scale leaves out
+ * x     [rows,K] dtype         device, read
+ * q     [rows,K] e4m3 bytes    device, written
+ * scale [K/128,rows] fp32      device, written (the rows of a block side by side)
+ * K % 128 == 0; rows * K up to about 2^37 (else MOE_ERR_UNSUPPORTED). x and q
+ * 16-byte, scale 4-byte aligned; outputs that overlap each other or x are
+ * MOE_ERR_INVALID_ARG. No workspace.
+ */
+int moe_quantize(const void* x, int rows, int K, int dtype, void* q, float* scale, void* stream);
+
+/*
+ * moe_quantize_weight - the same for weights, with one scale for each block of 128
+ * rows x 128 elements (the last block of an N that is no multiple of 128 has fewer
+ * rows):
+ *   scale[i,n/128,b] as above over the block, q[i,n,c] = w[i,n,c] / scale
+ * w [count,N,K] dtype, q [count,N,K] e4m3, scale [count,ceil(N/128),K/128] fp32. count:
+ * the matrices (experts, and gate and up halves). N % 64 == 0, else as moe_quantize.
+ */
+int moe_quantize_weight(const void* w, int count, int N, int K, int dtype, void* q, float* scale,
+                        void* stream);
+
+/*
+ * moe_linear_fp8 - moe_linear of e4m3 operands with block scales, in bf16:
+ *   a[m,n] = sum_b x_scale[b,m] * w_scale[n/128,b] *
+ *            sum_{k = 128 b .. 128 b + 127} x[m,k] * w[n,k]      + bias[n]
+ *   y[m,n] = act(a[m,n]) + residual[m,n], or with a gate as moe_linear
+ * The products of a block are summed by the matrix cores (8 neighbours of K at a time, cut
+ * at 2^-13 of the largest of the 8, then in fp32), the blocks scaled and summed in fp32; bias, act, gate and residual as moe_linear's bf16 form; one rounding.
+ * x [M,K] e4m3, x_scale [K/128,M] fp32, w [N,K] or [2,N,K] e4m3, w_scale
+ *   [ceil(N/128),K/128] or [2,ceil(N/128),K/128] fp32 (any values: those of
+ *   moe_quantize and moe_quantize_weight, or a checkpoint's), bias [N] or [2,N] bf16 or
+ *   NULL, residual [M,N] bf16 or NULL: device, read; y [M,N] bf16: device, written; it
+ *   may be residual itself.
+ * K % 128 == 0, N % 64 == 0. Scales 4-byte, the others 16-byte aligned. Sizes whose
+ * tiles do not fit a launch are MOE_ERR_UNSUPPORTED, an output or workspace that
+ * overlaps another operand (other than y being residual) MOE_ERR_INVALID_ARG.
+ * ws / ws_bytes: moe_linear_fp8_workspace_bytes(M,N,K,act) (NULL allowed when that is 0)
+ */
+int moe_linear_fp8(const void* x, const float* x_scale, const void* w, const float* w_scale,
+                   const void* bias, int act, const void* residual, int M, int N, int K, void* y,
+                   void* ws, size_t ws_bytes, void* stream);
+size_t moe_linear_fp8_workspace_bytes(int M, int N, int K, int act);
+
+/*
+ * moe_linear_grouped_fp8 - moe_linear_fp8 over the experts' ragged segments, as
+ * moe_linear_grouped: buffer row p in [offsets[e], offsets[e+1]) takes w[e], w_scale[e]
+ * and bias[e]; rows of y past offsets[E] are left as they were.
+ * x [rows,K] and x_scale [K/128,rows], or with perm the token rows [T,K] and
+ *   [K/128,T]: buffer row p then reads row perm[p] / k (clamped into x)
+ * w [E,N,K] or [E,2,N,K], w_scale [E,ceil(N/128),K/128] or [E,2,ceil(N/128),K/128].
+ * perm, k, T, offsets, rows, bias, residual, y as moe_linear_grouped; the rest as
+ * moe_linear_fp8.
+ * ws / ws_bytes: moe_linear_grouped_fp8_workspace_bytes(E,rows,N,K,act)
+ */
+int moe_linear_grouped_fp8(const void* x, const float* x_scale, const int32_t* perm, int k, int T,
+                           const int32_t* offsets, int E, int rows, const void* w,
+                           const float* w_scale, const void* bias, int act, const void* residual,
+                           int N, int K, void* y, void* ws, size_t ws_bytes, void* stream);
+size_t moe_linear_grouped_fp8_workspace_bytes(int E, int rows, int N, int K, int act);
+
+typedef enum {
+  MOE_FP8_ROWS = 0,    /* few rows: weights straight to registers */
+  MOE_FP8_64X64 = 1,   /* tiles of 64 rows x 64 weight rows, K slices */
+  MOE_FP8_128X128 = 2, /* tiles of 128 rows x 128 weight rows */
+  MOE_FP8_256X256 = 3  /* tiles of 256 rows x 256 weight rows */
+} moe_fp8_path;
+
+/* The kernels and K slices that an 8-bit product of these sizes takes, as
+ * moe_linear_path: a moe_fp8_path, or a negative status. */
+int moe_linear_fp8_path(int E, int rows, int N, int K, int act, int grouped, int* slices);
 
 /* Static, human-readable text for a status code. */
 const char* moe_status_string(int status);

@@ -52,6 +52,14 @@ SIGNATURES = {
                                 _vp, _sz, _vp]),
     "moe_linear_grouped_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "moe_linear_path": (_i, [_i, _i, _i, _i, _i, _i, _i, _vp]),
+    "moe_quantize": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp]),
+    "moe_quantize_weight": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "moe_linear_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "moe_linear_fp8_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "moe_linear_grouped_fp8": (_i, [_vp, _vp, _vp, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _i, _vp, _i, _i,
+                                    _vp, _vp, _sz, _vp]),
+    "moe_linear_grouped_fp8_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "moe_linear_fp8_path": (_i, [_i, _i, _i, _i, _i, _i, _vp]),
     "moe_status_string": (ctypes.c_char_p, [_i]),
 }
 
@@ -601,6 +609,12 @@ def _ptr(t, name: str, shape, dtype, device):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _given(t, name: str):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return t
+
+
 def _fits(*sizes):
     """Refuses sizes that a C int does not hold: ctypes would pass their low 32 bits."""
     if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
@@ -849,6 +863,176 @@ def moe_linear_grouped(x, offsets, w, bias=None, act: str = "none", residual=Non
         yp = y.data_ptr()
     _check("moe_linear_grouped", L.moe_linear_grouped(
         xp, pp, k, T, fp, E, rows, wp, bp, code, rp, N, K, dt, yp, wsp, wsn,
+        _raw_stream(dev.index)))
+    return y
+
+
+FP8 = torch.float8_e4m3fn  # 8-bit operands: 4 bits of exponent, 3 of mantissa, no infinities
+FP8_BLOCK = 128            # elements of a scale block
+
+
+def moe_quantize(x, q=None, scale=None, stream=None):
+    """Rows x [rows,K] (bf16 or fp32) as float8_e4m3fn with one scale for each block of
+    128 elements: x = q * scale. The scales are powers of two (one rounding), the least
+    with |q| <= 448. K a multiple of 128. Returns (q [rows,K], scale fp32 [K/128,rows])."""
+    rows, K = _shape(x, "x", 2)
+    _fits(rows, K)
+    dev, dtype = x.device, x.dtype
+    dt = _dtype_code(x)
+    sshape = (K // FP8_BLOCK, rows)
+    xp = _ptr(x, "x", (rows, K), dtype, dev)
+    qp = _ptr(q, "q", (rows, K), FP8, dev)
+    sp = _ptr(scale, "scale", sshape, torch.float32, dev)
+    other = _other_stream(dev, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return moe_quantize(x, q, scale)
+    if q is None:
+        q = torch.empty((rows, K), dtype=FP8, device=dev)
+        qp = q.data_ptr()
+    if scale is None:
+        scale = torch.empty(sshape, dtype=torch.float32, device=dev)
+        sp = scale.data_ptr()
+    _check("moe_quantize", lib().moe_quantize(xp, rows, K, dt, qp, sp, _raw_stream(dev.index)))
+    return q, scale
+
+
+def moe_quantize_weight(w, q=None, scale=None, stream=None):
+    """Weights w [...,N,K] (bf16 or fp32) as float8_e4m3fn with one scale for each block of
+    128 x 128. N a multiple of 64, K of 128. Returns (q [...,N,K], scale fp32
+    [...,ceil(N/128),K/128])."""
+    if not isinstance(w, torch.Tensor) or w.dim() < 2:
+        raise ValueError("w must be a torch tensor of two dimensions or more")
+    *lead, N, K = w.shape
+    count = 1
+    for n in lead:
+        count *= n
+    _fits(count, N, K)
+    dev, dtype = w.device, w.dtype
+    dt = _dtype_code(w)
+    sshape = (*lead, -(-N // FP8_BLOCK), K // FP8_BLOCK)
+    wp = _ptr(w, "w", w.shape, dtype, dev)
+    qp = _ptr(q, "q", w.shape, FP8, dev)
+    sp = _ptr(scale, "scale", sshape, torch.float32, dev)
+    other = _other_stream(dev, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return moe_quantize_weight(w, q, scale)
+    if q is None:
+        q = torch.empty(w.shape, dtype=FP8, device=dev)
+        qp = q.data_ptr()
+    if scale is None:
+        scale = torch.empty(sshape, dtype=torch.float32, device=dev)
+        sp = scale.data_ptr()
+    _check("moe_quantize_weight", lib().moe_quantize_weight(wp, count, N, K, dt, qp, sp,
+                                                            _raw_stream(dev.index)))
+    return q, scale
+
+
+def moe_linear_fp8_workspace_bytes(M: int, N: int, K: int, act: str) -> int:
+    _fits(M, N, K)
+    return lib().moe_linear_fp8_workspace_bytes(M, N, K, _enum(ACTS, act, "act"))
+
+
+def moe_linear_fp8(x, x_scale, w, w_scale, bias=None, act: str = "none", residual=None, y=None,
+                   ws=None, stream=None):
+    """moe_linear of 8-bit operands with block scales; y in bf16.
+
+    x [M,K] float8_e4m3fn with x_scale fp32 [K/128,M] (moe_quantize), w [N,K] (gated:
+    [2,N,K]) with w_scale fp32 [ceil(N/128),K/128] ([2,...]; moe_quantize_weight, or
+    a checkpoint's scales of any value); bias, residual and y bf16. K a multiple of 128, N
+    of 64. y may be residual itself. Returns y."""
+    M, K = _shape(x, "x", 2)
+    code = _enum(ACTS, act, "act")
+    two = (2,) if code >= 3 else ()
+    N = _shape(w, "w", 2 + len(two))[-2]
+    _fits(M, N, K)
+    dev, bf16 = x.device, torch.bfloat16
+    nkb, nnb = K // FP8_BLOCK, -(-N // FP8_BLOCK)
+    xp, wp = _ptr(x, "x", (M, K), FP8, dev), _ptr(w, "w", (*two, N, K), FP8, dev)
+    xsp = _ptr(_given(x_scale, "x_scale"), "x_scale", (nkb, M), torch.float32, dev)
+    wsc = _ptr(_given(w_scale, "w_scale"), "w_scale", (*two, nnb, nkb), torch.float32, dev)
+    bp = _ptr(bias, "bias", (*two, N), bf16, dev)
+    rp, yp = _ptr(residual, "residual", (M, N), bf16, dev), _ptr(y, "y", (M, N), bf16, dev)
+    other = _other_stream(dev, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return moe_linear_fp8(x, x_scale, w, w_scale, bias, act, residual, y, ws)
+    L = lib()
+    wsp, wsn, ws = _ws(L.moe_linear_fp8_workspace_bytes(M, N, K, code), dev, ws)
+    if y is None:
+        y = torch.empty((M, N), dtype=bf16, device=dev)
+        yp = y.data_ptr()
+    _check("moe_linear_fp8", L.moe_linear_fp8(xp, xsp, wp, wsc, bp, code, rp, M, N, K, yp, wsp, wsn,
+                                              _raw_stream(dev.index)))
+    return y
+
+
+def moe_linear_grouped_fp8_workspace_bytes(E: int, rows: int, N: int, K: int, act: str) -> int:
+    _fits(E, rows, N, K)
+    return lib().moe_linear_grouped_fp8_workspace_bytes(E, rows, N, K, _enum(ACTS, act, "act"))
+
+
+FP8_PATHS = ("rows", "64x64", "128x128", "256x256")
+
+
+def moe_linear_fp8_path(M: int, N: int, K: int, act: str, E: int | None = None):
+    """(kernels, K slices) of an 8-bit product, as moe_linear_path: "rows", "64x64",
+    "128x128" or "256x256"."""
+    _fits(M, N, K, E or 1)
+    n = ctypes.c_int(0)
+    path = lib().moe_linear_fp8_path(1 if E is None else E, M, N, K, _enum(ACTS, act, "act"),
+                                     int(E is not None), ctypes.byref(n))
+    if path < 0:
+        _check("moe_linear_fp8_path", path)
+    return FP8_PATHS[path], n.value
+
+
+def moe_linear_grouped_fp8(x, x_scale, offsets, w, w_scale, bias=None, act: str = "none",
+                           residual=None, perm=None, k: int = 1, rows=None, y=None, ws=None,
+                           stream=None):
+    """moe_linear_fp8 over the experts' segments, as moe_linear_grouped.
+
+    w [E,N,K] (gated: [E,2,N,K]) with w_scale [E,ceil(N/128),K/128] ([E,2,...]). Without
+    perm, x is the buffer [rows,K] with x_scale [K/128,rows]; with perm x is the token
+    rows [T,K] with x_scale [K/128,T], and row p reads row perm[p] // k. Returns y
+    [rows,N] in bf16; its rows past offsets[E] are left as they were."""
+    T, K = _shape(x, "x", 2)
+    code = _enum(ACTS, act, "act")
+    two = (2,) if code >= 3 else ()
+    dims = _shape(w, "w", 3 + len(two))
+    E, N = dims[0], dims[-2]
+    dev, bf16 = x.device, torch.bfloat16
+    most = T if perm is None else T * k
+    if rows is None:
+        rows = most
+    _fits(T, K, E, N, k, rows)
+    if not 1 <= rows <= most:
+        raise ValueError(f"rows {rows} outside [1, {most}]")
+    if perm is not None and _shape(perm, "perm", 1)[0] < rows:
+        raise ValueError(f"perm must have at least rows = {rows} entries")
+    if perm is None and rows != T:
+        raise ValueError(f"rows {rows} without perm must be x's {T} (x_scale has that many columns)")
+    nkb, nnb = K // FP8_BLOCK, -(-N // FP8_BLOCK)
+    xp, wp = _ptr(x, "x", (T, K), FP8, dev), _ptr(w, "w", (E, *two, N, K), FP8, dev)
+    xsp = _ptr(_given(x_scale, "x_scale"), "x_scale", (nkb, T), torch.float32, dev)
+    wsc = _ptr(_given(w_scale, "w_scale"), "w_scale", (E, *two, nnb, nkb), torch.float32, dev)
+    fp = _ptr(_given(offsets, "offsets"), "offsets", (E + 1,), torch.int32, dev)
+    pp = None if perm is None else _ptr(perm, "perm", perm.shape, torch.int32, dev)
+    bp = _ptr(bias, "bias", (E, *two, N), bf16, dev)
+    rp, yp = _ptr(residual, "residual", (rows, N), bf16, dev), _ptr(y, "y", (rows, N), bf16, dev)
+    other = _other_stream(dev, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return moe_linear_grouped_fp8(x, x_scale, offsets, w, w_scale, bias, act, residual, perm,
+                                          k, rows, y, ws)
+    L = lib()
+    wsp, wsn, ws = _ws(L.moe_linear_grouped_fp8_workspace_bytes(E, rows, N, K, code), dev, ws)
+    if y is None:
+        y = torch.empty((rows, N), dtype=bf16, device=dev)
+        yp = y.data_ptr()
+    _check("moe_linear_grouped_fp8", L.moe_linear_grouped_fp8(
+        xp, xsp, pp, k, T, fp, E, rows, wp, wsc, bp, code, rp, N, K, yp, wsp, wsn,
         _raw_stream(dev.index)))
     return y
 

@@ -67,6 +67,21 @@ hipError_t launch_linear(const void* x, const int32_t* gather, int gk, int gT,
                          const void* bias, int act, const void* res, bool bf16, void* y, void* ws,
                          hipStream_t s);
 
+bool quantize_fits(int rows, int K);
+bool quantize_weight_fits(int count, int N, int K);
+hipError_t launch_quantize(const void* x, int rows, int K, bool bf16, void* q, float* scale,
+                           hipStream_t s);
+hipError_t launch_quantize_weight(const void* w, int count, int N, int K, bool bf16, void* q,
+                                  float* scale, hipStream_t s);
+
+bool linear_fp8_fits(int E, int M, int N, int K, int act, bool grouped);
+size_t linear_fp8_ws_bytes(int E, int M, int N, int K, int act, bool grouped);
+int linear_fp8_path(int E, int M, int N, int K, int act, bool grouped, int* slices);
+hipError_t launch_linear_fp8(const void* x, const float* x_scale, const int32_t* gather, int gk,
+                             int gT, const int32_t* offsets, int E, int M, int N, int K,
+                             const void* w, const float* w_scale, const void* bias, int act,
+                             const void* res, void* y, void* ws, hipStream_t s);
+
 hipError_t launch_bias_update(const int32_t* counts, int E, float gamma, float* bias,
                               float* load_frac, hipStream_t s);
 

@@ -27,100 +27,6 @@ using namespace lin;
 
 constexpr int kThreads = 256;
 
-struct LinTile {
-  int e, row0, M, n0;  // expert; first buffer row and rows of the tile; first output column
-  int q;               // number of the tile
-};
-
-// Row tile `mt` of BM rows of the segments: each wave finds it for itself (no
-// barrier): lane l sums the row tiles of experts 4 l .. 4 l + 3, a wave scan
-// orders the lanes. Segments are clamped into the buffer, whatever the offsets
-// hold. total: all row tiles.
-struct SegScan {
-  int off[4], cnt[4], nb[4];
-  int incl, total;
-};
-template <int BM>
-__device__ __forceinline__ void scan_segments(const LinArgs& a, SegScan& s) {
-  const int lane = threadIdx.x & 63;
-  int sum = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int e = lane * 4 + j;
-    s.off[j] = s.cnt[j] = 0;
-    if (e < a.E) {
-      s.off[j] = min(max(a.offsets[e], 0), a.M);
-      s.cnt[j] = min(max(a.offsets[e + 1], s.off[j]), a.M) - s.off[j];
-    }
-    s.nb[j] = (s.cnt[j] + BM - 1) / BM;
-    sum += s.nb[j];
-  }
-  s.incl = sum;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(s.incl, d);
-    if (lane >= d) s.incl += v;
-  }
-  s.total = __shfl(s.incl, 63);
-}
-
-// The tile of this workgroup, BM rows x bnc output columns. Tiles are numbered
-// segment by segment, column tile by column tile, row tile by row tile, and XCD
-// x (workgroups x, x + 8, ...) takes a contiguous run of them: the tiles that
-// share a weight panel run on one XCD at about one time. M = 0: no work.
-template <int BM>
-__device__ __forceinline__ LinTile lin_tile(const LinArgs& a, int bnc) {
-  LinTile t{};
-  const int ntn = (a.N + bnc - 1) / bnc;
-  const int g = blockIdx.x;
-  if (a.offsets == nullptr) {
-    const int nm = (a.M + BM - 1) / BM;
-    const long long total = (long long)nm * ntn;
-    const int chunk = (int)((total + 7) / 8);
-    const long long q = (long long)(g & 7) * chunk + (g >> 3);
-    if ((g >> 3) >= chunk || q >= total) return t;
-    t.e = 0;
-    t.q = (int)q;
-    t.row0 = t.q % nm * BM;
-    t.n0 = t.q / nm * bnc;
-    const int left = a.M - t.row0;
-    t.M = left < BM ? left : BM;
-    return t;
-  }
-  SegScan s;
-  scan_segments<BM>(a, s);
-  // offsets that overlap could name more tiles than the launch has room for: the rest is
-  // left out
-  const long long total = min((long long)s.total * ntn, (long long)a.tiles);
-  const int chunk = (int)((total + 7) / 8);
-  const long long q = (long long)(g & 7) * chunk + (g >> 3);
-  if ((g >> 3) >= chunk || q >= total) return t;
-  const int lane = threadIdx.x & 63;
-  int excl = s.incl;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) excl -= s.nb[j];
-  const bool mine = q >= (long long)excl * ntn && q < (long long)s.incl * ntn;
-  const int src = __ffsll((unsigned long long)__ballot(mine)) - 1;
-  int e = 0, off = 0, cnt = 0, nb = 1, base = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (mine && q >= (long long)excl * ntn && q < (long long)(excl + s.nb[j]) * ntn)
-      e = lane * 4 + j, off = s.off[j], cnt = s.cnt[j], nb = s.nb[j], base = excl;
-    excl += s.nb[j];
-  }
-  e = __shfl(e, src), off = __shfl(off, src), cnt = __shfl(cnt, src);
-  nb = __shfl(nb, src), base = __shfl(base, src);
-  const int local = (int)(q - (long long)base * ntn);
-  const int m = local % nb;
-  t.e = e;
-  t.q = (int)q;
-  t.row0 = off + m * BM;
-  const int left = cnt - m * BM;
-  t.M = left < BM ? left : BM;
-  t.n0 = local / nb * bnc;
-  return t;
-}
-
 // ----------------------------------------------------------------- 64 x 64 tiles
 
 // Tiles of BM rows x 64 weight rows (64 output columns, or 32 of a gated

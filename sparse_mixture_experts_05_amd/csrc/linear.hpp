@@ -68,6 +68,111 @@ __device__ __forceinline__ size_t x_row(const LinArgs& a, int p) {
   return (size_t)((unsigned)min(max(a.gather[p], 0), a.gT * a.gk - 1) / (unsigned)a.gk);
 }
 
+struct LinTile {
+  int e, row0, M, n0;  // expert; first buffer row and rows of the tile; first output column
+  int q;               // number of the tile
+};
+
+// Row tile `mt` of BM rows of the segments: each wave finds it for itself (no
+// barrier): lane l sums the row tiles of experts 4 l .. 4 l + 3, a wave scan
+// orders the lanes. Segments are clamped into the buffer, whatever the offsets
+// hold. total: all row tiles.
+struct SegScan {
+  int off[4], cnt[4], nb[4];
+  int incl, total;
+};
+template <int BM>
+__device__ __forceinline__ void scan_segments(const LinArgs& a, SegScan& s) {
+  const int lane = threadIdx.x & 63;
+  int sum = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = lane * 4 + j;
+    s.off[j] = s.cnt[j] = 0;
+    if (e < a.E) {
+      s.off[j] = min(max(a.offsets[e], 0), a.M);
+      s.cnt[j] = min(max(a.offsets[e + 1], s.off[j]), a.M) - s.off[j];
+    }
+    s.nb[j] = (s.cnt[j] + BM - 1) / BM;
+    sum += s.nb[j];
+  }
+  s.incl = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(s.incl, d);
+    if (lane >= d) s.incl += v;
+  }
+  s.total = __shfl(s.incl, 63);
+}
+
+// Number `local` of a segment's tiles, nm row tiles by ntn column tiles: blocks of GN
+// column tiles, row tile by row tile inside a block (GN = 1: column tile by column
+// tile). Returns (row tile, column tile).
+template <int GN>
+__device__ __forceinline__ int2 order_tile(int local, int nm, int ntn) {
+  if constexpr (GN == 1) return make_int2(local % nm, local / nm);
+  const int blk = local / (nm * GN), li = local - blk * nm * GN;
+  const int w = min(GN, ntn - blk * GN);
+  return make_int2(li / w, blk * GN + li % w);
+}
+
+// The tile of this workgroup, BM rows x bnc output columns. Tiles are numbered
+// segment by segment, in a segment by order_tile, and XCD
+// x (workgroups x, x + 8, ...) takes a contiguous run of them: the tiles that
+// share a weight panel run on one XCD at about one time. M = 0: no work.
+template <int BM, int GN = 1>
+__device__ __forceinline__ LinTile lin_tile(const LinArgs& a, int bnc) {
+  LinTile t{};
+  const int ntn = (a.N + bnc - 1) / bnc;
+  const int g = blockIdx.x;
+  if (a.offsets == nullptr) {
+    const int nm = (a.M + BM - 1) / BM;
+    const long long total = (long long)nm * ntn;
+    const int chunk = (int)((total + 7) / 8);
+    const long long q = (long long)(g & 7) * chunk + (g >> 3);
+    if ((g >> 3) >= chunk || q >= total) return t;
+    t.e = 0;
+    t.q = (int)q;
+    const int2 at = order_tile<GN>(t.q, nm, ntn);
+    t.row0 = at.x * BM;
+    t.n0 = at.y * bnc;
+    const int left = a.M - t.row0;
+    t.M = left < BM ? left : BM;
+    return t;
+  }
+  SegScan s;
+  scan_segments<BM>(a, s);
+  // offsets that overlap could name more tiles than the launch has room for: the rest is
+  // left out
+  const long long total = min((long long)s.total * ntn, (long long)a.tiles);
+  const int chunk = (int)((total + 7) / 8);
+  const long long q = (long long)(g & 7) * chunk + (g >> 3);
+  if ((g >> 3) >= chunk || q >= total) return t;
+  const int lane = threadIdx.x & 63;
+  int excl = s.incl;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) excl -= s.nb[j];
+  const bool mine = q >= (long long)excl * ntn && q < (long long)s.incl * ntn;
+  const int src = __ffsll((unsigned long long)__ballot(mine)) - 1;
+  int e = 0, off = 0, cnt = 0, nb = 1, base = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (mine && q >= (long long)excl * ntn && q < (long long)(excl + s.nb[j]) * ntn)
+      e = lane * 4 + j, off = s.off[j], cnt = s.cnt[j], nb = s.nb[j], base = excl;
+    excl += s.nb[j];
+  }
+  e = __shfl(e, src), off = __shfl(off, src), cnt = __shfl(cnt, src);
+  nb = __shfl(nb, src), base = __shfl(base, src);
+  const int2 at = order_tile<GN>((int)(q - (long long)base * ntn), nb, ntn);
+  t.e = e;
+  t.q = (int)q;
+  t.row0 = off + at.x * BM;
+  const int left = cnt - at.x * BM;
+  t.M = left < BM ? left : BM;
+  t.n0 = at.y * bnc;
+  return t;
+}
+
 // Output of one lane: 4 consecutive columns of a row (bf16, 8-byte aligned).
 struct Out4 {
   float v[4];

@@ -410,4 +410,115 @@ int moe_linear_grouped(const void* x, const int32_t* perm, int k, int T, const i
                     ws_bytes, stream);
 }
 
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+size_t scale_blocks(int n) { return ((size_t)n + 127) / 128; }
+
+int check_quantize(int count, int N, int K, int dtype, const void* x, const void* q,
+                   const float* scale, size_t scales) {
+  if (!x || !q || !scale || count < 1 || N < 1 || K < 1 || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q) || !aligned4(scale)) return MOE_ERR_INVALID_ARG;
+  if (K % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  const size_t n = (size_t)count * N * K;
+  const Span sx{x, n * elem(dtype)}, ss{scale, scales * sizeof(float)};
+  return overlap_any(q, n, {sx, ss}) || overlap_any(scale, ss.n, {sx}) ? MOE_ERR_INVALID_ARG : MOE_OK;
+}
+
+int check_linear_fp8(int E, int M, int N, int K, int act, bool grouped) {
+  if (E < 1 || M < 1 || N < 1 || K < 1 || act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU)
+    return MOE_ERR_INVALID_ARG;
+  if (E > kMaxExperts || N % 64 != 0 || K % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  return moe::linear_fp8_fits(E, M, N, K, act, grouped) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+int run_linear_fp8(const void* x, const float* x_scale, const int32_t* perm, int k, int T,
+                   const int32_t* offsets, int E, int M, const void* w, const float* w_scale,
+                   const void* bias, int act, const void* residual, int N, int K, void* y, void* ws,
+                   size_t ws_bytes, void* stream) {
+  if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned_or_null(bias) ||
+      !aligned_or_null(residual) || !aligned_or_null(ws) || !aligned4(x_scale) || !aligned4(w_scale))
+    return MOE_ERR_INVALID_ARG;
+  const size_t ny = (size_t)M * N * 2, xr = (size_t)(perm ? T : M), nkb = (size_t)K / 128;
+  const size_t mats = (size_t)E * (act == MOE_ACT_GEGLU || act == MOE_ACT_SWIGLU ? 2 : 1);
+  const Span sx{x, xr * K}, sxs{x_scale, xr * nkb * 4}, sw{w, mats * N * K};
+  const Span sws{w_scale, mats * scale_blocks(N) * nkb * 4}, sb{bias, mats * N * 2};
+  const Span so{offsets, (size_t)(E + 1) * sizeof(int32_t)}, sp{perm, (size_t)M * sizeof(int32_t)};
+  if (overlap_any(y, ny, {sx, sxs, sw, sws, sb, so, sp}) ||
+      (y != residual && overlap(y, ny, residual, ny)))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = moe::linear_fp8_ws_bytes(E, M, N, K, act, offsets != nullptr);
+  if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (overlap_any(ws, need, {sx, sxs, sw, sws, sb, so, sp, Span{residual, ny}, Span{y, ny}}))
+    return MOE_ERR_INVALID_ARG;
+  return from_hip(moe::launch_linear_fp8(x, x_scale, perm, k, T, offsets, E, M, N, K, w, w_scale, bias,
+                                         act, residual, y, ws, as_stream(stream)));
+}
+
+}  // namespace
+
+int moe_quantize(const void* x, int rows, int K, int dtype, void* q, float* scale, void* stream) {
+  const int st = check_quantize(1, rows, K, dtype, x, q, scale, rows < 1 || K < 1 ? 0 : (size_t)rows * (K / 128));
+  if (st != MOE_OK) return st;
+  if (!moe::quantize_fits(rows, K)) return MOE_ERR_UNSUPPORTED;
+  return from_hip(moe::launch_quantize(x, rows, K, dtype == MOE_BF16, q, scale, as_stream(stream)));
+}
+
+int moe_quantize_weight(const void* w, int count, int N, int K, int dtype, void* q, float* scale,
+                        void* stream) {
+  const bool sized = count >= 1 && N >= 1 && K >= 1;
+  const int st = check_quantize(count, N, K, dtype, w, q, scale,
+                                sized ? (size_t)count * scale_blocks(N) * (K / 128) : 0);
+  if (st != MOE_OK) return st;
+  if (N % 64 != 0 || !moe::quantize_weight_fits(count, N, K)) return MOE_ERR_UNSUPPORTED;
+  return from_hip(moe::launch_quantize_weight(w, count, N, K, dtype == MOE_BF16, q, scale,
+                                              as_stream(stream)));
+}
+
+size_t moe_linear_fp8_workspace_bytes(int M, int N, int K, int act) {
+  if (check_linear_fp8(1, M, N, K, act, false) != MOE_OK) return 0;
+  return moe::linear_fp8_ws_bytes(1, M, N, K, act, false);
+}
+
+int moe_linear_fp8(const void* x, const float* x_scale, const void* w, const float* w_scale,
+                   const void* bias, int act, const void* residual, int M, int N, int K, void* y,
+                   void* ws, size_t ws_bytes, void* stream) {
+  if (!x || !x_scale || !w || !w_scale || !y) return MOE_ERR_INVALID_ARG;
+  const int st = check_linear_fp8(1, M, N, K, act, false);
+  if (st != MOE_OK) return st;
+  return run_linear_fp8(x, x_scale, nullptr, 1, M, nullptr, 1, M, w, w_scale, bias, act, residual, N, K,
+                        y, ws, ws_bytes, stream);
+}
+
+size_t moe_linear_grouped_fp8_workspace_bytes(int E, int rows, int N, int K, int act) {
+  if (check_linear_fp8(E, rows, N, K, act, true) != MOE_OK) return 0;
+  return moe::linear_fp8_ws_bytes(E, rows, N, K, act, true);
+}
+
+int moe_linear_grouped_fp8(const void* x, const float* x_scale, const int32_t* perm, int k, int T,
+                           const int32_t* offsets, int E, int rows, const void* w,
+                           const float* w_scale, const void* bias, int act, const void* residual,
+                           int N, int K, void* y, void* ws, size_t ws_bytes, void* stream) {
+  if (!x || !x_scale || !offsets || !w || !w_scale || !y) return MOE_ERR_INVALID_ARG;
+  const int st = check_linear_fp8(E, rows, N, K, act, true);
+  if (st != MOE_OK) return st;
+  if (perm) {
+    if (T < 1 || k < 1) return MOE_ERR_INVALID_ARG;
+    if (k > kMaxTopK || (long long)T * k >= (1LL << 31) || rows > (long long)T * k)
+      return MOE_ERR_UNSUPPORTED;
+  }
+  return run_linear_fp8(x, x_scale, perm, k, T, offsets, E, rows, w, w_scale, bias, act, residual, N,
+                        K, y, ws, ws_bytes, stream);
+}
+
+int moe_linear_fp8_path(int E, int rows, int N, int K, int act, int grouped, int* slices) {
+  if ((grouped != 0 && grouped != 1) || (grouped == 0 && E != 1)) return MOE_ERR_INVALID_ARG;
+  const int st = check_linear_fp8(E, rows, N, K, act, grouped != 0);
+  if (st != MOE_OK) return st;
+  int n = 1;
+  const int path = moe::linear_fp8_path(E, rows, N, K, act, grouped != 0, &n);
+  if (slices) *slices = n;
+  return path;
+}
+
 }  // extern "C"

@@ -17,6 +17,8 @@
  *   moe_route_grouped  sigmoid / softmax scores, choice bias, groups, top-k
  *   moe_linear, moe_linear_grouped  product with bias, activation or gate, and
  *                  residual; grouped: over the experts' segments
+ * for a decode step:
+ *   moe_layer_few  the whole layer for up to 64 tokens in two launches
  * the same products in 8-bit floating point:
  *   moe_quantize, moe_quantize_weight  rows and weights to e4m3 with block scales
  *   moe_linear_fp8, moe_linear_grouped_fp8  products of such operands
@@ -558,6 +560,44 @@ typedef enum {
 /* The kernels and K slices that an 8-bit product of these sizes takes, as
  * moe_linear_path: a moe_fp8_path, or a negative status. */
 int moe_linear_fp8_path(int E, int rows, int N, int K, int act, int grouped, int* slices);
+
+/* What a routing bias moves. */
+typedef enum {
+  MOE_BIAS_CHOICE = 0, /* the choice, not the weights (moe_route_grouped) */
+  MOE_BIAS_SCORE = 1   /* the scores themselves (moe_route) */
+} moe_bias_mode;
+
+/*
+ * moe_layer_few - a whole MoE layer for a few tokens (1 <= T <= 64), in two launches:
+ *   s[t,e] = sum_h x[t,h] * wg[e,h]  (+ bias[e] with MOE_BIAS_SCORE)
+ *   topk_idx, topk_w from s as moe_route_grouped (bias as its bias with
+ *            MOE_BIAS_CHOICE, none with MOE_BIAS_SCORE; softmax, MOE_BIAS_SCORE, one
+ *            group, renorm and scale 1 are moe_route)
+ *   h_j    = act(x[t] . w_up[e_j]^T + b_up[e_j]), e_j = topk_idx[t,j]   rounded to dtype
+ *   out[t] = sum_j topk_w[t,j] * (h_j . w_down[e_j]^T + b_down[e_j])
+ *            + act(x[t] . ws_up^T) . ws_down^T              (shared expert, Fs > 0)
+ * Products and sums in fp32; h and out are rounded once each (an expert's row is not
+ * rounded before the weighted sum, as moe_combine's ys are). A gated act has a gate and
+ * an up half as moe_linear. Sums are in an order fixed by the sizes and the choice:
+ * equal calls give equal bits.
+ * x [T,H], wg [E,H], w_up [E,F,H] or [E,2,F,H], w_down [E,H,F], b_up [E,F] or
+ *   [E,2,F] or NULL, b_down [E,H] or NULL, ws_up [Fs,H] or [2,Fs,H], ws_down [H,Fs]
+ *   (NULL / Fs = 0: no shared expert), all dtype; bias [E] fp32 or NULL: device, read
+ * out [T,H] dtype, topk_idx [T,k] int32, topk_w [T,k] fp32: device, written
+ * E, k, H, F, Fs as the layer's, H, F, Fs <= 2^20; routing options as moe_route_grouped.
+ * T > 64 is MOE_ERR_UNSUPPORTED; an output or workspace that overlaps another operand
+ * MOE_ERR_INVALID_ARG.
+ * ws / ws_bytes: device workspace of at least
+ *   moe_layer_few_workspace_bytes(T,H,E,k,F,Fs,dtype); its content does not matter. Calls
+ *   that may run at the same time need workspaces of their own.
+ */
+int moe_layer_few(const void* x, const void* wg, const float* bias, int bias_mode,
+                  const void* w_up, const void* w_down, const void* b_up, const void* b_down,
+                  const void* ws_up, const void* ws_down, int T, int H, int E, int k, int F, int Fs,
+                  int act, int score, int groups, int topk_groups, int group_top, int renorm,
+                  float scale, int dtype, void* out, int32_t* topk_idx, float* topk_w, void* ws,
+                  size_t ws_bytes, void* stream);
+size_t moe_layer_few_workspace_bytes(int T, int H, int E, int k, int F, int Fs, int dtype);
 
 /* Static, human-readable text for a status code. */
 const char* moe_status_string(int status);

@@ -60,6 +60,9 @@ SIGNATURES = {
                                     _vp, _vp, _sz, _vp]),
     "moe_linear_grouped_fp8_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "moe_linear_fp8_path": (_i, [_i, _i, _i, _i, _i, _i, _vp]),
+    "moe_layer_few": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
+                           _i, _i, _i, _i, _i, _f, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_layer_few_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "moe_status_string": (ctypes.c_char_p, [_i]),
 }
 
@@ -1035,6 +1038,72 @@ def moe_linear_grouped_fp8(x, x_scale, offsets, w, w_scale, bias=None, act: str 
         xp, xsp, pp, k, T, fp, E, rows, wp, wsc, bp, code, rp, N, K, yp, wsp, wsn,
         _raw_stream(dev.index)))
     return y
+
+
+FEW_TOKENS = 64  # of moe_layer_few, at most
+BIAS_MODES = {"choice": 0, "score": 1}
+
+
+def moe_layer_few_workspace_bytes(T: int, H: int, E: int, k: int, F: int, Fs: int,
+                                  dtype_code: int) -> int:
+    _fits(T, H, E, k, F, Fs)
+    return lib().moe_layer_few_workspace_bytes(T, H, E, k, F, Fs, dtype_code)
+
+
+def moe_layer_few(x, wg, bias, w_up, w_down, k: int, score: str = "softmax",
+                  bias_mode: str = "choice", groups: int = 1, topk_groups: int = 1,
+                  group_top: int = 2, renorm: bool = True, scale: float = 1.0, act: str = "gelu",
+                  b_up=None, b_down=None, ws_up=None, ws_down=None, out=None, topk_idx=None,
+                  topk_w=None, ws=None, stream=None):
+    """The whole layer for a few tokens (x [T,H], T <= 64) in two launches: routing,
+    experts, shared expert and combine.
+
+    Routing as moe_route_grouped; bias (fp32 [E] or None) moves the choice only
+    (bias_mode "choice") or the scores themselves ("score", as moe_route). Experts as
+    moe_block_forward: w_up [E,F,H] or, for a gated act, [E,2,F,H]; w_down [E,H,F];
+    b_up [E,F] or [E,2,F], b_down [E,H]; ws_up, ws_down the same without E (the shared
+    expert, no biases). moe_layer_forward's layer is act "gelu", bias_mode "score" and the
+    other defaults. Returns (out [T,H], topk_idx int32 [T,k], topk_w fp32 [T,k])."""
+    T, H = _shape(x, "x", 2)
+    E = _shape(wg, "wg", 2)[0]
+    code = _enum(ACTS, act, "act")
+    two = (2,) if code >= 3 else ()
+    F = _shape(w_up, "w_up", 3 + len(two))[-2]
+    if (ws_up is None) != (ws_down is None):
+        raise ValueError("the shared expert needs ws_up and ws_down")
+    Fs = 0 if ws_up is None else _shape(ws_up, "ws_up", 2 + len(two))[-2]
+    _fits(T, H, E, k, F, Fs, groups, topk_groups, group_top)
+    dev, dtype = x.device, x.dtype
+    dt, sc, bm = _dtype_code(x), _enum(SCORES, score, "score"), _enum(BIAS_MODES, bias_mode, "bias_mode")
+    args = (_ptr(x, "x", (T, H), dtype, dev), _ptr(wg, "wg", (E, H), dtype, dev),
+            _ptr(bias, "bias", (E,), torch.float32, dev), bm,
+            _ptr(w_up, "w_up", (E, *two, F, H), dtype, dev),
+            _ptr(_given(w_down, "w_down"), "w_down", (E, H, F), dtype, dev),
+            _ptr(b_up, "b_up", (E, *two, F), dtype, dev), _ptr(b_down, "b_down", (E, H), dtype, dev),
+            _ptr(ws_up, "ws_up", (*two, Fs, H), dtype, dev), _ptr(ws_down, "ws_down", (H, Fs), dtype, dev),
+            T, H, E, k, F, Fs, code, sc, groups, topk_groups, group_top, int(renorm), scale, dt)
+    op = _ptr(out, "out", (T, H), dtype, dev)
+    ip = _ptr(topk_idx, "topk_idx", (T, k), torch.int32, dev)
+    wp = _ptr(topk_w, "topk_w", (T, k), torch.float32, dev)
+    other = _other_stream(dev, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return moe_layer_few(x, wg, bias, w_up, w_down, k, score, bias_mode, groups, topk_groups,
+                                 group_top, renorm, scale, act, b_up, b_down, ws_up, ws_down, out,
+                                 topk_idx, topk_w, ws)
+    L = lib()
+    wsp, wsn, ws = _ws(L.moe_layer_few_workspace_bytes(T, H, E, k, F, Fs, dt), dev, ws)
+    if out is None:
+        out = torch.empty((T, H), dtype=dtype, device=dev)
+        op = out.data_ptr()
+    if topk_idx is None:
+        topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        ip = topk_idx.data_ptr()
+    if topk_w is None:
+        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        wp = topk_w.data_ptr()
+    _check("moe_layer_few", L.moe_layer_few(*args, op, ip, wp, wsp, wsn, _raw_stream(dev.index)))
+    return out, topk_idx, topk_w
 
 
 def moe_block_forward(h, wg, w_up, w_down, k: int, x=None, norm_weight=None, norm_bias=None,

@@ -82,6 +82,27 @@ hipError_t launch_linear_fp8(const void* x, const float* x_scale, const int32_t*
                              const void* w, const float* w_scale, const void* bias, int act,
                              const void* res, void* y, void* ws, hipStream_t s);
 
+// Arguments of the few-token layer (moe_layer_few, after its checks).
+struct FewCall {
+  const void *x, *wg;
+  const float* bias;
+  bool bias_in_score;
+  const void *up, *down, *b_up, *b_down, *s_up, *s_down;
+  int T, H, E, k, F, Fs, act;
+  bool softmax;
+  int groups, topk_groups, group_top;
+  bool renorm;
+  float scale;
+  bool bf16;
+  void* out;
+  int32_t* idx;
+  float* w;
+  void* ws;
+};
+int few_max_tokens();
+size_t few_ws_bytes(int T, int H, int E, int k, int F, int Fs, bool bf16);
+hipError_t launch_few(const FewCall& c, hipStream_t s);
+
 hipError_t launch_bias_update(const int32_t* counts, int E, float gamma, float* bias,
                               float* load_frac, hipStream_t s);
 

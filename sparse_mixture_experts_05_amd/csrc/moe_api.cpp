@@ -521,4 +521,70 @@ int moe_linear_fp8_path(int E, int rows, int N, int K, int act, int grouped, int
   return path;
 }
 
+namespace {
+
+constexpr int kMaxFewSize = 1 << 20;
+
+int check_few(int T, int H, int E, int k, int F, int Fs, int dtype) {
+  if (T < 1 || F < 1 || Fs < 0 || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+  const int st = check_tokens(T, H, E, k);
+  if (st != MOE_OK) return st;
+  if (T > moe::few_max_tokens() || F % 64 != 0 || Fs % 64 != 0 || H > kMaxFewSize || F > kMaxFewSize ||
+      Fs > kMaxFewSize)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_layer_few_workspace_bytes(int T, int H, int E, int k, int F, int Fs, int dtype) {
+  if (check_few(T, H, E, k, F, Fs, dtype) != MOE_OK) return 0;
+  return moe::few_ws_bytes(T, H, E, k, F, Fs, dtype == MOE_BF16);
+}
+
+int moe_layer_few(const void* x, const void* wg, const float* bias, int bias_mode,
+                  const void* w_up, const void* w_down, const void* b_up, const void* b_down,
+                  const void* ws_up, const void* ws_down, int T, int H, int E, int k, int F, int Fs,
+                  int act, int score, int groups, int topk_groups, int group_top, int renorm,
+                  float scale, int dtype, void* out, int32_t* topk_idx, float* topk_w, void* ws,
+                  size_t ws_bytes, void* stream) {
+  if (!x || !wg || !w_up || !w_down || !out || !topk_idx || !topk_w) return MOE_ERR_INVALID_ARG;
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU ||
+      (bias_mode != MOE_BIAS_CHOICE && bias_mode != MOE_BIAS_SCORE))
+    return MOE_ERR_INVALID_ARG;
+  int st = check_few(T, H, E, k, F, Fs, dtype);
+  if (st != MOE_OK) return st;
+  st = check_grouped(T, E, k, score, groups, topk_groups, group_top, renorm, scale);
+  if (st != MOE_OK) return st;
+  if ((Fs > 0) != (ws_up != nullptr) || (Fs > 0) != (ws_down != nullptr)) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {x, wg, w_up, w_down, b_up, b_down, ws_up, ws_down, (const void*)out, (const void*)ws})
+    if (!aligned_or_null(p)) return MOE_ERR_INVALID_ARG;
+  const size_t b = elem(dtype), two = act == MOE_ACT_GEGLU || act == MOE_ACT_SWIGLU ? 2 : 1;
+  const size_t e = (size_t)E, t = (size_t)T;
+  const Span in[] = {{x, t * H * b}, {wg, e * H * b}, {bias, e * 4}, {w_up, e * two * F * H * b},
+                     {w_down, e * H * F * b}, {b_up, e * two * F * b}, {b_down, e * H * b},
+                     {ws_up, two * Fs * H * b}, {ws_down, (size_t)H * Fs * b}};
+  const Span outs[] = {{out, t * H * b}, {topk_idx, t * k * 4}, {topk_w, t * k * 4}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Span& s : in)
+      if (overlap(outs[i].p, outs[i].n, s.p, s.n)) return MOE_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return MOE_ERR_INVALID_ARG;
+  }
+  const size_t need = moe::few_ws_bytes(T, H, E, k, F, Fs, dtype == MOE_BF16);
+  if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  for (const Span& s : in)
+    if (overlap(ws, need, s.p, s.n)) return MOE_ERR_INVALID_ARG;
+  for (const Span& s : outs)
+    if (overlap(ws, need, s.p, s.n)) return MOE_ERR_INVALID_ARG;
+  moe::FewCall c{};
+  c.x = x, c.wg = wg, c.bias = bias, c.bias_in_score = bias_mode == MOE_BIAS_SCORE;
+  c.up = w_up, c.down = w_down, c.b_up = b_up, c.b_down = b_down, c.s_up = ws_up, c.s_down = ws_down;
+  c.T = T, c.H = H, c.E = E, c.k = k, c.F = F, c.Fs = Fs, c.act = act;
+  c.softmax = score == MOE_SCORE_SOFTMAX, c.groups = groups, c.topk_groups = topk_groups;
+  c.group_top = group_top, c.renorm = renorm != 0, c.scale = scale, c.bf16 = dtype == MOE_BF16;
+  c.out = out, c.idx = topk_idx, c.w = topk_w, c.ws = ws;
+  return from_hip(moe::launch_few(c, as_stream(stream)));
+}
+
 }  // extern "C"

@@ -1,0 +1,88 @@
+"""Refusals of moe_layer_few: host validation only, nothing is launched."""
+import ctypes
+
+import pytest
+import torch
+
+import sparse_mixture_experts_05_amd as moe
+
+P = [ctypes.c_void_p(0x10000000 * (i + 1)) for i in range(16)]  # far apart, never dereferenced
+ODD = ctypes.c_void_p(0x10000008)
+T, H, E, K, F, FS = 4, 128, 16, 2, 192, 64
+
+
+def at(p, n):
+    return ctypes.c_void_p(p.value + n)
+
+
+def few(x=P[0], wg=P[1], bias=P[2], mode=0, up=P[3], down=P[4], bu=P[5], bd=P[6], su=P[7], sd=P[8], T=T, H=H,
+        E=E, k=K, F=F, Fs=FS, act=4, score=1, groups=4, tg=2, gt=2, rn=1, scale=1.0, dt=1, out=P[9], idx=P[10],
+        w=P[11], ws=P[12], n=1 << 24):
+    return moe.lib().moe_layer_few(x, wg, bias, mode, up, down, bu, bd, su, sd, T, H, E, k, F, Fs, act, score,
+                                   groups, tg, gt, rn, scale, dt, out, idx, w, ws, n, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    *[({n: None}, -1) for n in ("x", "wg", "up", "down", "out", "idx", "w", "su", "sd")], (dict(ws=None), -3),
+    *[({n: ODD}, -1) for n in ("x", "wg", "up", "down", "bu", "bd", "su", "sd", "out", "ws")],
+    (dict(mode=2), -1), (dict(act=5), -1), (dict(act=-1), -1), (dict(score=2), -1), (dict(dt=2), -1),
+    (dict(T=0), -1), (dict(H=0), -1), (dict(E=0), -1), (dict(k=0), -1), (dict(F=0), -1), (dict(Fs=-64), -1),
+    (dict(Fs=0), -1), (dict(rn=2), -1), (dict(gt=3), -1), (dict(scale=float("nan")), -1),
+    (dict(T=65), -2), (dict(H=100), -2), (dict(F=100), -2), (dict(Fs=32), -2), (dict(E=257), -2),
+    (dict(k=9), -2), (dict(groups=5), -2), (dict(tg=5), -2), (dict(tg=1, k=5), -2), (dict(H=(1 << 20) + 64), -2),
+    (dict(F=(1 << 20) + 64), -2), (dict(n=1024), -3),
+    (dict(out=P[0]), -1), (dict(out=at(P[0], T * H * 2 - 16)), -1), (dict(out=at(P[1], 16)), -1),
+    (dict(out=at(P[3], E * 2 * F * H * 2 - 16)), -1), (dict(out=at(P[4], E * H * F * 2 - 16)), -1),
+    (dict(out=at(P[5], E * 2 * F * 2 - 16)), -1), (dict(out=at(P[6], E * H * 2 - 16)), -1),
+    (dict(out=at(P[7], 2 * FS * H * 2 - 16)), -1), (dict(out=at(P[8], H * FS * 2 - 16)), -1),
+    (dict(idx=at(P[9], T * H * 2 - 4)), -1), (dict(w=at(P[10], 4)), -1), (dict(w=at(P[2], 4)), -1),
+    (dict(ws=P[9]), -1), (dict(ws=P[10]), -1), (dict(ws=P[11]), -1), (dict(ws=P[4]), -1), (dict(ws=P[2]), -1),
+])
+def test_refusals(kw, status):
+    assert few(**kw) == status
+
+
+def test_workspace():
+    q = moe.lib().moe_layer_few_workspace_bytes
+    need = q(T, H, E, K, F, FS, 1)
+    assert need > 0 and few(n=need - 1) == -3
+    assert few(ws=at(P[0], 16 - need)) == -1
+    for bad in ((65, H, E, K, F, FS, 1), (T, 96, E, K, F, FS, 1), (T, H, 257, K, F, FS, 1), (T, H, E, 9, F, FS, 1),
+                (T, H, E, K, 0, FS, 1), (T, H, E, K, F, 32, 1), (T, H, E, K, F, FS, 2)):
+        assert q(*bad) == 0
+
+
+def t(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype)
+
+
+X, WG, UP, DOWN = t(2, 64), t(8, 64), t(8, 128, 64), t(8, 64, 128)
+BAD = [
+    ("x must have 2 dimensions", lambda: moe.moe_layer_few(t(64), WG, None, UP, DOWN, 2)),
+    ("unsupported dtype", lambda: moe.moe_layer_few(t(2, 64, dtype=torch.float16), WG, None, UP, DOWN, 2)),
+    ("wg has shape", lambda: moe.moe_layer_few(X, t(8, 128), None, UP, DOWN, 2)),
+    ("bias must be torch.float32", lambda: moe.moe_layer_few(X, WG, t(8), UP, DOWN, 2)),
+    ("w_up must have 4 dimensions", lambda: moe.moe_layer_few(X, WG, None, UP, DOWN, 2, act="swiglu")),
+    ("w_up must be torch.bfloat16", lambda: moe.moe_layer_few(X, WG, None, UP.float(), DOWN, 2)),
+    ("w_down has shape", lambda: moe.moe_layer_few(X, WG, None, UP, t(8, 128, 64), 2)),
+    ("w_down is required", lambda: moe.moe_layer_few(X, WG, None, UP, None, 2)),
+    ("b_up has shape", lambda: moe.moe_layer_few(X, WG, None, UP, DOWN, 2, b_up=t(8, 64))),
+    ("b_down has shape", lambda: moe.moe_layer_few(X, WG, None, UP, DOWN, 2, b_down=t(8, 128))),
+    ("needs ws_up and ws_down", lambda: moe.moe_layer_few(X, WG, None, UP, DOWN, 2, ws_up=t(64, 64))),
+    ("ws_down has shape", lambda: moe.moe_layer_few(X, WG, None, UP, DOWN, 2, ws_up=t(64, 64), ws_down=t(64, 128))),
+    ("act must be one of", lambda: moe.moe_layer_few(X, WG, None, UP, DOWN, 2, act="tanh")),
+    ("score must be one of", lambda: moe.moe_layer_few(X, WG, None, UP, DOWN, 2, score="x")),
+    ("bias_mode must be one of", lambda: moe.moe_layer_few(X, WG, None, UP, DOWN, 2, bias_mode="x")),
+    ("out has shape", lambda: moe.moe_layer_few(X, WG, None, UP, DOWN, 2, out=t(3, 64))),
+    ("topk_idx has shape", lambda: moe.moe_layer_few(X, WG, None, UP, DOWN, 2, topk_idx=t(2, 3, dtype=torch.int32))),
+    ("topk_w must be torch.float32", lambda: moe.moe_layer_few(X, WG, None, UP, DOWN, 2, topk_w=t(2, 2))),
+    ("must be contiguous", lambda: moe.moe_layer_few(t(64, 2).t(), WG, None, UP, DOWN, 2)),
+    ("must be GPU tensors", lambda: moe.moe_layer_few(X, WG, None, UP, DOWN, 2)),
+]
+
+
+@pytest.mark.parametrize("i", range(len(BAD)))
+def test_binding_refuses(i):
+    text, call = BAD[i]
+    with pytest.raises(ValueError, match=text):
+        call()

@@ -6,18 +6,22 @@
 //   h[t,j]  = act(x[t] . up[e_j]^T + b_up[e_j])           rounded to the layer's type
 //   out[t]  = sum_j w[t,j] (h[t,j] . down[e_j]^T + b_down[e_j])  + shared expert(x[t])
 //
-// The second launch is one queue of tasks, taken by ticket in this order:
-//   up tasks    (expert, 32 weight rows of up: 32 columns of h, or 16 of a gated act)
-//   down tasks  (K slice, 32 columns of out), over all chosen experts of the slice
-// A down task waits until the up tasks of its experts are done. It waits only for lower
-// tickets, and whoever holds a lower ticket is running and waits for nothing (an up task)
-// or for lower tickets still: the queue empties whatever number of workgroups is resident
-// and whatever else the GPU runs. (The wait ends after a second in any case: a workspace
-// that another call is using gives wrong results, no hang.)
+// The second launch chooses (every workgroup for itself: cheaper than handing it round) and
+// then has two kinds of tasks:
+//   up    (unit, 16 weight rows of up: 16 columns of h, or 8 of a gated act), by ticket
+//   down  (K slice, 16 columns of out) over all units, dealt out by workgroup
+// A down task waits until every up task is done. A workgroup starts on its down tasks only
+// when it has drawn a ticket past the last up task, so by then every up task is held by a
+// workgroup that runs, and that waits for nothing before it is through with its tickets:
+// the wait ends whatever number of workgroups is resident and whatever else the GPU runs.
+// (It ends after a second in any case: in a workspace that another call is using results
+// are wrong, and nothing hangs.)
 //
-// MFMA columns are tokens, in order: an expert's product is made for all of them and kept
-// for those that chose it, so nothing is sorted or gathered, and a token's sum stays in
-// one lane. Weights go straight to registers (nothing else on the chip reads them).
+// The pairs (token, chosen expert) are sorted by expert in every workgroup's LDS; up to 16
+// pairs of an expert make a unit, the columns of one MFMA tile, and the shared expert has
+// units of 16 tokens. Weights go straight to registers (nothing else on the chip reads
+// them); the first steps of a task are loaded while the task before it is summed up and
+// stored, those of the down weights while the last up tasks are waited for.
 #include <algorithm>
 
 #include "kernels.hpp"
@@ -29,54 +33,52 @@ namespace {
 
 using namespace lin;
 
-constexpr int kWaves = 8, kFewThreads = kWaves * 64;
-constexpr int kFewT = 64, kSlots = 8;     // tokens, experts of a token
-constexpr int kCols = 32;                 // weight rows of a task: two MFMA row tiles
+constexpr int kWaves = 8;                 // streaming waves of a workgroup
+constexpr int kFewT = 64, kPairs = kFewT * 8;  // tokens; pairs of a token and its expert
+constexpr int kUnits = kMaxE + kPairs / 16 + kFewT / 16;  // at most
+constexpr int kCols = 16;                 // weight rows of a task
 constexpr int kMaxDown = 8;               // K slices of the down tasks
-constexpr int kBT = 16;                   // tokens of a pass of the choice
+constexpr int kMaxScore = 8;              // K slices of the scores
 
 struct FewArgs {
   const void *x, *up, *down, *b_up, *b_down, *s_up, *s_down;
   const float* bias;  // inside the scores, or null
   GroupArgs g;
   int T, H, E, k, F, Fs, act;
-  float* scores;       // [T, E]
-  void* h;             // [T * k, F], then [T, Fs]
-  float* part;         // [H / 32, D, 2, column tiles, 64, 4]: partial columns of out
-  unsigned* counters;  // ticket | done [E + 1] | arrived [H / 32, column tiles]
-  int D;
+  float* scores;       // [KS, T, E]
+  void* h;             // [T * k, F] in the order of the experts, then [T, Fs]
+  float* part;         // [H / 16, D, T, 16]: partial columns of out
+  unsigned* counters;  // tickets | up tasks done | arrived [H / 16]
+  int KS, D;
   int32_t* idx;
   float* w;
   void* out;
 };
 
-__host__ __device__ inline int counter_ints(int E, int H, int nt) { return 1 + E + 1 + H / kCols * nt; }
+constexpr int kLine = 32;  // ints of a cache line: tickets and done have one each
+inline int counter_ints(int H) { return 2 * kLine + H / kCols; }
 
 // ----------------------------------------------------------------- scores
 
-// 16 experts x 16 tokens a workgroup of 16 waves, which share H (64 bytes of a row a step)
-// and add their sums in wave order. Clears the second launch's counters.
-constexpr int kScoreWaves = 16;
-
+// 16 experts x 16 tokens x a slice of H a workgroup of 4 waves, which share the slice (64
+// bytes of a row a step) and add their sums in wave order. Clears the counters of the
+// second launch. The slices spread Wg over the CUs: one CU reads about 55 GB/s.
 template <typename T>
-__global__ __launch_bounds__(kScoreWaves * 64) void few_scores_kernel(const T* __restrict__ x,
-                                                                     const T* __restrict__ wg, int nT,
-                                                                     int H, int E, float* __restrict__ scores,
-                                                                     unsigned* __restrict__ counters,
-                                                                     int ncount) {
-  constexpr int U = 8;
-  __shared__ f32x4_t red[kScoreWaves][64];
+__global__ __launch_bounds__(256) void few_scores_kernel(const T* __restrict__ x, const T* __restrict__ wg,
+                                                        int nT, int H, int E, float* __restrict__ scores,
+                                                        unsigned* __restrict__ counters, int ncount) {
+  constexpr int U = 4, NW = 4;
+  __shared__ f32x4_t red[NW][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int id = blockIdx.y * gridDim.x + blockIdx.x;
-  for (int i = id * (kScoreWaves * 64) + threadIdx.x; i < ncount; i += gridDim.x * gridDim.y * kScoreWaves * 64)
-    counters[i] = 0;
+  const int id = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+  for (int i = id * 256 + threadIdx.x; i < ncount; i += gridDim.x * gridDim.y * gridDim.z * 256) counters[i] = 0;
   const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
   const uint8_t* a = reinterpret_cast<const uint8_t*>(wg + (size_t)min(e0 + (lane & 15), E - 1) * H) + (lane >> 4) * 16;
   const uint8_t* b = reinterpret_cast<const uint8_t*>(x + (size_t)min(t0 + (lane & 15), nT - 1) * H) + (lane >> 4) * 16;
-  const int S = H * (int)sizeof(T) / 64;
-  const int s1 = (wave + 1) * S / kScoreWaves;
+  const int S = H * (int)sizeof(T) / 64, parts = gridDim.z * NW, part = blockIdx.z * NW + wave;
+  const int s1 = (int)((long long)(part + 1) * S / parts);
   f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  int s = wave * S / kScoreWaves;
+  int s = (int)((long long)part * S / parts);
   for (; s + U <= s1; s += U) {
     u32x4_t av[U], bv[U];
 #pragma unroll
@@ -89,69 +91,44 @@ __global__ __launch_bounds__(kScoreWaves * 64) void few_scores_kernel(const T* _
   __syncthreads();
   if (wave != 0) return;
 #pragma unroll
-  for (int q = 1; q < kScoreWaves; ++q) acc += red[q][lane];
+  for (int q = 1; q < NW; ++q) acc += red[q][lane];
   const int t = t0 + (lane & 15);
   if (t >= nT) return;
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const int e = e0 + (lane >> 4) * 4 + v;
-    if (e < E) scores[(size_t)t * E + e] = acc[v];
+    if (e < E) scores[((size_t)blockIdx.z * nT + t) * E + e] = acc[v];
   }
 }
 
-// ----------------------------------------------------------------- the queue
+// ----------------------------------------------------------------- handing over
 
-// acc[r][c] += rows of w[r] . rows of col[c] over the steps [s0, s1) of 64 bytes. The
-// pointers are the lane's: row lane % 16 of its tile, 16 bytes at lane / 16. U steps are
-// in flight while U are multiplied.
-template <typename T, int NT, int U>
-__device__ __forceinline__ void stream(const uint8_t* const (&w)[2], const uint8_t* const (&col)[NT],
-                                       int s0, int s1, f32x4_t (&acc)[2][NT]) {
-  u32x4_t wa[U][2], ca[U][NT], wb[U][2], cb[U][NT];
-  auto load = [&](u32x4_t (&wv)[U][2], u32x4_t (&cv)[U][NT], int s) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) wv[u][r] = ld16(w[r] + (size_t)(s + u) * 64);
-#pragma unroll
-      for (int c = 0; c < NT; ++c) cv[u][c] = ld16(col[c] + (size_t)(s + u) * 64);
-    }
-  };
-  auto mma = [&](const u32x4_t (&wv)[U][2], const u32x4_t (&cv)[U][NT]) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int c = 0; c < NT; ++c) acc[r][c] = mma16<T>(wv[u][r], cv[u][c], acc[r][c]);
-  };
-  int s = s0;
-  if (s + U <= s1) {
-    load(wa, ca, s);
-    for (;;) {
-      s += U;
-      const bool more = s + U <= s1;
-      if (more) load(wb, cb, s);
-      mma(wa, ca);
-      if (!more) break;
-      s += U;
-      const bool again = s + U <= s1;
-      if (again) load(wa, ca, s);
-      mma(wb, cb);
-      if (!again) break;
-    }
-  }
-  for (; s < s1; ++s) {
-    u32x4_t cv[NT];
-#pragma unroll
-    for (int c = 0; c < NT; ++c) cv[c] = ld16(col[c] + (size_t)s * 64);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const u32x4_t wv = ld16(w[r] + (size_t)s * 64);
-#pragma unroll
-      for (int c = 0; c < NT; ++c) acc[r][c] = mma16<T>(wv, cv[c], acc[r][c]);
-    }
-  }
+// What workgroups hand to each other within the launch (h and the partial columns of out)
+// goes past the caches that they do not share: stores at agent scope, which are complete
+// at memory once vmcnt says so, and 16-byte loads with sc1, the same scope. Fences would do
+// as well and write back and invalidate a whole XCD's L2 each (1 token of 128 experts
+// 173 us, 113 this way).
+__device__ __forceinline__ void put8(void* p, uint2 v) {
+  __hip_atomic_store(static_cast<uint64_t*>(p), (uint64_t)v.y << 32 | v.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void put16(void* p, const f32x4_t& v) {
+  put8(p, make_uint2(__float_as_uint(v[0]), __float_as_uint(v[1])));
+  put8(static_cast<uint8_t*>(p) + 8, make_uint2(__float_as_uint(v[2]), __float_as_uint(v[3])));
+}
+typedef __amdgpu_buffer_rsrc_t Shared;  // a buffer and its bytes: loads past it give zeros
+__device__ __forceinline__ Shared shared_buffer(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
+}
+__device__ __forceinline__ u32x4_t get16(Shared b, uint32_t at, uint32_t uniform) {
+  return __builtin_amdgcn_raw_buffer_load_b128(b, at, uniform, 16);  // sc1
+}
+
+// Everything that this wave stored is at memory; then *p counts one more.
+__device__ __forceinline__ unsigned announce(unsigned* p) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  unsigned before = 0;
+  if ((threadIdx.x & 63) == 0) before = __hip_atomic_fetch_add(p, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return __builtin_amdgcn_readfirstlane(before);
 }
 
 // Waits until *p has reached n, a second at most (100 ticks of this clock a microsecond).
@@ -161,298 +138,443 @@ __device__ __forceinline__ void wait_count(const unsigned* p, unsigned n) {
     __builtin_amdgcn_s_sleep(2);
     if (wall_clock64() - start > 100000000ull) break;
   }
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
 }
 
-template <typename T, int NT, int EPX>
-struct FewLds {
-  static constexpr int S = tile_stride<kBT, kWaves>();
-  union {
-    struct {
-      float sc[kBT * S];
-      GroupLds<kBT, kWaves> g;
-    } choice;
-    f32x4_t red[kWaves][2][NT][64];
-  };
-  int idx[NT * 16][kSlots];  // -1 past k
-  float w[NT * 16][kSlots];
-  int mark[kMaxE];           // a pair of the expert, or -1
-  int segs[kMaxE];           // the chosen experts, ascending
-  int nseg, ticket;
+// ----------------------------------------------------------------- the stream
+
+// 16 rows of weights: their uniform base at the wave's first step, and the lane's offset
+// (row lane % 16, 16 bytes at lane / 16).
+struct Rows {
+  const uint8_t* w;
+  uint32_t lane;
+  int steps;  // of 64 bytes a row
 };
 
-// The pair (token, slot) of expert e among token t's, or -1; its weight in wt.
-__device__ __forceinline__ int pair_of(const int (&idx)[kSlots], const float (&w)[kSlots], int t, int e,
-                                       int k, float& wt) {
-  int p = -1;
-  wt = 0.0f;
+// R steps of the weights and of the columns, in flight or landed.
+template <int R>
+struct Ring {
+  u32x4_t w[R], c[R];
+};
+
+// The first steps of a stream. Steps past its end repeat the last one (and a stream
+// without steps reads the row's start), which nobody multiplies.
+template <int R, typename Col>
+__device__ __forceinline__ void first_steps(Ring<R>& g, const Rows& w, Col col) {
 #pragma unroll
-  for (int j = 0; j < kSlots; ++j)
-    if (idx[j] == e) p = t * k + j, wt = w[j];
-  return p;
+  for (int u = 0; u < R; ++u) {  // in the order of their use
+    const int s = min(u, max(w.steps - 1, 0));
+    g.w[u] = ld16(w.w + (size_t)s * 64 + w.lane);
+    g.c[u] = col(s);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+template <int R>
+__device__ __forceinline__ void first_rows(Ring<R>& g, const Rows& w) {
+#pragma unroll
+  for (int u = 0; u < R; ++u) g.w[u] = ld16(w.w + (size_t)min(u, max(w.steps - 1, 0)) * 64 + w.lane);
+}
+template <int R, typename Col>
+__device__ __forceinline__ void first_cols(Ring<R>& g, int steps, Col col) {
+#pragma unroll
+  for (int u = 0; u < R; ++u) g.c[u] = col(min(u, max(steps - 1, 0)));
 }
 
-template <typename T, int NT, int EPX>
-__global__ __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) void few_kernel(FewArgs a) {
-  constexpr int U = NT == 4 ? 1 : 2;
-  constexpr int ES = (int)sizeof(T);
-  __shared__ FewLds<T, NT, EPX> L;
+// Rows of w . columns over w's steps, the first R of which are in the ring. A step's place
+// is refilled with the step R further on, or from there on with the first steps of the next
+// stream, so that R steps are in flight at any time: the barrier between two tasks does not
+// drain them. col(s, next): step s of the columns of this stream, or of the next one.
+template <typename T, int R, typename Col>
+__device__ __forceinline__ f32x4_t stream(Ring<R>& g, const Rows& w, const Rows& next, Col col) {
+  const int S = w.steps, last = max(next.steps - 1, 0);
+  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  int b = 0;
+  do {  // one round at least, which fetches the next stream's
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+      const bool live = b + u < S;  // a last, partial round multiplies zeros
+      const u32x4_t zero = {0, 0, 0, 0};
+      acc = mma16<T>(live ? g.w[u] : zero, live ? g.c[u] : zero, acc);
+      const bool more = b + u + R < S;
+      const int s = more ? b + u + R : min(u, last);
+      const uint8_t* base = (more ? w.w : next.w) + (size_t)s * 64;
+      g.w[u] = ld16(base + (more ? w.lane : next.lane));
+      g.c[u] = col(s, !more);
+      __builtin_amdgcn_sched_barrier(0);  // loads stay in the order of their use
+    }
+    b += R;
+  } while (b < S);
+  return acc;
+}
+
+// ----------------------------------------------------------------- the queue
+
+struct FewLds {
+  static constexpr int S = tile_stride<kWaves, kWaves>();
+  union {
+    struct {
+      float sc[kWaves * S];
+      GroupLds<kWaves, kWaves> g;
+      int idx[kPairs];
+      float w[kPairs];
+      int count[kWaves][kMaxE];  // pairs of each expert by wave; then [0]: its first place
+    } choice;
+    f32x4_t red[2][kWaves][64];               // up: the waves' sums of two tasks in turn
+    float out[2][kWaves][kFewT][kCols];       // down: each wave's part of the columns of out
+  };
+  int tok[kPairs];     // by place in the experts' order: the pair's token
+  float w[kPairs];     // and weight
+  // a unit: its expert (-1: the shared one), first place (the shared one's: token) and pairs
+  int expert[kUnits], first[kUnits], pairs[kUnits];
+  int units, start[2], ticket[2];  // a workgroup's first two tickets, then every next one in turn
+};
+
+// The choice of every token; the pairs in the experts' order, and the units: the shared
+// expert's, then each expert's. One wave a token, for itself, then one thread a pair.
+template <int EPX>
+__device__ __forceinline__ void choose(const FewArgs& a, FewLds& L) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const bool gt = gated(a.act);
-
-  // the choice, in every workgroup: it costs less than handing it round
-  for (int i = tid; i < kMaxE; i += kFewThreads) L.mark[i] = -1;
-  for (int i = tid; i < NT * 16 * kSlots; i += kFewThreads) {
-    L.idx[i / kSlots][i % kSlots] = -1;
-    L.w[i / kSlots][i % kSlots] = 0.0f;
-  }
-  for (int t0 = 0; t0 < a.T; t0 += kBT) {
-    __syncthreads();
-    for (int i = tid; i < kBT * EPX; i += kFewThreads) {
-      const int e = min(i % EPX, a.E - 1);
-      const float s = a.scores[(size_t)min(t0 + i / EPX, a.T - 1) * a.E + e];
-      L.choice.sc[i / EPX * L.S + i % EPX] = a.bias != nullptr ? s + a.bias[e] : s;
+  for (int t = wave; t < a.T && wave < kWaves; t += kWaves) {
+    float* row = L.choice.sc + wave * L.S;
+#pragma unroll
+    for (int i = 0; i < EPX / 64; ++i) {
+      const int e = min(i * 64 + lane, a.E - 1);
+      float v[kMaxScore];
+#pragma unroll
+      for (int q = 0; q < kMaxScore; ++q) v[q] = a.scores[((size_t)min(q, a.KS - 1) * a.T + t) * a.E + e];
+      float s = v[0];
+#pragma unroll
+      for (int q = 1; q < kMaxScore; ++q)
+        if (q < a.KS) s += v[q];
+      row[i * 64 + lane] = a.bias != nullptr ? s + a.bias[e] : s;
     }
-    __syncthreads();
-    // rows of k: spread to rows of kSlots below
-    int32_t* idx = &L.idx[0][0] + t0 * a.k;
-    float* w = &L.w[0][0] + t0 * a.k;
-    grouped_phase<kBT, EPX, kWaves>(L.choice.sc, L.choice.g, a.g, 0, min(kBT, a.T - t0), a.E, a.k, idx, w);
+    wave_lds_fence();
+    grouped_phase<kWaves, EPX, kWaves>(L.choice.sc, L.choice.g, a.g, t - wave, a.T, a.E, a.k, L.choice.idx,
+                                       L.choice.w);
+    wave_lds_fence();
   }
-  __syncthreads();
-  int pi = -1;
-  float pw = 0.0f;
-  static_assert(NT * 16 * kSlots <= kFewThreads, "one thread a slot");
-  if (tid < NT * 16 * kSlots && tid / kSlots < a.T && tid % kSlots < a.k) {
-    pi = (&L.idx[0][0])[tid / kSlots * a.k + tid % kSlots];
-    pw = (&L.w[0][0])[tid / kSlots * a.k + tid % kSlots];
-    if (blockIdx.x == 0) {
-      a.idx[tid / kSlots * a.k + tid % kSlots] = pi;
-      a.w[tid / kSlots * a.k + tid % kSlots] = pw;
+  for (int i = tid; i < kWaves * kMaxE; i += kWaves * 64) (&L.choice.count[0][0])[i] = 0;
+  lds_barrier();
+  // Places have to be the same in every workgroup: pairs of an expert keep their order.
+  // Pairs of this wave with the lane's expert: by the 8 bits of its number.
+  const bool pair = tid < a.T * a.k;  // the streams' threads
+  static_assert(kPairs <= kWaves * 64 && kMaxE <= 256, "one thread a pair");
+  int e = 0, rank = 0;
+  float w = 0.0f;
+  if (pair) {
+    e = L.choice.idx[tid];
+    w = L.choice.w[tid];
+    if (blockIdx.x == 0) a.idx[tid] = e, a.w[tid] = w;
+    unsigned long long same = __ballot(true);
+#pragma unroll
+    for (int bit = 0; bit < 8; ++bit) {
+      const unsigned long long on = __ballot((e >> bit) & 1);
+      same &= (e >> bit) & 1 ? on : ~on;
     }
+    rank = __popcll(same & ((1ull << lane) - 1));
+    if (rank == 0) L.choice.count[wave][e] = __popcll(same);
   }
-  __syncthreads();
-  if (tid < NT * 16 * kSlots) {
-    L.idx[tid / kSlots][tid % kSlots] = pi;
-    L.w[tid / kSlots][tid % kSlots] = pw;
-    if (pi >= 0) atomicMax(&L.mark[pi], tid / kSlots * a.k + tid % kSlots);
-  }
-  __syncthreads();
+  lds_barrier();
+  if (pair)
+    for (int q = 0; q < wave; ++q) rank += L.choice.count[q][e];
+  lds_barrier();
   if (wave == 0) {
-    int n = 0;
-    for (int e0 = 0; e0 < kMaxE; e0 += 64) {
-      const bool in = L.mark[e0 + lane] >= 0;
-      const unsigned long long m = __ballot(in);
-      if (in) L.segs[n + __popcll(m & ((1ull << lane) - 1))] = e0 + lane;
-      n += __popcll(m);
+    // places and units before each of this lane's 4 experts
+    int c[4], places = 0, units = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = 0;
+#pragma unroll
+      for (int q = 0; q < kWaves; ++q) c[i] += L.choice.count[q][lane * 4 + i];
+      places += c[i];
+      units += (c[i] + 15) / 16;
     }
-    if (lane == 0) L.nseg = n;
+    int p = places, u = units;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int vp = __shfl_up(p, d), vu = __shfl_up(u, d);
+      if (lane >= d) p += vp, u += vu;
+    }
+    const int su = a.Fs > 0 ? (a.T + 15) / 16 : 0;
+    if (lane == 63) L.units = su + u;
+    p -= places;
+    u += su - units;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      L.choice.count[0][lane * 4 + i] = p;
+      for (int q = 0; q < c[i]; q += 16, ++u) {
+        L.expert[u] = lane * 4 + i;
+        L.first[u] = p + q;
+        L.pairs[u] = min(16, c[i] - q);
+      }
+      p += c[i];
+    }
+    if (lane < su) {
+      L.expert[lane] = -1;
+      L.first[lane] = lane * 16;
+      L.pairs[lane] = min(16, a.T - lane * 16);
+    }
   }
-  __syncthreads();
-  const int nseg = L.nseg;
+  lds_barrier();
+  if (pair) {
+    const int at = L.choice.count[0][e] + rank;
+    L.tok[at] = tid / a.k;
+    L.w[at] = w;
+  }
+  lds_barrier();
+}
 
-  const int H = a.H, F = a.F, Fs = a.Fs;
-  const int chunk = gt ? kCols / 2 : kCols;  // columns of h of an up task
+template <typename T>
+__device__ __forceinline__ void store4(T* row, const f32x4_t& v) {
+  if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<uint2*>(row) = make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
+  else
+    *reinterpret_cast<f32x4_t*>(row) = v;
+}
+
+// kWaves waves stream weights; one more sums up what those made of a task, finishes it and
+// draws the tickets while the streams go on with the next task.
+template <typename T, int EPX>
+__global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
+  constexpr int R = 8;
+  constexpr int ES = (int)sizeof(T);
+  __shared__ FewLds L;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  auto draw = [&] { return (int)__hip_atomic_fetch_add(a.counters, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+  const bool drawer = tid == kWaves * 64;
+  if (drawer) L.start[0] = draw();
+  choose<EPX>(a, L);
+  // the second ticket only now: every workgroup has its first
+  if (drawer) L.start[1] = draw();
+  lds_barrier();
+  auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  const bool gt = gated(a.act);
+  const int H = a.H, F = a.F, Fs = a.Fs, units = uni(L.units);
+  const int su = Fs > 0 ? (a.T + 15) / 16 : 0;  // the shared expert's units
+  const int chunk = gt ? kCols / 2 : kCols;     // columns of h of an up task
   const int CS = Fs / chunk, CF = F / chunk;
-  const int nup = CS + nseg * CF, ntile = H / kCols;
-  const int total = nup + ntile * a.D;
-  const int two = gt ? 2 : 1;
+  const int nup = su * CS + (units - su) * CF, ntile = H / kCols, ndown = ntile * a.D;
   T* h = static_cast<T*>(a.h);
-  T* hs = h + (size_t)a.T * a.k * F;
-  unsigned* done = a.counters + 1;  // [0]: shared expert, [1 + e]
-  unsigned* arrived = done + a.E + 1;
+  const size_t shared_at = (size_t)a.T * a.k * F;  // the shared expert's rows (elements)
+  unsigned* done = a.counters + kLine;
   const int l16 = lane & 15, kq = lane >> 4;
-  int tok[NT];  // the lane's token of each column tile
-#pragma unroll
-  for (int c = 0; c < NT; ++c) tok[c] = min(c * 16 + l16, a.T - 1);
+  struct Task {
+    int unit, f0;  // first column of h
+  };
+  auto up_task = [&](int t) {
+    const int r = t - su * CS;
+    return r < 0 ? Task{t / CS, t % CS * chunk} : Task{su + r / CF, r % CF * chunk};
+  };
+  int t0 = uni(L.start[0]), t1 = uni(L.start[1]);
+  int task = blockIdx.x;
 
-  for (;;) {
-    if (tid == 0) L.ticket = (int)__hip_atomic_fetch_add(a.counters, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    const int task = __builtin_amdgcn_readfirstlane(L.ticket);
-    if (task >= total) return;
-    f32x4_t acc[2][NT];
+  if (wave == kWaves) {
+    int turn = 0;
+    while (t0 < nup) {
+      if (drawer) L.ticket[turn] = draw();
+      lds_barrier();
+      // sums in wave order; with a gate, the up half is in the lanes 32 further on
+      f32x4_t v = L.red[turn][0][lane], u = L.red[turn][0][lane ^ 32];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int c = 0; c < NT; ++c) acc[r][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-
-    if (task < nup) {
-      const bool sh = task < CS;
-      const int e = sh ? -1 : L.segs[(task - CS) / CF];
-      const int f0 = (sh ? task : (task - CS) % CF) * chunk, N = sh ? Fs : F;
-      const uint8_t* base = static_cast<const uint8_t*>(sh ? a.s_up : a.up) +
-                            (sh ? 0 : (size_t)e * two * F * H * ES) + kq * 16;
-      const uint8_t* wp[2] = {base + (size_t)(f0 + l16) * H * ES,
-                              base + ((size_t)(gt ? N : 16) + f0 + l16) * H * ES};
-      const uint8_t* cp[NT];
-#pragma unroll
-      for (int c = 0; c < NT; ++c) cp[c] = static_cast<const uint8_t*>(a.x) + (size_t)tok[c] * H * ES + kq * 16;
-      const int S = H * ES / 64;
-      stream<T, NT, U>(wp, cp, wave * S / kWaves, (wave + 1) * S / kWaves, acc);
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int c = 0; c < NT; ++c) L.red[wave][r][c][lane] = acc[r][c];
-      __syncthreads();
-      if (wave < NT) {
-        // column tile `wave`
-        f32x4_t v[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          v[r] = L.red[0][r][wave][lane];
-#pragma unroll
-          for (int q = 1; q < kWaves; ++q) v[r] += L.red[q][r][wave][lane];
+      for (int q = 1; q < kWaves; ++q) v += L.red[turn][q][lane], u += L.red[turn][q][lane ^ 32];
+      const Task k = up_task(t0);
+      const int e = uni(L.expert[k.unit]);
+      if (l16 < L.pairs[k.unit] && (!gt || kq < 2)) {
+        const size_t r = L.first[k.unit] + l16;
+        T* row = (e < 0 ? h + shared_at + r * Fs : h + r * F) + k.f0 + kq * 4;
+        Out4 bg{}, bu{}, none{};
+        if (e >= 0 && a.b_up != nullptr) {
+          const T* b = static_cast<const T*>(a.b_up) + (size_t)e * (gt ? 2 : 1) * F + k.f0 + kq * 4;
+          bg = load4(b);
+          if (gt) bu = load4(b + F);
         }
-        const int t = wave * 16 + l16;
-        float wt;
-        const int p = t < a.T ? (sh ? t : pair_of(L.idx[t], L.w[t], t, e, a.k, wt)) : -1;
-        if (p >= 0) {
-          T* row = (sh ? hs + (size_t)p * Fs : h + (size_t)p * F) + f0 + kq * 4;
-          const T* b = sh || a.b_up == nullptr ? nullptr
-                                               : static_cast<const T*>(a.b_up) + (size_t)e * two * F + f0 + kq * 4;
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            if (gt && r == 1) continue;
-            Out4 bg{}, bu{}, none{};
-            if (b != nullptr) {
-              bg = load4(b + r * 16);
-              if (gt) bu = load4(b + F);
-            }
-            const Out4 o = finish4<ES == 2>(a.act, v[r], v[1], bg, bu, false, none);
-            if constexpr (ES == 2) *reinterpret_cast<uint2*>(row + r * 16) = pack4(o);
-            else *reinterpret_cast<f32x4_t*>(row + r * 16) = f32x4_t{o.v[0], o.v[1], o.v[2], o.v[3]};
-          }
-        }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-        if (lane == 0)
-          __hip_atomic_fetch_add(done + 1 + e, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const Out4 o = finish4<ES == 2>(a.act, v, u, bg, bu, false, none);
+        if constexpr (ES == 2) put8(row, pack4(o));
+        else put16(row, f32x4_t{o.v[0], o.v[1], o.v[2], o.v[3]});
       }
-    } else {
-      // K slice d of all chosen experts' (the shared one's first) rows n0 .. n0 + 31 of down
-      const int d = (task - nup) / ntile, nt = (task - nup) % ntile, n0 = nt * kCols;
-      const int SS = Fs * ES / 64, SF = F * ES / 64;
-      const long long all = SS + (long long)nseg * SF;
-      const int lo = (int)(all * d / a.D), hi = (int)(all * (d + 1) / a.D);
-      int s = lo + (int)((long long)(hi - lo) * wave / kWaves);
-      const int end = lo + (int)((long long)(hi - lo) * (wave + 1) / kWaves);
-      while (s < end) {
-        const bool sh = s < SS;
-        const int seg = sh ? 0 : (s - SS) / SF, e = sh ? -1 : __builtin_amdgcn_readfirstlane(L.segs[seg]);
-        const int first = sh ? 0 : SS + seg * SF, K = sh ? Fs : F;
-        const int stop = min(end, first + (sh ? SS : SF));
-        const uint8_t* base = static_cast<const uint8_t*>(sh ? a.s_down : a.down) +
-                              (sh ? 0 : (size_t)e * H * F * ES) + kq * 16;
-        const uint8_t* wp[2] = {base + (size_t)(n0 + l16) * K * ES, base + (size_t)(n0 + 16 + l16) * K * ES};
-        const uint8_t* cp[NT];
-        float wt[NT];
-        bool in[NT];
+      announce(done);
+      t0 = t1;
+      t1 = uni(L.ticket[turn]);
+      turn ^= 1;
+    }
+    if (task >= ndown) return;
+    wait_count(done, (unsigned)nup);
+    lds_barrier();
+    for (turn = 0; task < ndown; task += gridDim.x, turn ^= 1) {
+      lds_barrier();
+      const int d = task / ntile, nt = task % ntile;
+      // lane l has columns 4 (l % 4) .. + 3 of token l / 4 and every 16th after it
+      const int n = (a.T + 15) / 16, c = (lane & 3) * 4;
+      f32x4_t v[kFewT / 16];
 #pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          // a token that did not choose the expert reads the row of one that did, and drops
-          // the result
-          int p = tok[c];
-          wt[c] = 1.0f;
-          if (!sh) p = pair_of(L.idx[tok[c]], L.w[tok[c]], tok[c], e, a.k, wt[c]);
-          in[c] = p >= 0;
-          if (p < 0) p = L.mark[e];
-          cp[c] = reinterpret_cast<const uint8_t*>((sh ? hs : h) + (size_t)p * K) + kq * 16;
+      for (int i = 0; i < kFewT / 16; ++i) {
+        if (i >= n) continue;
+        const int t = min(i * 16 + (lane >> 2), a.T - 1);
+        v[i] = *reinterpret_cast<const f32x4_t*>(&L.out[turn][0][t][c]);
+#pragma unroll
+        for (int q = 1; q < kWaves; ++q) v[i] += *reinterpret_cast<const f32x4_t*>(&L.out[turn][q][t][c]);
+      }
+      if (a.D > 1) {
+        // the slice that arrives last adds all of them up, in slice order
+        const uint32_t tile = (uint32_t)a.T * kCols * 4, at = (uint32_t)(nt * a.D) * tile + lane * 16;
+        uint8_t* P = reinterpret_cast<uint8_t*>(a.part) + at + d * tile;
+#pragma unroll
+        for (int i = 0; i < kFewT / 16; ++i)
+          if (i < n && i * 16 + (lane >> 2) < a.T) put16(P + i * 1024, v[i]);
+        if (announce(a.counters + 2 * kLine + nt) != (unsigned)(a.D - 1)) continue;
+        const Shared pb = shared_buffer(a.part, (uint32_t)ndown * tile);
+#pragma unroll
+        for (int i = 0; i < kFewT / 16; ++i) {
+          if (i >= n) continue;
+          u32x4_t q[kMaxDown];
+#pragma unroll
+          for (int j = 0; j < kMaxDown; ++j)  // all loads first, from clamped slices
+            q[j] = get16(pb, at + i * 1024, (uint32_t)min(j, a.D - 1) * tile);
+          v[i] = __builtin_bit_cast(f32x4_t, q[0]);
+#pragma unroll
+          for (int j = 1; j < kMaxDown; ++j)
+            if (j < a.D) v[i] += __builtin_bit_cast(f32x4_t, q[j]);
         }
-        f32x4_t part[2][NT];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int c = 0; c < NT; ++c) part[r][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        wait_count(done + 1 + e, (unsigned)((sh ? CS : CF) * NT));
-        stream<T, NT, U>(wp, cp, s - first, stop - first, part);
-        if (!sh && s == first && a.b_down != nullptr) {  // the bias once, with the first part
-          const T* b = static_cast<const T*>(a.b_down) + (size_t)e * H + n0 + kq * 4;
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const Out4 bv = load4(b + r * 16);
-#pragma unroll
-            for (int c = 0; c < NT; ++c)
-#pragma unroll
-              for (int v = 0; v < 4; ++v) part[r][c][v] += bv.v[v];
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          if (!in[c]) continue;
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) acc[r][c][v] = fmaf(wt[c], part[r][c][v], acc[r][c][v]);
-        }
-        s = stop;
       }
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int c = 0; c < NT; ++c) L.red[wave][r][c][lane] = acc[r][c];
-      __syncthreads();
-      if (wave < NT) {
-        f32x4_t v[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          v[r] = L.red[0][r][wave][lane];
-#pragma unroll
-          for (int q = 1; q < kWaves; ++q) v[r] += L.red[q][r][wave][lane];
-        }
-        bool last = true;
-        if (a.D > 1) {
-          // the slice that arrives last adds all of them up, in slice order
-          float* P = a.part + ((size_t)nt * a.D * 2 * NT + wave) * 256 + lane * 4;
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-            *reinterpret_cast<f32x4_t*>(P + (size_t)((d * 2 + r) * NT) * 256) = v[r];
-          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-          unsigned before = 0;
-          if (lane == 0)
-            before = __hip_atomic_fetch_add(arrived + nt * NT + wave, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          last = __builtin_amdgcn_readfirstlane(before) == (unsigned)(a.D - 1);
-          if (last) {
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              f32x4_t q[kMaxDown];
-#pragma unroll
-              for (int i = 0; i < kMaxDown; ++i)  // all loads first, from clamped slices
-                q[i] = *reinterpret_cast<const f32x4_t*>(P + (size_t)((min(i, a.D - 1) * 2 + r) * NT) * 256);
-              v[r] = q[0];
-#pragma unroll
-              for (int i = 1; i < kMaxDown; ++i)
-                if (i < a.D) v[r] += q[i];
-            }
-          }
-        }
-        const int t = wave * 16 + l16;
-        if (last && t < a.T) {
-          T* row = static_cast<T*>(a.out) + (size_t)t * H + n0 + kq * 4;
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            if constexpr (ES == 2)
-              *reinterpret_cast<uint2*>(row + r * 16) = make_uint2(cvt_bf16x2(v[r][0], v[r][1]), cvt_bf16x2(v[r][2], v[r][3]));
-            else
-              *reinterpret_cast<f32x4_t*>(row + r * 16) = v[r];
-          }
-        }
+      for (int i = 0; i < kFewT / 16; ++i) {
+        const int t = i * 16 + (lane >> 2);
+        if (t < a.T) store4(static_cast<T*>(a.out) + (size_t)t * H + nt * kCols + c, v[i]);
       }
     }
-    __syncthreads();  // red and ticket are free
+    return;
+  }
+
+  // the streams
+  const int SH = H * ES / 64, lo = wave * SH / kWaves, hi = (wave + 1) * SH / kWaves;
+  struct Up {
+    Rows rows;
+    uint32_t col;  // the lane's row of x
+  };
+  auto up = [&](int t) {
+    const Task k = up_task(t);
+    const int e = uni(L.expert[k.unit]), N = e < 0 ? Fs : F;
+    Up u;
+    u.rows.w = static_cast<const uint8_t*>(e < 0 ? a.s_up : a.up) +
+               (e < 0 ? 0 : (size_t)e * (gt ? 2 : 1) * F * H * ES) + (size_t)k.f0 * H * ES + lo * 64;
+    // with a gate, 8 gate rows and the 8 up rows of the same columns
+    const uint32_t row = gt ? (l16 & 7) + (l16 >> 3) * N : l16;
+    u.rows.lane = row * (uint32_t)(H * ES) + kq * 16;
+    u.rows.steps = hi - lo;
+    const int p = L.first[k.unit] + min(l16, L.pairs[k.unit] - 1);
+    u.col = (uint32_t)((e < 0 ? p : L.tok[p]) * H * ES + kq * 16);
+    return u;
+  };
+  const Shared xb = shared_buffer(a.x, (uint32_t)a.T * H * ES);
+
+  // A piece of a down task: steps of one unit in this wave's part of the task's K slice.
+  struct Piece {
+    Rows rows;
+    uint32_t col, at;   // the lane's row of h and the first byte of it
+    int unit, s, n0;    // first step among all units', first column of the task
+    bool first;         // has the unit's first step
+  };
+  const Shared hb = shared_buffer(h, (uint32_t)((shared_at + (size_t)a.T * Fs) * ES));
+  const int SS = Fs * ES / 64, SF = F * ES / 64, all = su * SS + (units - su) * SF;
+  auto piece = [&](int n0, int s0, int end) {
+    Piece p;
+    const int s = min(s0, all - 1), r = s - su * SS;  // an empty piece points at something
+    const bool sh = r < 0;
+    p.unit = sh ? s / SS : su + r / SF;
+    const int first = sh ? p.unit * SS : su * SS + (p.unit - su) * SF, K = sh ? Fs : F;
+    const int e = uni(L.expert[p.unit]);
+    p.s = s0, p.n0 = n0;
+    p.rows.steps = max(0, min(end, first + (sh ? SS : SF)) - s0);
+    p.first = s == first;
+    p.at = (uint32_t)(s - first) * 64;
+    p.rows.w = static_cast<const uint8_t*>(sh ? a.s_down : a.down) + (sh ? 0 : (size_t)e * H * F * ES) +
+               (size_t)n0 * K * ES + p.at;
+    p.rows.lane = (uint32_t)(l16 * K * ES + kq * 16);
+    const size_t row = L.first[p.unit] + min(l16, L.pairs[p.unit] - 1);
+    p.col = (uint32_t)(((sh ? shared_at : 0) + row * K) * ES) + kq * 16;
+    return p;
+  };
+  auto wave_end = [&](int t, int w) {  // step at which the part of wave w - 1 ends
+    const int d = t / ntile;
+    const int from = (int)((long long)all * d / a.D), to = (int)((long long)all * (d + 1) / a.D);
+    return from + (int)((long long)(to - from) * w / kWaves);
+  };
+  auto first_piece = [&](int t) { return piece(t % ntile * kCols, wave_end(t, wave), wave_end(t, wave + 1)); };
+
+  Piece p = first_piece(min(task, ndown - 1));
+  Ring<R> ring;
+  int turn = 0;
+  if (t0 < nup) {
+    Up u = up(t0);
+    first_steps(ring, u.rows, [&](int s) { return __builtin_amdgcn_raw_buffer_load_b128(xb, u.col, (lo + s) * 64, 0); });
+    while (t0 < nup) {
+      const bool more = t1 < nup;  // else the down weights, whose rows of h are not there yet
+      Up n;
+      n.rows = p.rows, n.col = 0;
+      if (more) n = up(t1);
+      L.red[turn][wave][lane] = stream<T>(ring, u.rows, n.rows, [&](int s, bool next) {
+        return __builtin_amdgcn_raw_buffer_load_b128(xb, next ? n.col : u.col, next && !more ? 0 : (lo + s) * 64, 0);
+      });
+      lds_barrier();
+      t0 = t1;
+      t1 = uni(L.ticket[turn]);
+      turn ^= 1;
+      u = n;
+    }
+  } else if (task < ndown) {
+    first_rows(ring, p.rows);
+  }
+  if (task >= ndown) return;
+  lds_barrier();  // every up task is done: no load from h before this, and red is read
+  first_cols(ring, p.rows.steps, [&](int s) { return get16(hb, p.col, p.at + s * 64); });
+  for (turn = 0; task < ndown; task += gridDim.x, turn ^= 1) {
+    float (*out)[kCols] = L.out[turn][wave];
+    for (int i = lane; i < a.T * (kCols / 4); i += 64)
+      *reinterpret_cast<f32x4_t*>(&out[i >> 2][(i & 3) * 4]) = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const int end = wave_end(task, wave + 1);
+    for (bool more = true; more;) {
+      more = p.s + p.rows.steps < end;
+      const Piece q = more ? piece(p.n0, p.s + p.rows.steps, end)
+                           : first_piece(task + (int)gridDim.x < ndown ? task + (int)gridDim.x : task);
+      f32x4_t part = stream<T>(ring, p.rows, q.rows, [&](int s, bool next) {
+        return get16(hb, next ? q.col : p.col, (next ? q.at : p.at) + s * 64);
+      });
+      if (p.rows.steps > 0 && l16 < L.pairs[p.unit]) {
+        const int e = L.expert[p.unit], place = L.first[p.unit] + l16;
+        if (p.first && e >= 0 && a.b_down != nullptr) {  // the bias once, with the first part
+          const Out4 b = load4(static_cast<const T*>(a.b_down) + (size_t)e * H + p.n0 + kq * 4);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) part[v] += b.v[v];
+        }
+        const int t = e < 0 ? place : L.tok[place];
+        const float w = e < 0 ? 1.0f : L.w[place];
+        f32x4_t* at = reinterpret_cast<f32x4_t*>(&out[t][kq * 4]);
+        f32x4_t o = *at;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) o[v] = fmaf(w, part[v], o[v]);
+        *at = o;
+      }
+      p = q;
+    }
+    lds_barrier();
   }
 }
 
 // ----------------------------------------------------------------- host side
 
-int col_tiles(int T) { return T <= 16 ? 1 : T <= 32 ? 2 : 4; }
-
-// K slices of the down tasks: two tasks a CU, each wave of a task with 4 steps or more.
+// K slices of the down tasks: a task a CU, each wave of a task with 4 steps or more.
 int down_slices(int H, int F, int Fs, int k, bool bf16) {
   const int steps = (int)(((long long)k * F + Fs) * (bf16 ? 2 : 4) / 64);
   int d = 1;
-  while (d < kMaxDown && H / kCols * d * 2 <= 512 && steps / (d * 2) >= 4 * kWaves) d *= 2;
+  while (d < kMaxDown && H / kCols * d * 2 <= 256 && steps / (d * 2) >= 4 * kWaves) d *= 2;
   return d;
+}
+
+// K slices of the scores: up to 128 workgroups, each wave of one with a step or more.
+int score_slices(int T, int H, int E, bool bf16) {
+  const int tiles = ((E + 15) / 16) * ((T + 15) / 16), steps = H * (bf16 ? 2 : 4) / 64;
+  int n = 1;
+  while (n < kMaxScore && tiles * n * 2 <= 128 && steps >= 8 * n) n *= 2;
+  return n;
 }
 
 struct FewLayout {
@@ -460,46 +582,37 @@ struct FewLayout {
 };
 FewLayout layout(int T, int H, int E, int k, int F, int Fs, bool bf16) {
   FewLayout l{};
-  const int nt = col_tiles(T), D = down_slices(H, F, Fs, k, bf16);
+  const int D = down_slices(H, F, Fs, k, bf16);
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t p = at;
     at += align256(n);
     return p;
   };
-  l.scores = take((size_t)T * E * 4);
+  l.scores = take((size_t)score_slices(T, H, E, bf16) * T * E * 4);
   l.h = take(((size_t)T * k * F + (size_t)T * Fs) * (bf16 ? 2 : 4));
-  l.part = take(D > 1 ? (size_t)(H / kCols) * D * 2 * nt * 1024 : 0);
-  l.counters = take((size_t)counter_ints(E, H, nt) * 4);
+  l.part = take(D > 1 ? (size_t)(H / kCols) * D * T * kCols * 4 : 0);
+  l.counters = take((size_t)counter_ints(H) * 4);
   l.bytes = at;
   return l;
 }
 
-template <typename T, int NT>
-hipError_t launch_queue(const FewArgs& a, int grid, hipStream_t s) {
-  if (a.E <= 64) hipLaunchKernelGGL((few_kernel<T, NT, 64>), dim3(grid), dim3(kFewThreads), 0, s, a);
-  else hipLaunchKernelGGL((few_kernel<T, NT, kMaxE>), dim3(grid), dim3(kFewThreads), 0, s, a);
-  return hipGetLastError();
-}
-
 template <typename T>
 hipError_t launch_few_t(const FewArgs& a, const void* wg, hipStream_t s) {
-  const int nt = col_tiles(a.T);
-  hipLaunchKernelGGL((few_scores_kernel<T>), dim3((a.E + 15) / 16, (a.T + 15) / 16), dim3(kScoreWaves * 64),
-                     0, s, static_cast<const T*>(a.x), static_cast<const T*>(wg), a.T, a.H, a.E, a.scores,
-                     a.counters, counter_ints(a.E, a.H, nt));
+  hipLaunchKernelGGL((few_scores_kernel<T>), dim3((a.E + 15) / 16, (a.T + 15) / 16, a.KS), dim3(256), 0, s,
+                     static_cast<const T*>(a.x), static_cast<const T*>(wg), a.T, a.H, a.E, a.scores,
+                     a.counters, counter_ints(a.H));
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  // two workgroups a CU, no more than there are tasks
+  // a workgroup a CU, no more than there are tasks
   const int chunk = a.act == kActGeglu || a.act == kActSwiglu ? kCols / 2 : kCols;
   const long long tasks = (long long)std::min(a.E, a.T * a.k) * (a.F / chunk) + a.Fs / chunk +
                           (long long)(a.H / kCols) * a.D;
-  const int grid = (int)std::min(tasks, 512LL);
-  switch (nt) {
-    case 1: return launch_queue<T, 1>(a, grid, s);
-    case 2: return launch_queue<T, 2>(a, grid, s);
-    default: return launch_queue<T, 4>(a, grid, s);
-  }
+  const dim3 grid((unsigned)std::min(tasks, 256LL)), block((kWaves + 1) * 64);
+  if (a.E <= 64) hipLaunchKernelGGL((few_kernel<T, 64>), grid, block, 0, s, a);
+  else if (a.E <= 128) hipLaunchKernelGGL((few_kernel<T, 128>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((few_kernel<T, kMaxE>), grid, block, 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -524,6 +637,7 @@ hipError_t launch_few(const FewCall& c, hipStream_t s) {
   a.h = ws + l.h;
   a.part = reinterpret_cast<float*>(ws + l.part);
   a.counters = reinterpret_cast<unsigned*>(ws + l.counters);
+  a.KS = score_slices(c.T, c.H, c.E, c.bf16);
   a.D = down_slices(c.H, c.F, c.Fs, c.k, c.bf16);
   a.idx = c.idx, a.w = c.w, a.out = c.out;
   return c.bf16 ? launch_few_t<uint16_t>(a, c.wg, s) : launch_few_t<float>(a, c.wg, s);

@@ -3,6 +3,8 @@
 // including file. The formulas are at the head of route_grouped.hip.
 #pragma once
 
+#include <type_traits>
+
 #include "route_tile.hpp"
 
 namespace moe {
@@ -41,6 +43,49 @@ struct GroupLds {
   float v[BT * tile_stride<BT, NW>()];
   float gs[BT][kMaxGroups + 1];
 };
+
+// The largest u of the wave, in every lane: DPP steps within 16 lanes, then their last
+// lanes broadcast to the next 16 and 32 (row_bcast), lane 63 has it.
+__device__ __forceinline__ uint32_t wave_max(uint32_t u) {
+  auto step = [&](auto ctrl) {
+    u = max(u, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  step(std::integral_constant<int, 0x111>{});  // row_shr 1, 2, 4, 8
+  step(std::integral_constant<int, 0x112>{});
+  step(std::integral_constant<int, 0x114>{});
+  step(std::integral_constant<int, 0x118>{});
+  step(std::integral_constant<int, 0x142>{});  // row_bcast 15, 31
+  step(std::integral_constant<int, 0x143>{});
+  return (uint32_t)__builtin_amdgcn_readlane((int)u, 63);
+}
+
+// list[0 .. k-1] <- the k largest keys of a token that has a whole wave: lane g holds the
+// high halves (scores) of the keys of experts g, g + 64, ... (0: none). k times the largest
+// score, then its lowest expert from the lanes' masks, in scalar registers: 20 instructions
+// a round, where merging sorted lists of 8 over 64 lanes takes 700.
+template <int KP, int NSUB>
+__device__ __forceinline__ void pop_top(uint32_t (&o)[NSUB], int k, uint64_t (&list)[KP]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int j = 0; j < KP; ++j) {
+    list[j] = 0;
+    if (j >= k) continue;
+    uint32_t m = o[0];
+#pragma unroll
+    for (int i = 1; i < NSUB; ++i) m = max(m, o[i]);
+    m = wave_max(m);
+    int e = -1;
+#pragma unroll
+    for (int i = NSUB - 1; i >= 0; --i) {
+      const unsigned long long at = __ballot(o[i] == m);
+      if (at != 0) e = 64 * i + __ffsll(at) - 1;
+    }
+#pragma unroll
+    for (int i = 0; i < NSUB; ++i)
+      if (e == 64 * i + lane) o[i] = 0;
+    list[j] = ((uint64_t)m << 32) | (uint32_t)(~(uint32_t)e);
+  }
+}
 
 // Chooses for the BT tokens whose scores are in the LDS tile sc (row stride
 // tile_stride<BT, NW>(), no bias in them). Lanes as in topk_tokens: G = 64 * NW / BT
@@ -154,24 +199,35 @@ __device__ __forceinline__ void grouped_tokens(const float* sc, GroupLds<BT, NW>
   }
 
   uint64_t list[KP];
+  if constexpr (G == 64) {
+    uint32_t o[NSUB];
 #pragma unroll
-  for (int b = 0; b < NBLK; ++b) {
-    uint64_t blk[KP];
-#pragma unroll
-    for (int i = 0; i < KP; ++i) {
-      const int e = g + G * (b * KP + i);
+    for (int i = 0; i < NSUB; ++i) {
+      const int e = g + G * i;
       const bool in = e < E && ((mask >> ((min(e, E - 1) * a.magic) >> 16)) & 1);
-      blk[i] = topk_key(x[b * KP + i], e) & (uint64_t)(-(int64_t)in);
+      o[i] = in ? (uint32_t)(topk_key(x[i], e) >> 32) : 0u;
     }
-    bitonic_sort<KP>(blk);
-    if (b == 0) {
+    pop_top<KP, NSUB>(o, k, list);
+  } else {
 #pragma unroll
-      for (int i = 0; i < KP; ++i) list[i] = blk[i];
-    } else {
-      merge_top<KP>(list, blk);
+    for (int b = 0; b < NBLK; ++b) {
+      uint64_t blk[KP];
+#pragma unroll
+      for (int i = 0; i < KP; ++i) {
+        const int e = g + G * (b * KP + i);
+        const bool in = e < E && ((mask >> ((min(e, E - 1) * a.magic) >> 16)) & 1);
+        blk[i] = topk_key(x[b * KP + i], e) & (uint64_t)(-(int64_t)in);
+      }
+      bitonic_sort<KP>(blk);
+      if (b == 0) {
+#pragma unroll
+        for (int i = 0; i < KP; ++i) list[i] = blk[i];
+      } else {
+        merge_top<KP>(list, blk);
+      }
     }
+    group_merge<0, G, KP>(list);
   }
-  group_merge<0, G, KP>(list);
 
   // the chosen scores; an expert that is off (chosen only when fewer than k
   // are on) weighs nothing

@@ -48,15 +48,18 @@ struct FewArgs {
   float* scores;       // [KS, T, E]
   void* h;             // [T * k, F] in the order of the experts, then [T, Fs]
   float* part;         // [H / 16, D, T, 16]: partial columns of out
-  unsigned* counters;  // tickets | up tasks done | arrived [H / 16]
+  unsigned* counters;  // tickets | up tasks done | go [kGo] | arrived [H / 16]
   int KS, D;
   int32_t* idx;
   float* w;
   void* out;
 };
 
-constexpr int kLine = 32;  // ints of a cache line: tickets and done have one each
-inline int counter_ints(int H) { return 2 * kLine + H / kCols; }
+// Tickets, done and every go have 512 bytes of their own: workgroups that wait would slow
+// down those that count, and they look at one of kGo places, which the last up task sets.
+constexpr int kLine = 128, kGo = 16;
+constexpr int kArrived = (2 + kGo) * kLine;
+inline int counter_ints(int H) { return kArrived + H / kCols; }
 
 // ----------------------------------------------------------------- scores
 
@@ -131,11 +134,11 @@ __device__ __forceinline__ unsigned announce(unsigned* p) {
   return __builtin_amdgcn_readfirstlane(before);
 }
 
-// Waits until *p has reached n, a second at most (100 ticks of this clock a microsecond).
-__device__ __forceinline__ void wait_count(const unsigned* p, unsigned n) {
+// Waits until *p is set, a second at most (100 ticks of this clock a microsecond).
+__device__ __forceinline__ void wait_set(const unsigned* p) {
   const unsigned long long start = wall_clock64();
-  while (__hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < n) {
-    __builtin_amdgcn_s_sleep(2);
+  while (__hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0) {
+    __builtin_amdgcn_s_sleep(4);
     if (wall_clock64() - start > 100000000ull) break;
   }
 }
@@ -230,9 +233,17 @@ struct FewLds {
 
 // The choice of every token; the pairs in the experts' order, and the units: the shared
 // expert's, then each expert's. One wave a token, for itself, then one thread a pair.
+// The wave that finishes tasks draws the workgroup's first two tickets meanwhile, the
+// second when every workgroup has its first.
+__device__ __forceinline__ int draw_ticket(const FewArgs& a) {
+  return (int)__hip_atomic_fetch_add(a.counters, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 template <int EPX>
 __device__ __forceinline__ void choose(const FewArgs& a, FewLds& L) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const bool drawer = tid == kWaves * 64;
+  if (drawer) L.start[0] = draw_ticket(a);
   for (int t = wave; t < a.T && wave < kWaves; t += kWaves) {
     float* row = L.choice.sc + wave * L.S;
 #pragma unroll
@@ -254,6 +265,7 @@ __device__ __forceinline__ void choose(const FewArgs& a, FewLds& L) {
   }
   for (int i = tid; i < kWaves * kMaxE; i += kWaves * 64) (&L.choice.count[0][0])[i] = 0;
   lds_barrier();
+  if (drawer) L.start[1] = draw_ticket(a);
   // Places have to be the same in every workgroup: pairs of an expert keep their order.
   // Pairs of this wave with the lane's expert: by the 8 bits of its number.
   const bool pair = tid < a.T * a.k;  // the streams' threads
@@ -339,13 +351,7 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
   constexpr int ES = (int)sizeof(T);
   __shared__ FewLds L;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  auto draw = [&] { return (int)__hip_atomic_fetch_add(a.counters, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-  const bool drawer = tid == kWaves * 64;
-  if (drawer) L.start[0] = draw();
   choose<EPX>(a, L);
-  // the second ticket only now: every workgroup has its first
-  if (drawer) L.start[1] = draw();
-  lds_barrier();
   auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
   const bool gt = gated(a.act);
   const int H = a.H, F = a.F, Fs = a.Fs, units = uni(L.units);
@@ -355,7 +361,6 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
   const int nup = su * CS + (units - su) * CF, ntile = H / kCols, ndown = ntile * a.D;
   T* h = static_cast<T*>(a.h);
   const size_t shared_at = (size_t)a.T * a.k * F;  // the shared expert's rows (elements)
-  unsigned* done = a.counters + kLine;
   const int l16 = lane & 15, kq = lane >> 4;
   struct Task {
     int unit, f0;  // first column of h
@@ -370,7 +375,7 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
   if (wave == kWaves) {
     int turn = 0;
     while (t0 < nup) {
-      if (drawer) L.ticket[turn] = draw();
+      if (lane == 0) L.ticket[turn] = draw_ticket(a);
       lds_barrier();
       // sums in wave order; with a gate, the up half is in the lanes 32 further on
       f32x4_t v = L.red[turn][0][lane], u = L.red[turn][0][lane ^ 32];
@@ -391,13 +396,14 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
         if constexpr (ES == 2) put8(row, pack4(o));
         else put16(row, f32x4_t{o.v[0], o.v[1], o.v[2], o.v[3]});
       }
-      announce(done);
+      if (announce(a.counters + kLine) == (unsigned)(nup - 1) && lane < kGo)
+        __hip_atomic_store(a.counters + (2 + lane) * kLine, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       t0 = t1;
       t1 = uni(L.ticket[turn]);
       turn ^= 1;
     }
     if (task >= ndown) return;
-    wait_count(done, (unsigned)nup);
+    wait_set(a.counters + (2 + blockIdx.x % kGo) * kLine);
     lds_barrier();
     for (turn = 0; task < ndown; task += gridDim.x, turn ^= 1) {
       lds_barrier();
@@ -420,7 +426,7 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
 #pragma unroll
         for (int i = 0; i < kFewT / 16; ++i)
           if (i < n && i * 16 + (lane >> 2) < a.T) put16(P + i * 1024, v[i]);
-        if (announce(a.counters + 2 * kLine + nt) != (unsigned)(a.D - 1)) continue;
+        if (announce(a.counters + kArrived + nt) != (unsigned)(a.D - 1)) continue;
         const Shared pb = shared_buffer(a.part, (uint32_t)ndown * tile);
 #pragma unroll
         for (int i = 0; i < kFewT / 16; ++i) {

@@ -209,11 +209,13 @@ __device__ __forceinline__ Out4 load4(const float* p) {
 
 // Bias and residual of the 4 columns c .. c + 3 of buffer row `row`, then finish4
 // and the store. e: the row's expert.
-template <typename T>
+// ACT: the act where it is known when compiling.
+template <typename T, int ACT = -1>
 __device__ __forceinline__ void store4(const LinArgs& a, int e, size_t row, int c,
                                        const f32x4_t& g, const f32x4_t& u) {
   constexpr bool BF16 = sizeof(T) == 2;
-  const bool gt = gated(a.act);
+  const int act = ACT >= 0 ? ACT : a.act;
+  const bool gt = gated(act);
   Out4 bg{}, bu{}, rv{};
   if (a.bias != nullptr) {
     const T* b = static_cast<const T*>(a.bias) + (size_t)e * (gt ? 2 : 1) * a.N + c;
@@ -222,7 +224,7 @@ __device__ __forceinline__ void store4(const LinArgs& a, int e, size_t row, int 
   }
   const size_t at = row * a.N + c;
   if (a.res != nullptr) rv = load4(static_cast<const T*>(a.res) + at);
-  const Out4 o = finish4<BF16>(a.act, g, u, bg, bu, a.res != nullptr, rv);
+  const Out4 o = finish4<BF16>(act, g, u, bg, bu, a.res != nullptr, rv);
   T* y = static_cast<T*>(a.y) + at;
   if constexpr (BF16) *reinterpret_cast<uint2*>(y) = pack4(o);
   else *reinterpret_cast<f32x4_t*>(y) = f32x4_t{o.v[0], o.v[1], o.v[2], o.v[3]};

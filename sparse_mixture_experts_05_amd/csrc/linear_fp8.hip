@@ -19,43 +19,12 @@
 
 #include "common.hpp"
 #include "kernels.hpp"
-#include "linear.hpp"
+#include "linear_fp8.hpp"
 
 namespace moe {
 namespace {
 
 using namespace lin;
-
-constexpr int kBlock = 128;  // elements of a scale block, a stage of K and a fragment row
-
-struct Fp8Args {
-  LinArgs a;
-  const float* xs;  // [K / 128, rows of x]
-  const float* ws;  // [E, (2,) ceil(N / 128), K / 128]
-  int xrows;
-};
-
-typedef int v8i_t __attribute__((ext_vector_type(8)));
-
-// 16 x 16 products of one block: lane l holds 32 bytes of row l % 16 of each operand.
-// D as mma16.
-__device__ __forceinline__ f32x4_t mma_block(u32x4_t a0, u32x4_t a1, u32x4_t b0, u32x4_t b1) {
-  const v8i_t a = __builtin_bit_cast(v8i_t, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
-  const v8i_t b = __builtin_bit_cast(v8i_t, __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7));
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0,
-                                                          0, 0, 0, 0);
-}
-
-// Scales of the weights of 128 output columns around column c of expert e: its first block.
-__device__ __forceinline__ const float* w_scales(const Fp8Args& f, int e, int half, bool gt, int c) {
-  const int nkb = f.a.K / kBlock, nnb = (f.a.N + kBlock - 1) / kBlock;
-  return f.ws + (((size_t)e * (gt ? 2 : 1) + half) * nnb + min(c / kBlock, nnb - 1)) * nkb;
-}
-
-__device__ __forceinline__ void fma4(f32x4_t& acc, float s, const f32x4_t& p) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) acc[c] = fmaf(s, p[c], acc[c]);
-}
 
 // ----------------------------------------------------------------- tiles
 
@@ -123,7 +92,7 @@ __global__ __launch_bounds__(Sh::NT) void fp8_tile_kernel(Fp8Args f) {
   const int N = a.N, K = a.K;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / Sh::WN, wn = wave % Sh::WN;
-  const int KT0 = K / kBlock;
+  const int KT0 = K / kBlock8;
   const int kbase = (int)((long long)blockIdx.y * KT0 / gridDim.y);
   const int KT = (int)((long long)(blockIdx.y + 1) * KT0 / gridDim.y) - kbase;
 
@@ -143,7 +112,7 @@ __global__ __launch_bounds__(Sh::NT) void fp8_tile_kernel(Fp8Args f) {
       const int c = t.n0 + col8<Sh>(b / (BN / Sh::WN), j - half * (TN / 2), GT) + b % 16;
       row = w + ((size_t)half * N + min(c, N - 1)) * K;  // columns past the end: its last
     }
-    src[q] = row + (size_t)kbase * kBlock + chunk * 16;
+    src[q] = row + (size_t)kbase * kBlock8 + chunk * 16;
   }
   const float* ssrc[SI];
 #pragma unroll
@@ -154,7 +123,7 @@ __global__ __launch_bounds__(Sh::NT) void fp8_tile_kernel(Fp8Args f) {
   auto issue = [&](int kt) {
     uint8_t* base = smem + (kt % NS) * Sh::STAGE;
 #pragma unroll
-    for (int q = 0; q < NI; ++q) lds_dma16(src[q] + (size_t)kt * kBlock, base + (wave * NI + q) * 1024);
+    for (int q = 0; q < NI; ++q) lds_dma16(src[q] + (size_t)kt * kBlock8, base + (wave * NI + q) * 1024);
 #pragma unroll
     for (int q = 0; q < SI; ++q)
       lds_dma4(ssrc[q] + (size_t)kt * f.xrows, base + Sh::ROWS + (wave * SI + q) * 256);
@@ -285,7 +254,7 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args f) {
   if (t.M == 0) return;
   const int N = a.N, K = a.K;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int S = K / kBlock;
+  const int S = K / kBlock8;
   const int s0 = wave * S / KQ, s1 = (wave + 1) * S / KQ;
   const uint8_t* wp[H];
   const float* wsp[H];
@@ -311,12 +280,12 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args f) {
     for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        d[u].w[h][0] = ld16(wp[h] + (size_t)(s + u) * kBlock);
-        d[u].w[h][1] = ld16(wp[h] + (size_t)(s + u) * kBlock + 64);
+        d[u].w[h][0] = ld16(wp[h] + (size_t)(s + u) * kBlock8);
+        d[u].w[h][1] = ld16(wp[h] + (size_t)(s + u) * kBlock8 + 64);
         d[u].ws[h] = wsp[h][s + u];
       }
-      d[u].x[0] = ld16(xp + (size_t)(s + u) * kBlock);
-      d[u].x[1] = ld16(xp + (size_t)(s + u) * kBlock + 64);
+      d[u].x[0] = ld16(xp + (size_t)(s + u) * kBlock8);
+      d[u].x[1] = ld16(xp + (size_t)(s + u) * kBlock8 + 64);
       d[u].xs = xsp[(size_t)(s + u) * f.xrows];
     }
   };
@@ -350,12 +319,12 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args f) {
     Step d;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      d.w[h][0] = ld16(wp[h] + (size_t)s * kBlock);
-      d.w[h][1] = ld16(wp[h] + (size_t)s * kBlock + 64);
+      d.w[h][0] = ld16(wp[h] + (size_t)s * kBlock8);
+      d.w[h][1] = ld16(wp[h] + (size_t)s * kBlock8 + 64);
       d.ws[h] = wsp[h][s];
     }
-    d.x[0] = ld16(xp + (size_t)s * kBlock);
-    d.x[1] = ld16(xp + (size_t)s * kBlock + 64);
+    d.x[0] = ld16(xp + (size_t)s * kBlock8);
+    d.x[1] = ld16(xp + (size_t)s * kBlock8 + 64);
     d.xs = xsp[(size_t)s * f.xrows];
     one(d);
   }
@@ -379,7 +348,6 @@ bool host_gated(int act) { return act == kActGeglu || act == kActSwiglu; }
 
 using Small = Shape8<64, 64, 2, 2, 3>;
 using Mid = Shape8<128, 128, 2, 2, 2>;
-using Large = Shape8<256, 256, 2, 4, 2>;
 
 // Tiles of a launch, at most: sum_e ceil(c_e / BM) <= M / BM + #{e : c_e > 0} row tiles,
 // each with all column tiles.
@@ -394,6 +362,8 @@ long long tiles8(const LinArgs& a) {
 }
 unsigned rounds8(long long tiles) { return (unsigned)((tiles + 7) / 8 * 8); }  // of the 8 XCDs
 
+long long big_tiles8(const LinArgs& a) { return tiles8(a, 256, host_gated(a.act) ? 128 : 256); }
+
 enum Fp8Path { kRows8, kSmall8, kMid8, kLarge8 };  // moe_fp8_path
 struct Fp8Plan {
   Fp8Path path;
@@ -404,10 +374,10 @@ Fp8Plan plan8(const LinArgs& a) {
   const double live = a.offsets ? a.E * (1.0 - std::exp(-(double)a.M / a.E)) : 1.0;
   const double per = a.M / live;
   if (per <= 16) return {kRows8, 1};
-  if (tiles8<Large>(a) >= 200) return {kLarge8, 1};
+  if (fp8_big_ok(a) && big_tiles8(a) >= 200) return {kLarge8, 1};
   if (tiles8<Mid>(a) >= 200) return {kMid8, 1};
   int nks = 1;
-  while (nks < kMaxSlices && tiles8<Small>(a) * nks * 2 <= 512 && a.K / kBlock >= 8 * nks) nks *= 2;
+  while (nks < kMaxSlices && tiles8<Small>(a) * nks * 2 <= 512 && a.K / kBlock8 >= 8 * nks) nks *= 2;
   return {kSmall8, nks};
 }
 
@@ -438,7 +408,7 @@ hipError_t run8(Fp8Args f, const Fp8Plan& p, void* ws, hipStream_t s) {
     }
     case kSmall8: return run_tiles8<Small, GT>(f, p.nks, ws, s);
     case kMid8: return run_tiles8<Mid, GT>(f, p.nks, ws, s);
-    default: return run_tiles8<Large, GT>(f, p.nks, ws, s);
+    default: f.a.tiles = (int)big_tiles8(f.a); return launch_fp8_big(f, rounds8(f.a.tiles), s);
   }
 }
 
@@ -463,7 +433,8 @@ bool linear_fp8_fits(int E, int M, int N, int K, int act, bool grouped) {
     case kRows8: return tiles8(a, 16, 16) + 8 < (1LL << 32) / 256;
     case kSmall8: return tiles8<Small>(a) + 8 < (1LL << 32) / Small::NT;
     case kMid8: return tiles8<Mid>(a) + 8 < (1LL << 32) / Mid::NT;
-    default: return tiles8<Large>(a) + 8 < (1LL << 32) / Large::NT;
+    default:  // or, for gathered rows past 4 GiB, the 128 x 128 tiles
+      return big_tiles8(a) + 8 < (1LL << 32) / 512 && tiles8<Mid>(a) + 8 < (1LL << 32) / Mid::NT;
   }
 }
 
@@ -474,7 +445,7 @@ size_t linear_fp8_ws_bytes(int E, int M, int N, int K, int act, bool grouped) {
     case kRows8: return 0;
     case kSmall8: return part_bytes8<Small>(a, p.nks);
     case kMid8: return part_bytes8<Mid>(a, p.nks);
-    default: return part_bytes8<Large>(a, p.nks);
+    default: return 0;
   }
 }
 
@@ -492,7 +463,9 @@ hipError_t launch_linear_fp8(const void* x, const float* x_scale, const int32_t*
   f.a = args8(x, gather, gk, gT, offsets, E, M, N, K, act);
   f.a.w = w, f.a.bias = bias, f.a.res = res, f.a.y = y;
   f.xs = x_scale, f.ws = w_scale, f.xrows = gather ? gT : M;
-  const Fp8Plan p = plan8(f.a);
+  Fp8Plan p = plan8(f.a);
+  // gathered rows past the large tiles' 32-bit offsets: no workspace needed either
+  if (p.path == kLarge8 && !fp8_big_ok(f.a)) p = Fp8Plan{kMid8, 1};
   return host_gated(act) ? run8<true>(f, p, ws, s) : run8<false>(f, p, ws, s);
 }
 

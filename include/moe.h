@@ -552,7 +552,7 @@ size_t moe_linear_grouped_fp8_workspace_bytes(int E, int rows, int N, int K, int
 
 typedef enum {
   MOE_FP8_ROWS = 0,    /* few rows: weights straight to registers */
-  MOE_FP8_64X64 = 1,   /* tiles of 64 rows x 64 weight rows, K slices */
+  MOE_FP8_64X64 = 1,   /* tiles of 64 rows x 64 weight rows */
   MOE_FP8_128X128 = 2, /* tiles of 128 rows x 128 weight rows */
   MOE_FP8_256X256 = 3  /* tiles of 256 rows x 256 weight rows */
 } moe_fp8_path;

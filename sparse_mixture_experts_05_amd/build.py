@@ -24,7 +24,7 @@ PROBE_LIB = os.path.join(PKG, "libmoe_probe.so")
 
 SOURCES = ["route.hip", "dispatch.hip", "ffn.hip", "combine.hip", "stats.hip", "bias.hip",
            "norm.hip", "route_grouped.hip", "linear.hip", "linear_big.hip",
-           "quantize.hip", "linear_fp8.hip", "linear_fp8_big.hip", "few.hip", "moe_api.cpp"]
+           "quantize.hip", "linear_fp8.hip", "linear_fp8_tiles.hip", "few.hip", "moe_api.cpp"]
 PROBE_SOURCES = ["probe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -74,7 +74,8 @@ hipError_t launch_quantize(const void* x, int rows, int K, bool bf16, void* q, f
 hipError_t launch_quantize_weight(const void* w, int count, int N, int K, bool bf16, void* q,
                                   float* scale, hipStream_t s);
 
-bool linear_fp8_fits(int E, int M, int N, int K, int act, bool grouped);
+// gather_rows: rows that perm gathers from (0: none).
+bool linear_fp8_fits(int E, int M, int N, int K, int act, bool grouped, int gather_rows);
 size_t linear_fp8_ws_bytes(int E, int M, int N, int K, int act, bool grouped);
 int linear_fp8_path(int E, int M, int N, int K, int act, bool grouped, int* slices);
 hipError_t launch_linear_fp8(const void* x, const float* x_scale, const int32_t* gather, int gk,

@@ -37,9 +37,12 @@ __device__ __forceinline__ void fma4(f32x4_t& acc, float s, const f32x4_t& p) {
   for (int c = 0; c < 4; ++c) acc[c] = fmaf(s, p[c], acc[c]);
 }
 
-// 256 x 256 tiles (linear_fp8_big.hip), dense or grouped, whole K.
-bool fp8_big_ok(const LinArgs& a);  // its offsets fit the kernel's addressing
-hipError_t launch_fp8_big(const Fp8Args& f, unsigned grid, hipStream_t s);
+constexpr int kMaxSlices8 = 16;
+
+// Square tiles of 64, 128 or 256 rows (linear_fp8_tiles.hip), dense or grouped, K in nks
+// slices (their partial tiles in a.part).
+bool fp8_tiles_ok(const LinArgs& a);  // the offsets fit the kernel's addressing
+hipError_t launch_fp8_tiles(const Fp8Args& f, int rows, int nks, unsigned grid, hipStream_t s);
 
 }  // namespace lin
 }  // namespace moe

@@ -425,11 +425,11 @@ int check_quantize(int count, int N, int K, int dtype, const void* x, const void
   return overlap_any(q, n, {sx, ss}) || overlap_any(scale, ss.n, {sx}) ? MOE_ERR_INVALID_ARG : MOE_OK;
 }
 
-int check_linear_fp8(int E, int M, int N, int K, int act, bool grouped) {
+int check_linear_fp8(int E, int M, int N, int K, int act, bool grouped, int gather_rows = 0) {
   if (E < 1 || M < 1 || N < 1 || K < 1 || act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU)
     return MOE_ERR_INVALID_ARG;
   if (E > kMaxExperts || N % 64 != 0 || K % 128 != 0) return MOE_ERR_UNSUPPORTED;
-  return moe::linear_fp8_fits(E, M, N, K, act, grouped) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+  return moe::linear_fp8_fits(E, M, N, K, act, grouped, gather_rows) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
 int run_linear_fp8(const void* x, const float* x_scale, const int32_t* perm, int k, int T,
@@ -500,7 +500,7 @@ int moe_linear_grouped_fp8(const void* x, const float* x_scale, const int32_t* p
                            const float* w_scale, const void* bias, int act, const void* residual,
                            int N, int K, void* y, void* ws, size_t ws_bytes, void* stream) {
   if (!x || !x_scale || !offsets || !w || !w_scale || !y) return MOE_ERR_INVALID_ARG;
-  const int st = check_linear_fp8(E, rows, N, K, act, true);
+  const int st = check_linear_fp8(E, rows, N, K, act, true, perm && T > 0 ? T : 0);
   if (st != MOE_OK) return st;
   if (perm) {
     if (T < 1 || k < 1) return MOE_ERR_INVALID_ARG;

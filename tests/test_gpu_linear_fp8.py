@@ -195,7 +195,8 @@ def test_overlapping_offsets_stay_in_the_workspace():
     """Offsets that go back and forth name more tiles than rows can have; no K slice's
     partial tile may land past the workspace."""
     print("\n[gpu] grouped_fp8 overlapping offsets", flush=True)
-    E, rows, N, K = 4, 96, 192, 8192
+    E, rows, N, K = 4, 600, 192, 8192
+    assert moe.moe_linear_fp8_path(rows, N, K, "none", E)[1] > 1
     x, xs = rows8(rows, K, 1)
     w, ws = weight8((E,), N, K, 2)
     off = torch.tensor([0, rows] * (E // 2) + [rows], dtype=torch.int32, device="cuda")

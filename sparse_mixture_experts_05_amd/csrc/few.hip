@@ -1,27 +1,37 @@
-// A whole MoE layer for a few tokens (T <= 64) in two launches: scores, then choice,
-// experts, shared expert and combine. A decode step is a stream of the chosen experts'
-// weights; what the layer's separate launches cost there is their drains and starts.
+// A whole MoE layer for a few tokens (T <= 64): a launch for the scores, from 9 tokens on
+// one for the choice, and one for choice (up to 8 tokens), experts, shared expert and
+// combine. A decode step is a stream of the chosen experts' weights; what the layer's
+// separate launches cost there is their drains and starts.
 //
 //   s[t,e]  = x[t] . wg[e] (+ bias[e])                    top-k as moe_route_grouped
 //   h[t,j]  = act(x[t] . up[e_j]^T + b_up[e_j])           rounded to the layer's type
 //   out[t]  = sum_j w[t,j] (h[t,j] . down[e_j]^T + b_down[e_j])  + shared expert(x[t])
 //
-// The second launch chooses (every workgroup for itself: cheaper than handing it round) and
-// then has two kinds of tasks:
+// In the last launch every workgroup chooses for itself or loads the choice, and then has
+// two kinds of tasks:
 //   up    (unit, 16 weight rows of up: 16 columns of h, or 8 of a gated act), by ticket
 //   down  (K slice, 16 columns of out) over all units, dealt out by workgroup
 // A down task waits until every up task is done. A workgroup starts on its down tasks only
 // when it has drawn a ticket past the last up task, so by then every up task is held by a
 // workgroup that runs, and that waits for nothing before it is through with its tickets:
 // the wait ends whatever number of workgroups is resident and whatever else the GPU runs.
-// (It ends after a second in any case: in a workspace that another call is using results
-// are wrong, and nothing hangs.)
+// (It gives up after some seconds, and out is NaN then: so a workspace that another call is
+// using at the same time does not hang the GPU.)
 //
 // The pairs (token, chosen expert) are sorted by expert in every workgroup's LDS; up to 16
 // pairs of an expert make a unit, the columns of one MFMA tile, and the shared expert has
 // units of 16 tokens. Weights go straight to registers (nothing else on the chip reads
 // them); the first steps of a task are loaded while the task before it is summed up and
 // stored, those of the down weights while the last up tasks are waited for.
+//
+// Bound by HBM (T = 64 reads 5.8 TB/s of weights) and, for a token or two, by the launches'
+// starts, the choice and the wait between up and down (22 of 1 token's 56 us). bf16, eager,
+// cold weights, against the separate calls (route, dispatch, products, combine) in a graph:
+//   1 token, 128 experts of 4096 x 1536 swiglu, 8 chosen, one shared   75 us (108)
+//   16 tokens, 128 experts of 4096 x 1024 gelu, 8 chosen              222 us (270)
+//   64 tokens, 128 experts of 4096 x 1024 swiglu, 8 chosen            548 us (559)
+// 4 steps in flight a wave (R): 2, 3, 5, 6, 8, 12 and 16 are slower by 1 to 20 % (1 token of
+// gelu 58.3 us; 62.7, 62.0, 64.9, 60.1, 61.6, 70.6, 69.0), as are two workgroups a CU (70.7).
 #include <algorithm>
 
 #include "kernels.hpp"
@@ -65,7 +75,7 @@ inline int counter_ints(int H) { return kArrived + H / kCols; }
 
 // 16 experts x 16 tokens x a slice of H a workgroup of 4 waves, which share the slice (64
 // bytes of a row a step) and add their sums in wave order. Clears the counters of the
-// second launch. The slices spread Wg over the CUs: one CU reads about 55 GB/s.
+// last launch. The slices spread Wg over the CUs: one CU reads about 55 GB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void few_scores_kernel(const T* __restrict__ x, const T* __restrict__ wg,
                                                         int nT, int H, int E, float* __restrict__ scores,
@@ -134,13 +144,16 @@ __device__ __forceinline__ unsigned announce(unsigned* p) {
   return __builtin_amdgcn_readfirstlane(before);
 }
 
-// Waits until *p is set, a second at most (100 ticks of this clock a microsecond).
-__device__ __forceinline__ void wait_set(const unsigned* p) {
-  const unsigned long long start = wall_clock64();
-  while (__hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0) {
+// Waits until *p is set; false if it has not been after kLooks looks, of about a
+// microsecond each. Looks and not time: a workgroup that the GPU has put aside for
+// another process does not look.
+constexpr int kLooks = 1 << 22;
+__device__ __forceinline__ bool wait_set(const unsigned* p) {
+  for (int i = 0; i < kLooks; ++i) {
+    if (__hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0) return true;
     __builtin_amdgcn_s_sleep(4);
-    if (wall_clock64() - start > 100000000ull) break;
   }
+  return false;
 }
 
 // ----------------------------------------------------------------- the stream
@@ -150,7 +163,9 @@ __device__ __forceinline__ void wait_set(const unsigned* p) {
 struct Rows {
   const uint8_t* w;
   uint32_t lane;
-  int steps;  // of 64 bytes a row
+  int steps;   // of 64 bytes a row
+  int stride;  // bytes from one to the next
+  __device__ __forceinline__ const uint8_t* at(int s) const { return w + (size_t)s * stride; }
 };
 
 // R steps of the weights and of the columns, in flight or landed.
@@ -166,7 +181,7 @@ __device__ __forceinline__ void first_steps(Ring<R>& g, const Rows& w, Col col) 
 #pragma unroll
   for (int u = 0; u < R; ++u) {  // in the order of their use
     const int s = min(u, max(w.steps - 1, 0));
-    g.w[u] = ld16(w.w + (size_t)s * 64 + w.lane);
+    g.w[u] = ld16(w.at(s) + w.lane);
     g.c[u] = col(s);
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -174,7 +189,7 @@ __device__ __forceinline__ void first_steps(Ring<R>& g, const Rows& w, Col col) 
 template <int R>
 __device__ __forceinline__ void first_rows(Ring<R>& g, const Rows& w) {
 #pragma unroll
-  for (int u = 0; u < R; ++u) g.w[u] = ld16(w.w + (size_t)min(u, max(w.steps - 1, 0)) * 64 + w.lane);
+  for (int u = 0; u < R; ++u) g.w[u] = ld16(w.at(min(u, max(w.steps - 1, 0))) + w.lane);
 }
 template <int R, typename Col>
 __device__ __forceinline__ void first_cols(Ring<R>& g, int steps, Col col) {
@@ -199,7 +214,7 @@ __device__ __forceinline__ f32x4_t stream(Ring<R>& g, const Rows& w, const Rows&
       acc = mma16<T>(live ? g.w[u] : zero, live ? g.c[u] : zero, acc);
       const bool more = b + u + R < S;
       const int s = more ? b + u + R : min(u, last);
-      const uint8_t* base = (more ? w.w : next.w) + (size_t)s * 64;
+      const uint8_t* base = more ? w.at(s) : next.at(s);
       g.w[u] = ld16(base + (more ? w.lane : next.lane));
       g.c[u] = col(s, !more);
       __builtin_amdgcn_sched_barrier(0);  // loads stay in the order of their use
@@ -231,9 +246,42 @@ struct FewLds {
   int units, start[2], ticket[2];  // a workgroup's first two tickets, then every next one in turn
 };
 
-// The choice of every token; the pairs in the experts' order, and the units: the shared
-// expert's, then each expert's. One wave a token, for itself, then one thread a pair.
-// The wave that finishes tasks draws the workgroup's first two tickets meanwhile, the
+// The scores of token t, expert i * 64 + lane, summed in slice order.
+template <int EPX>
+__device__ __forceinline__ void sum_scores(const FewArgs& a, int t, float* row) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < EPX / 64; ++i) {
+    const int e = min(i * 64 + lane, a.E - 1);
+    float v[kMaxScore];
+#pragma unroll
+    for (int q = 0; q < kMaxScore; ++q) v[q] = a.scores[((size_t)min(q, a.KS - 1) * a.T + t) * a.E + e];
+    float s = v[0];
+#pragma unroll
+    for (int q = 1; q < kMaxScore; ++q)
+      if (q < a.KS) s += v[q];
+    row[i * 64 + lane] = a.bias != nullptr ? s + a.bias[e] : s;
+  }
+}
+
+// The choice as a launch of its own, a token a workgroup of one wave, for more than kOwn
+// tokens: the workgroups of the last launch choose up to kOwn, a token a wave, in what
+// the launch costs (6 us), but take a wave's tokens one after another (5.5 us a token:
+// 16 tokens 17 us, 64 49).
+constexpr int kOwn = kWaves;
+template <int EPX>
+__global__ __launch_bounds__(64) void few_choice_kernel(FewArgs a) {
+  __shared__ float sc[tile_stride<1, 1>()];
+  __shared__ GroupLds<1, 1> g;
+  const int t = blockIdx.x;
+  sum_scores<EPX>(a, t, sc);
+  wave_lds_fence();
+  grouped_phase<1, EPX, 1>(sc, g, a.g, t, a.T, a.E, a.k, a.idx, a.w);
+}
+
+// The choice of every token, or its loads; the pairs in the experts' order, and the units:
+// the shared expert's, then each expert's. One wave a token, for itself, then one thread a
+// pair. The wave that finishes tasks draws the workgroup's first two tickets meanwhile, the
 // second when every workgroup has its first.
 __device__ __forceinline__ int draw_ticket(const FewArgs& a) {
   return (int)__hip_atomic_fetch_add(a.counters, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -244,24 +292,11 @@ __device__ __forceinline__ void choose(const FewArgs& a, FewLds& L) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const bool drawer = tid == kWaves * 64;
   if (drawer) L.start[0] = draw_ticket(a);
-  for (int t = wave; t < a.T && wave < kWaves; t += kWaves) {
-    float* row = L.choice.sc + wave * L.S;
-#pragma unroll
-    for (int i = 0; i < EPX / 64; ++i) {
-      const int e = min(i * 64 + lane, a.E - 1);
-      float v[kMaxScore];
-#pragma unroll
-      for (int q = 0; q < kMaxScore; ++q) v[q] = a.scores[((size_t)min(q, a.KS - 1) * a.T + t) * a.E + e];
-      float s = v[0];
-#pragma unroll
-      for (int q = 1; q < kMaxScore; ++q)
-        if (q < a.KS) s += v[q];
-      row[i * 64 + lane] = a.bias != nullptr ? s + a.bias[e] : s;
-    }
+  const bool own = a.T <= kOwn;
+  if (own && wave < a.T) {
+    sum_scores<EPX>(a, wave, L.choice.sc + wave * L.S);
     wave_lds_fence();
-    grouped_phase<kWaves, EPX, kWaves>(L.choice.sc, L.choice.g, a.g, t - wave, a.T, a.E, a.k, L.choice.idx,
-                                       L.choice.w);
-    wave_lds_fence();
+    grouped_phase<kWaves, EPX, kWaves>(L.choice.sc, L.choice.g, a.g, 0, a.T, a.E, a.k, L.choice.idx, L.choice.w);
   }
   for (int i = tid; i < kWaves * kMaxE; i += kWaves * 64) (&L.choice.count[0][0])[i] = 0;
   lds_barrier();
@@ -273,9 +308,9 @@ __device__ __forceinline__ void choose(const FewArgs& a, FewLds& L) {
   int e = 0, rank = 0;
   float w = 0.0f;
   if (pair) {
-    e = L.choice.idx[tid];
-    w = L.choice.w[tid];
-    if (blockIdx.x == 0) a.idx[tid] = e, a.w[tid] = w;
+    e = own ? L.choice.idx[tid] : a.idx[tid];
+    w = own ? L.choice.w[tid] : a.w[tid];
+    if (own && blockIdx.x == 0) a.idx[tid] = e, a.w[tid] = w;
     unsigned long long same = __ballot(true);
 #pragma unroll
     for (int bit = 0; bit < 8; ++bit) {
@@ -347,7 +382,7 @@ __device__ __forceinline__ void store4(T* row, const f32x4_t& v) {
 // draws the tickets while the streams go on with the next task.
 template <typename T, int EPX>
 __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
-  constexpr int R = 8;
+  constexpr int R = 4;
   constexpr int ES = (int)sizeof(T);
   __shared__ FewLds L;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -403,7 +438,7 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
       turn ^= 1;
     }
     if (task >= ndown) return;
-    wait_set(a.counters + (2 + blockIdx.x % kGo) * kLine);
+    const bool done = wait_set(a.counters + (2 + blockIdx.x % kGo) * kLine);
     lds_barrier();
     for (turn = 0; task < ndown; task += gridDim.x, turn ^= 1) {
       lds_barrier();
@@ -418,6 +453,7 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
         v[i] = *reinterpret_cast<const f32x4_t*>(&L.out[turn][0][t][c]);
 #pragma unroll
         for (int q = 1; q < kWaves; ++q) v[i] += *reinterpret_cast<const f32x4_t*>(&L.out[turn][q][t][c]);
+        if (!done) v[i] = f32x4_t{NAN, NAN, NAN, NAN};
       }
       if (a.D > 1) {
         // the slice that arrives last adds all of them up, in slice order
@@ -451,7 +487,12 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
   }
 
   // the streams
-  const int SH = H * ES / 64, lo = wave * SH / kWaves, hi = (wave + 1) * SH / kWaves;
+  // The steps of an up task go round the waves, so that what the workgroups read at one
+  // time lies anywhere in the rows: with a slice of a row each (1 KiB of 4096 bf16), all
+  // were at addresses with the same bits 6 to 9, which some of the HBM channels hold (64
+  // tokens of 128 experts 645 -> 587 us, 1 token 78.5 -> 75.3; 128 bytes at a time 640).
+  const int SH = H * ES / 64, lo = min(wave, SH - 1), mine = (SH - wave + kWaves - 1) / kWaves;
+  auto x_step = [&](int s) { return (lo + s * kWaves) * 64; };
   struct Up {
     Rows rows;
     uint32_t col;  // the lane's row of x
@@ -465,7 +506,8 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
     // with a gate, 8 gate rows and the 8 up rows of the same columns
     const uint32_t row = gt ? (l16 & 7) + (l16 >> 3) * N : l16;
     u.rows.lane = row * (uint32_t)(H * ES) + kq * 16;
-    u.rows.steps = hi - lo;
+    u.rows.steps = mine;  // none if the row is that short
+    u.rows.stride = kWaves * 64;
     const int p = L.first[k.unit] + min(l16, L.pairs[k.unit] - 1);
     u.col = (uint32_t)((e < 0 ? p : L.tok[p]) * H * ES + kq * 16);
     return u;
@@ -489,6 +531,7 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
     const int first = sh ? p.unit * SS : su * SS + (p.unit - su) * SF, K = sh ? Fs : F;
     const int e = uni(L.expert[p.unit]);
     p.s = s0, p.n0 = n0;
+    p.rows.stride = 64;
     p.rows.steps = max(0, min(end, first + (sh ? SS : SF)) - s0);
     p.first = s == first;
     p.at = (uint32_t)(s - first) * 64;
@@ -511,14 +554,14 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
   int turn = 0;
   if (t0 < nup) {
     Up u = up(t0);
-    first_steps(ring, u.rows, [&](int s) { return __builtin_amdgcn_raw_buffer_load_b128(xb, u.col, (lo + s) * 64, 0); });
+    first_steps(ring, u.rows, [&](int s) { return __builtin_amdgcn_raw_buffer_load_b128(xb, u.col, x_step(s), 0); });
     while (t0 < nup) {
       const bool more = t1 < nup;  // else the down weights, whose rows of h are not there yet
       Up n;
       n.rows = p.rows, n.col = 0;
       if (more) n = up(t1);
       L.red[turn][wave][lane] = stream<T>(ring, u.rows, n.rows, [&](int s, bool next) {
-        return __builtin_amdgcn_raw_buffer_load_b128(xb, next ? n.col : u.col, next && !more ? 0 : (lo + s) * 64, 0);
+        return __builtin_amdgcn_raw_buffer_load_b128(xb, next ? n.col : u.col, next && !more ? 0 : x_step(s), 0);
       });
       lds_barrier();
       t0 = t1;
@@ -615,10 +658,19 @@ hipError_t launch_few_t(const FewArgs& a, const void* wg, hipStream_t s) {
   const long long tasks = (long long)std::min(a.E, a.T * a.k) * (a.F / chunk) + a.Fs / chunk +
                           (long long)(a.H / kCols) * a.D;
   const dim3 grid((unsigned)std::min(tasks, 256LL)), block((kWaves + 1) * 64);
-  if (a.E <= 64) hipLaunchKernelGGL((few_kernel<T, 64>), grid, block, 0, s, a);
-  else if (a.E <= 128) hipLaunchKernelGGL((few_kernel<T, 128>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((few_kernel<T, kMaxE>), grid, block, 0, s, a);
-  return hipGetLastError();
+  auto choose_and_run = [&](auto epx) {
+    constexpr int EPX = decltype(epx)::value;
+    if (a.T > kOwn) {
+      hipLaunchKernelGGL((few_choice_kernel<EPX>), dim3(a.T), dim3(64), 0, s, a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((few_kernel<T, EPX>), grid, block, 0, s, a);
+    return hipGetLastError();
+  };
+  if (a.E <= 64) return choose_and_run(std::integral_constant<int, 64>{});
+  if (a.E <= 128) return choose_and_run(std::integral_constant<int, 128>{});
+  return choose_and_run(std::integral_constant<int, kMaxE>{});
 }
 
 }  // namespace

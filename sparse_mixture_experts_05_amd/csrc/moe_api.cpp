@@ -524,6 +524,7 @@ int moe_linear_fp8_path(int E, int rows, int N, int K, int act, int grouped, int
 namespace {
 
 constexpr int kMaxFewSize = 1 << 20;
+constexpr int kFewRows = 16;  // weight rows that a task reads side by side
 
 int check_few(int T, int H, int E, int k, int F, int Fs, int dtype) {
   if (T < 1 || F < 1 || Fs < 0 || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
@@ -561,6 +562,8 @@ int moe_layer_few(const void* x, const void* wg, const float* bias, int bias_mod
     if (!aligned_or_null(p)) return MOE_ERR_INVALID_ARG;
   const size_t b = elem(dtype), two = act == MOE_ACT_GEGLU || act == MOE_ACT_SWIGLU ? 2 : 1;
   const size_t e = (size_t)E, t = (size_t)T;
+  // a lane's offset of gate and up rows has 32 bits
+  if (two == 2 && ((size_t)(F > Fs ? F : Fs) + kFewRows) * H * b > UINT32_MAX) return MOE_ERR_UNSUPPORTED;
   const Span in[] = {{x, t * H * b}, {wg, e * H * b}, {bias, e * 4}, {w_up, e * two * F * H * b},
                      {w_down, e * H * F * b}, {b_up, e * two * F * b}, {b_down, e * H * b},
                      {ws_up, two * Fs * H * b}, {ws_down, (size_t)H * Fs * b}};

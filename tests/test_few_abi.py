@@ -86,3 +86,17 @@ def test_binding_refuses(i):
     text, call = BAD[i]
     with pytest.raises(ValueError, match=text):
         call()
+
+
+def test_gate_halves_of_4_gib():
+    """A lane's offset of the gate and up rows has 32 bits: up to (F + 16) * H elements."""
+    far = dict(x=ctypes.c_void_p(1 << 20), wg=ctypes.c_void_p(1 << 24), up=ctypes.c_void_p(1 << 44),
+               down=ctypes.c_void_p(1 << 45), bu=None, bd=None, su=None, sd=None, bias=None, Fs=0,
+               out=ctypes.c_void_p(1 << 28), idx=ctypes.c_void_p(1 << 29), w=ctypes.c_void_p(1 << 30), n=0)
+    big = dict(H=1 << 15, F=1 << 16)  # 4 GiB in bf16
+    assert few(**far, **big) == -2
+    assert few(**far, **dict(big, F=(1 << 16) - 64)) == -3  # accepted, up to the workspace
+    assert few(**far, **dict(big, F=1 << 15, dt=0)) == -2
+    assert few(**far, **dict(big, act=1)) == -3             # no gate: one row's offset only
+    wide = dict(far, Fs=1 << 16, su=ctypes.c_void_p(1 << 46), sd=ctypes.c_void_p(1 << 47))
+    assert few(**wide, H=1 << 15, F=64) == -2               # the shared expert's

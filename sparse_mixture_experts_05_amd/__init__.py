@@ -8,7 +8,10 @@ reading token rows through the permutation, with no copy of them); and moe_bias_
 dynamic routing-bias step that feeds the next layer call. Around the layer, for
 a whole decoder block: moe_norm, moe_norm_residual, moe_route_grouped,
 moe_linear and moe_linear_grouped, run together by moe_block_forward and
-MoEBlockGraph. Every step runs in the HIP kernels; this package only marshals tensors, sizes and the current stream.
+MoEBlockGraph. In 8 bits: moe_quantize, moe_quantize_weight, moe_linear_fp8 and
+moe_linear_grouped_fp8; moe_layer_few is the whole layer for up to 64 tokens in two
+or three launches (moe_block_forward takes both as options). Every step runs in the HIP kernels;
+this package only marshals tensors, sizes and the current stream.
 """
 from .binding import (MoEBlockGraph, MoEError, MoELayerGraph, lib, moe_block_forward, moe_bias_update, moe_capacity, moe_combine,
                       moe_dispatch, moe_dispatch_noalloc, moe_expert_ffn, moe_expert_ffn_gather,

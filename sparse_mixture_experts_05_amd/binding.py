@@ -1055,7 +1055,7 @@ def moe_layer_few(x, wg, bias, w_up, w_down, k: int, score: str = "softmax",
                   group_top: int = 2, renorm: bool = True, scale: float = 1.0, act: str = "gelu",
                   b_up=None, b_down=None, ws_up=None, ws_down=None, out=None, topk_idx=None,
                   topk_w=None, ws=None, stream=None):
-    """The whole layer for a few tokens (x [T,H], T <= 64) in two launches: routing,
+    """The whole layer for a few tokens (x [T,H], T <= 64) in two or three launches: routing,
     experts, shared expert and combine.
 
     Routing as moe_route_grouped; bias (fp32 [E] or None) moves the choice only
@@ -1113,7 +1113,8 @@ def moe_block_forward(h, wg, w_up, w_down, k: int, x=None, norm_weight=None, nor
                       act: str = "swiglu", b_up=None, b_down=None, ws_up=None, ws_down=None,
                       capacity=None, out_norm: str = "none", out_weight=None, out_bias=None,
                       gate=None, res_scale: float = 1.0, next_norm: str = "none",
-                      next_weight=None, next_bias=None, stream=None):
+                      next_weight=None, next_bias=None, stream=None, few: bool = False,
+                      w_up_scale=None, w_down_scale=None, ws_up_scale=None, ws_down_scale=None):
     """A whole MoE block of a decoder on the residual stream h [T,H], on one stream
     without host synchronisation:
 
@@ -1128,10 +1129,31 @@ def moe_block_forward(h, wg, w_up, w_down, k: int, x=None, norm_weight=None, nor
     [E,2,F], b_down [E,H]; ws_up, ws_down the same without E (no biases): the
     always-on shared expert. capacity (int) drops each expert's assignments past
     it. Returns a dict: res, next, and the steps' x, topk_idx, topk_w, counts,
-    offsets, perm, inv, out."""
+    offsets, perm, inv, out.
+
+    few=True runs route, experts and combine as moe_layer_few (T <= 64, no capacity; out
+    sums the experts' rows before they are rounded); counts, offsets, perm and inv are
+    not made then.
+
+    With w_up_scale and w_down_scale (moe_quantize_weight's, float8_e4m3fn weights, bf16 h
+    and biases) the experts' products are moe_linear_grouped_fp8 of x and of the
+    activated rows through moe_quantize; H and F are multiples of 128. ws_up_scale and
+    ws_down_scale the same for the shared expert (moe_linear_fp8); each pair is given
+    whole or not at all, and neither with few."""
     if (ws_up is None) != (ws_down is None):
         raise ValueError("the shared expert needs ws_up and ws_down")
     _dims(h, "h", 2)
+    for up, down, name in ((w_up_scale, w_down_scale, "w"), (ws_up_scale, ws_down_scale, "ws")):
+        if (up is None) != (down is None):
+            raise ValueError(f"8-bit experts need {name}_up_scale and {name}_down_scale")
+        if up is not None and few:
+            raise ValueError("few takes no 8-bit experts")
+        if up is not None and h.dtype != torch.bfloat16:
+            raise ValueError(f"h must be torch.bfloat16 with 8-bit experts, got {h.dtype}")
+    if ws_up_scale is not None and ws_up is None:
+        raise ValueError("ws_up_scale without a shared expert")
+    if few and capacity is not None:
+        raise ValueError("few takes no capacity")
     other = _other_stream(h.device, stream)
     if other is not None:
         with torch.cuda.stream(other):
@@ -1139,21 +1161,37 @@ def moe_block_forward(h, wg, w_up, w_down, k: int, x=None, norm_weight=None, nor
                                      route_bias, score, groups, topk_groups, group_top, renorm,
                                      scale, act, b_up, b_down, ws_up, ws_down, capacity, out_norm,
                                      out_weight, out_bias, gate, res_scale, next_norm, next_weight,
-                                     next_bias)
+                                     next_bias, None, few, w_up_scale, w_down_scale, ws_up_scale,
+                                     ws_down_scale)
     if x is None:
         x = moe_norm(h, norm_weight, norm_bias, eps, norm)
-    idx, w = moe_route_grouped(x, wg, route_bias, k, score, groups, topk_groups, group_top, renorm,
-                               scale)
-    d = moe_dispatch(idx, x, wg.shape[0], capacity=capacity, gather=False)
-    a = moe_linear_grouped(x, d["offsets"], w_up, b_up, act, perm=d["perm"], k=k)
-    ys = moe_linear_grouped(a, d["offsets"], w_down, b_down)
-    ysh = None
-    if ws_up is not None:
-        ysh = moe_linear(moe_linear(x, ws_up, act=act), ws_down)
-    out = moe_combine(ys, d["inv"], w, ysh)
+    if few:
+        out, idx, w = moe_layer_few(x, wg, route_bias, w_up, w_down, k, score, "choice", groups,
+                                    topk_groups, group_top, renorm, scale, act, b_up, b_down, ws_up,
+                                    ws_down)
+        d = {}
+    else:
+        idx, w = moe_route_grouped(x, wg, route_bias, k, score, groups, topk_groups, group_top, renorm,
+                                   scale)
+        d = moe_dispatch(idx, x, wg.shape[0], capacity=capacity, gather=False)
+        if w_up_scale is not None or ws_up_scale is not None:
+            x8 = moe_quantize(x)
+        if w_up_scale is not None:
+            a = moe_linear_grouped_fp8(*x8, d["offsets"], w_up, w_up_scale, b_up, act, perm=d["perm"], k=k)
+            ys = moe_linear_grouped_fp8(*moe_quantize(a), d["offsets"], w_down, w_down_scale, b_down)
+        else:
+            a = moe_linear_grouped(x, d["offsets"], w_up, b_up, act, perm=d["perm"], k=k)
+            ys = moe_linear_grouped(a, d["offsets"], w_down, b_down)
+        ysh = None
+        if ws_up_scale is not None:
+            ysh = moe_linear_fp8(*x8, ws_up, ws_up_scale, act=act)
+            ysh = moe_linear_fp8(*moe_quantize(ysh), ws_down, ws_down_scale)
+        elif ws_up is not None:
+            ysh = moe_linear(moe_linear(x, ws_up, act=act), ws_down)
+        out = moe_combine(ys, d["inv"], w, ysh)
+        del d["xs"]
     res, nxt = moe_norm_residual(out, h, out_weight, out_bias, gate, res_scale, eps, out_norm,
                                  next_weight, next_bias, next_norm)
-    del d["xs"]
     return dict(res=res, next=nxt, x=x, topk_idx=idx, topk_w=w, out=out, **d)
 
 

@@ -32,8 +32,11 @@ using namespace lin;
 
 // Decode: up to 16 rows of one segment and 16 output columns a workgroup, the weights
 // straight from memory to registers; as lin_rows_kernel (linear.hip), with a block of K a
-// step: lane l loads 32 bytes of weight row l % 16 and of x row l % 16. The 4 waves share
-// the blocks of K in turn; their sums are added in wave order through LDS.
+// step: lane l loads 32 bytes of weight row l % 16 and of x row l % 16. The blocks of K go
+// round the 4 waves (with a slice of K a wave, the workgroups read more often from the same
+// HBM channels at one time: 81 of 128 experts 2048 x 4096 126 -> 121 us); their sums are
+// added in wave order through LDS. Bound by HBM: 5.6 TB/s of weights there, and by a
+// launch's start below some 50 MB (8 x 4096 x 4096: 8 us, of which its bytes take 3).
 template <bool GT>
 __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args f) {
   constexpr int KQ = 4, U = 2, H = GT ? 2 : 1;
@@ -44,7 +47,7 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args f) {
   const int N = a.N, K = a.K;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int S = K / kBlock8;
-  const int s0 = wave * S / KQ, s1 = (wave + 1) * S / KQ;
+  const int mine = (S - wave + KQ - 1) / KQ;  // blocks wave, wave + KQ, ...
   const uint8_t* wp[H];
   const float* wsp[H];
 #pragma unroll
@@ -64,19 +67,21 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args f) {
     float ws[H], xs;
   };
   Step p[U], q[U];
+  auto one_load = [&](Step& d, int s) {
+    const size_t b = (size_t)s * KQ + wave;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      d.w[h][0] = ld16(wp[h] + b * kBlock8);
+      d.w[h][1] = ld16(wp[h] + b * kBlock8 + 64);
+      d.ws[h] = wsp[h][b];
+    }
+    d.x[0] = ld16(xp + b * kBlock8);
+    d.x[1] = ld16(xp + b * kBlock8 + 64);
+    d.xs = xsp[b * f.xrows];
+  };
   auto load = [&](Step (&d)[U], int s) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        d[u].w[h][0] = ld16(wp[h] + (size_t)(s + u) * kBlock8);
-        d[u].w[h][1] = ld16(wp[h] + (size_t)(s + u) * kBlock8 + 64);
-        d[u].ws[h] = wsp[h][s + u];
-      }
-      d[u].x[0] = ld16(xp + (size_t)(s + u) * kBlock8);
-      d[u].x[1] = ld16(xp + (size_t)(s + u) * kBlock8 + 64);
-      d[u].xs = xsp[(size_t)(s + u) * f.xrows];
-    }
+    for (int u = 0; u < U; ++u) one_load(d[u], s + u);
   };
   auto one = [&](const Step& d) {
 #pragma unroll
@@ -87,34 +92,26 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args f) {
 #pragma unroll
     for (int u = 0; u < U; ++u) one(d[u]);
   };
-  int s = s0;
-  if (s + U <= s1) {
+  int s = 0;
+  if (s + U <= mine) {
     load(p, s);
     for (;;) {
       s += U;
-      const bool more = s + U <= s1;
+      const bool more = s + U <= mine;
       if (more) load(q, s);
       mma(p);
       if (!more) break;
       s += U;
-      const bool again = s + U <= s1;
+      const bool again = s + U <= mine;
       if (again) load(p, s);
       mma(q);
       if (!again) break;
     }
   }
-  if (s < s1) {  // one block is left (U = 2)
+  if (s < mine) {  // one block is left (U = 2)
     static_assert(U == 2, "the rest is one block");
     Step d;
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      d.w[h][0] = ld16(wp[h] + (size_t)s * kBlock8);
-      d.w[h][1] = ld16(wp[h] + (size_t)s * kBlock8 + 64);
-      d.ws[h] = wsp[h][s];
-    }
-    d.x[0] = ld16(xp + (size_t)s * kBlock8);
-    d.x[1] = ld16(xp + (size_t)s * kBlock8 + 64);
-    d.xs = xsp[(size_t)s * f.xrows];
+    one_load(d, s);
     one(d);
   }
   if (wave != 0) {

@@ -41,8 +41,7 @@ template <int BM_, int BN_, int WM_, int NS_>
 struct Tile8 {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = BN / 64, NW = WM * WN;
   static constexpr int STAGES = NS_;                 // of the ring in LDS
-  static constexpr int WROWS = BM / WM;              // rows of a wave
-  static constexpr int TM = WROWS / 16, TN = 4;
+  static constexpr int TM = BM / WM / 16, TN = 4;    // sub-tiles of a wave
   static constexpr int ROWB = kBlock8;               // bytes of a stage's row
   static constexpr int XB = BM * ROWB, WB = BN * ROWB;  // stage buffers of rows and weights
   static constexpr int SB = NW * 256;                // and of the rows' scales, more than once
@@ -51,6 +50,14 @@ struct Tile8 {
   static constexpr int PANEL = 1024 / BN;            // column tiles of an n-block of the tile order
   static_assert(TM % 2 == 0 && WI <= TN && XI <= TN && NW * 64 >= BM && BM % 64 == 0 && LDS <= 160 * 1024, "tile");
 };
+
+// First row of sub-tile i among those of the tile's first wave (wave wm: wm * 32 further on):
+// pairs of sub-tiles go round the WM waves, so that a segment's last, partial row tile
+// spreads over all of them.
+template <int WM>
+__device__ __forceinline__ constexpr int sub_row(int i) {
+  return i / 2 * WM * 32 + i % 2 * 16;
+}
 
 template <typename F, int... I>
 __device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
@@ -73,7 +80,7 @@ template <typename Sh, int ACT>
 __global__ __launch_bounds__(Sh::NW * 64, 2) void fp8_tile_kernel(Fp8Args f) {
   constexpr int BM = Sh::BM, BN = Sh::BN, TM = Sh::TM, TN = Sh::TN, WN = Sh::WN, NW = Sh::NW;
   constexpr int ROWB = Sh::ROWB, XB = Sh::XB, WB = Sh::WB, SB = Sh::SB, XI = Sh::XI, WI = Sh::WI;
-  constexpr int WROWS = Sh::WROWS, RING = Sh::STAGES, COPIES = XI + WI + 1;
+  constexpr int WM = Sh::WM, RING = Sh::STAGES, COPIES = XI + WI + 1;
   constexpr bool GT = ACT == kActGeglu || ACT == kActSwiglu;
   constexpr int H = GT ? 2 : 1;
   constexpr int BC = GT ? BN / 2 : BN;            // output columns of a tile
@@ -157,11 +164,10 @@ __global__ __launch_bounds__(Sh::NW * 64, 2) void fp8_tile_kernel(Fp8Args f) {
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const int sw = (lane >> 1) & 7;                 // (row >> 1) & 7 of every fragment row
   const int slot0 = (kq ^ sw) << 4, slot1 = ((4 + kq) ^ sw) << 4;
-  const int fx = (wm * WROWS + l16) * ROWB, fw = W0 + (wn * 64 + l16) * ROWB;
-  const int fs = S0 + (wm * WROWS + l16) * 4;
-  // sub-tile rows of this wave that hold data, in pairs: all of them except in a segment's
-  // last, partial row tile
-  const int nsub = __builtin_amdgcn_readfirstlane(min(TM / 2, max(0, (M - wm * WROWS + 31) / 32)));
+  const int fx = (wm * 32 + l16) * ROWB, fw = W0 + (wn * 64 + l16) * ROWB;
+  const int fs = S0 + (wm * 32 + l16) * 4;
+  // pairs of this wave's sub-tile rows that hold data: all except in a partial row tile
+  const int nsub = __builtin_amdgcn_readfirstlane(min(TM / 2, (M + (WM - 1 - wm) * 32 + 31) / (WM * 32)));
 
   auto main_loop = [&](auto ns_tag) {
     constexpr int NS = decltype(ns_tag)::value;
@@ -174,9 +180,9 @@ __global__ __launch_bounds__(Sh::NW * 64, 2) void fp8_tile_kernel(Fp8Args f) {
       wf[j][1] = ld16(smem + buf * WB + fw + j * 16 * ROWB + slot1);
     };
     auto read_x = [&](int buf, int i) {
-      xf[i & 1][0] = ld16(smem + buf * XB + fx + i * 16 * ROWB + slot0);
-      xf[i & 1][1] = ld16(smem + buf * XB + fx + i * 16 * ROWB + slot1);
-      sx[i & 1] = *reinterpret_cast<const float*>(smem + buf * SB + fs + i * 64);
+      xf[i & 1][0] = ld16(smem + buf * XB + fx + sub_row<WM>(i) * ROWB + slot0);
+      xf[i & 1][1] = ld16(smem + buf * XB + fx + sub_row<WM>(i) * ROWB + slot1);
+      sx[i & 1] = *reinterpret_cast<const float*>(smem + buf * SB + fs + sub_row<WM>(i) * 4);
     };
     // prologue: the stages that fill the ring but for the last one's weights
     static_for<RING - 1>([&](auto st) {
@@ -276,7 +282,7 @@ __global__ __launch_bounds__(Sh::NW * 64, 2) void fp8_tile_kernel(Fp8Args f) {
   if (gridDim.y > 1) {  // a K slice: fp8_reduce_kernel adds them up
 #pragma unroll
     for (int i = 0; i < TM; ++i)
-      if (wm * WROWS + i * 16 < M)
+      if (wm * 32 + sub_row<WM>(i) < M)
 #pragma unroll
         for (int j = 0; j < TN; ++j)
           *reinterpret_cast<f32x4_t*>(part8<Sh>(a, t, blockIdx.y, gridDim.y, i, j)) = acc[i][j];
@@ -285,7 +291,7 @@ __global__ __launch_bounds__(Sh::NW * 64, 2) void fp8_tile_kernel(Fp8Args f) {
   // lane: row l16 of each row sub-tile, columns 4 kq .. + 3 of each weight sub-tile
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int r = wm * WROWS + i * 16 + l16;
+    const int r = wm * 32 + sub_row<WM>(i) + l16;
     if (r >= M) continue;
 #pragma unroll
     for (int j = 0; j < (GT ? TN / 2 : TN); ++j) {
@@ -306,8 +312,8 @@ __global__ __launch_bounds__(Sh::NW * 64) void fp8_reduce_kernel(Fp8Args f, int 
   if (t.M == 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / Sh::WN, wn = wave % Sh::WN, i = blockIdx.y;
-  const int r = wm * Sh::WROWS + i * 16 + (lane & 15);
-  if (wm * Sh::WROWS + i * 16 >= t.M) return;
+  const int r0 = wm * 32 + sub_row<Sh::WM>(i), r = r0 + (lane & 15);
+  if (r0 >= t.M) return;
   f32x4_t acc[TN];
 #pragma unroll
   for (int j = 0; j < TN; ++j) {

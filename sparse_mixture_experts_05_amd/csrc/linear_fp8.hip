@@ -153,29 +153,32 @@ struct Fp8Plan {
 // Path of a product: the least estimated time, in us. The estimates hold what was measured
 // (graph replay, no act; M x N x K dense, then 64 experts with evenly drawn rows):
 //                        rows    64 (slices)   128 (slices)   256
-//   16 x 4096 x 4096      8.7     12.6 (8)      13.3 (8)       31
-//   32 x 4096 x 4096     12.3     12.4 (4)      13.4 (8)       32
-//   64 x 4096 x 4096     19.5     13.3 (4)      14.3 (8)       33
-//   128 x 4096 x 4096    34       16.4 (1)      17.4 (4)       36
-//   256 x 4096 x 4096    63       17.5 (1)      21.3 (4)       48
-//   512 x 4096 x 4096   121       20.4 (1)      26.8 (4)       48
-//   1024 x 4096 x 4096  238       35.6 (1)      28.1 (1)       48
-//   2048 x 4096 x 4096  473       59.4 (1)      40.1 (1)       50
-//   4096 x 4096 x 4096           115   (1)      71   (1)       61
-//   8192 x 4096 x 4096           224   (1)     136   (1)      116
-//   64 x 4096 x 14336    55       20.6 (4)      21.4 (8)      101
-//   512 x 4096 x 14336  413       54   (1)      45   (4)      137
-//   2048 x 4096 x 14336          219   (1)     128   (1)      160
-//   4096 x 4096 x 14336                        243   (1)      192
-//   E 64, 512 rows, 1024 x 2048   45   41 (1)   31   (1)       33
-//   E 64, 2048 rows, 1024 x 2048  99   41 (1)   32   (1)       35
-//   E 64, 4096 rows, 1024 x 2048 176   48 (1)   34   (1)       38
+//   16 x 4096 x 4096      8.5     12.1 (4)      12.9 (8)       25
+//   32 x 4096 x 4096     12.0     12.2 (4)      13.3 (8)       25
+//   64 x 4096 x 4096     19.1     13.4 (4)      15.2 (8)       27
+//   128 x 4096 x 4096    33       15.9 (1)      16.7 (4)       31
+//   256 x 4096 x 4096    62       16.0 (1)      20.8 (4)       49
+//   512 x 4096 x 4096   119       19.9 (1)      22.9 (1)       49
+//   1024 x 4096 x 4096  234       35.5 (1)      23.9 (1)       49
+//   2048 x 4096 x 4096  464       61   (1)      38   (1)       50
+//   4096 x 4096 x 4096           111   (1)      72   (1)       63
+//   8192 x 4096 x 4096           217   (1)     141   (1)      123
+//   64 x 4096 x 14336    55       20.3 (4)      22.4 (8)       78
+//   1024 x 4096 x 14336          107   (1)      68   (1)      139
+//   1024 x 14336 x 4096          101   (1)      69   (1)       60
+//   E 64, 256 rows, 1024 x 2048   40   38 (1)   30   (1)       31
+//   E 64, 4096 rows, 1024 x 2048 173   47 (1)   33   (1)       34
+//   E 64, 8192 rows, 1024 x 2048 318   68 (1)   56   (1)       39
+//   E 64, 32768 rows, 1024 x 2048     173 (1)  119   (1)      107
 // A stage is 128 k. Few-row kernel: a stream of the weights, and of the rows from L2 once for
-// every 16 columns (4.4 TB/s). 64-row tiles: 0.35 us a stage while a CU has one workgroup,
-// and 0.23 us a tile and CU from there on; 128-row tiles: 0.68 and 0.53 (0.6 past 4 rounds:
-// the power limit and more traffic). Slices add a launch (4 us) and their partials' round
-// trip. Launches bound by their weights stream them at 0.97 to 1.35 of a copy's time. 256-row tiles: one workgroup a CU, 1.25 us a stage on an idle chip, 1.62 on a full
-// one, and 4 us a round outside the stages.
+// every 16 columns (4.4 TB/s); 3.5 ns a workgroup where those are short. 64-row tiles: 0.32
+// us a stage while a CU has one workgroup, then 0.19 and 0.9 us outside the stages a tile and
+// CU (0.23 and 1.4 where segments' weights come from HBM); 128-row tiles: 0.48, then 0.45 and
+// 3 (0.53 and 4). Slices add a launch (4 us, with segments 5.5) and their partials' round
+// trip. Launches bound by their weights stream them at 0.97 to 1.35 of a copy's time. 256-row
+// tiles: one workgroup a CU, 1.25 us a stage on an idle chip, 1.62 on a full one, and 4 us a
+// round outside the stages. Over 80 shapes, drawn ones among them, the path taken is 1.2 %
+// off the fastest in the mean.
 Fp8Plan plan8(const LinArgs& a) {
   const double cols = (host_gated(a.act) ? 2.0 : 1.0) * a.N;  // weight rows of an expert
   // experts with rows, as if each row drew its expert
@@ -189,30 +192,30 @@ Fp8Plan plan8(const LinArgs& a) {
   // What a call costs its caller: the GPU's time, but in a run of calls no less than the
   // host's for its launches; a tenth of the GPU's own time decides between equals.
   auto cost = [](double us, bool two) { return std::max(us, two ? 13.0 : 9.0) + 0.1 * us; };
-  const double rows = row_tiles(16) * (a.N / 16) * std::min(16.0, a.M / live) * a.K;
+  const double wgs = row_tiles(16) * (a.N / 16), rows = wgs * std::min(16.0, a.M / live) * a.K;
   Fp8Plan best{kRows8, 1};
   if (!fp8_tiles_ok(a)) return best;
-  double t = cost(3.2 + 0.97 * hbm + rows / 4.4e6, false);
+  double t = cost(3.2 + std::max(0.97 * hbm, 0.0035 * wgs) + rows / 4.4e6, false);
   auto take = [&](Fp8Path path, int nks, double us, double stream) {
     const double c = cost(std::max(us, start + stream * hbm), nks > 1);
     if (c < t) t = c, best = Fp8Plan{path, nks};
   };
-  auto small = [&](Fp8Path path, double idle, double full, double many, double stream) {
+  auto small = [&](Fp8Path path, double idle, double full, double tile, double stream) {
     const double tiles = row_tiles(kSide[path]) * std::ceil(cols / kSide[path]);
     for (int nks = 1; nks <= kMaxSlices8; nks *= 2) {
       if (nks > 1 && (a.K / kBlock8 < 4 * nks || tiles * nks > 1024)) break;
-      const double n = tiles * nks;
-      double us = start + std::ceil(stages / nks) * std::max(idle, (n > 1024 ? many : full) * n / 256);
-      if (nks > 1) us += 4.0 + 8.0 * a.M * cols * nks / 5e6;
+      const double n = tiles * nks / 256, st = std::ceil(stages / nks);
+      double us = start + std::max(st * idle + tile, n * (st * full + tile));
+      if (nks > 1) us += (a.offsets ? 5.5 : 4.0) + 8.0 * a.M * cols * nks / 5e6;
       take(path, nks, us, stream);
     }
   };
-  small(k64, 0.35, 0.23, 0.23, 1.35);
-  small(k128, 0.68, 0.53, 0.6, 1.03);
+  if (a.offsets) small(k64, 0.32, 0.23, 1.4, 1.35), small(k128, 0.48, 0.53, 4.0, 1.03);
+  else small(k64, 0.32, 0.19, 0.9, 1.35), small(k128, 0.48, 0.45, 3.0, 1.03);
   const double tiles = row_tiles(256) * std::ceil(cols / 256);
   const double whole = std::floor(tiles / 256), rest = tiles - 256 * whole;
   take(k256, 1, start + 3 + whole * (stages * 1.62 + 4) +
-                    (rest > 0 ? stages * std::max(1.25, 1.62 * rest / 256) + 4 : 0.0), 1.2);
+                    (rest > 0 ? stages * std::max(1.25, 1.62 * rest / 256) + 4 : 0.0), 1.05);
   return best;
 }
 

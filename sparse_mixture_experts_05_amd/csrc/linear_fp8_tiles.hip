@@ -13,14 +13,19 @@
 // scales of the stage with them. The weights are the MFMA's A operand and the rows its B: a
 // lane ends with 4 consecutive columns of one row. In a gated product half of a wave's weight
 // sub-tiles holds gate rows, the other the up rows of the same columns. The weights'
-// fragments stay in registers over a stage, the rows' come in two sets. One barrier a stage
-// stands where each wave has its last rows of the stage in registers: behind it the last
-// sub-tile row's MFMAs run, the next stage's first fragments are read, and the copies into
-// the buffer that was just read are issued.
+// fragments stay in registers over a stage, the rows' come in two sets.
 //
-// Measured (graph replay, no act): 8192^3 454-467 us (2.4 PFLOP/s; 325 us on zeros: the power
+// Two barriers a stage. The early one stands behind a wave's first row of MFMAs, when it has
+// its weight fragments of the stage in registers: the weights of the stage that takes this
+// one's buffers are copied from there on, so that they have more than a whole stage to come
+// from HBM (copied behind the late barrier instead: 65536 rows of 256 gated experts 797 ->
+// 728 us, 8192 rows of 8 experts x 4096 x 14336 561 -> 509, 8192^3 443 -> 442). The late one
+// stands where each wave has its last rows of the stage: behind it the last sub-tile row's
+// MFMAs run, the next stage's first fragments are read, and that stage's rows are copied.
+//
+// Measured (graph replay, no act): 8192^3 442-456 us (2.4 PFLOP/s; 325 us on zeros: the power
 // limit, at which MFMAs of this shape on registers alone, without the FMAs, hold 3.2), 4096^3
-// 61-63 us of which a round's prologue, epilogue and launch take about 10. The first form of
+// 62 us of which a round's prologue, epilogue and launch take about 10. The first form of
 // these tiles, MFMA and FMA in turn in one wave, took 791 and 94.
 #include <algorithm>
 #include <type_traits>
@@ -35,8 +40,8 @@ using namespace lin;
 
 // WM x WN waves with 64 weight rows each. The ring: two stages where two workgroups of a CU
 // take turns or LDS holds no more, three for the small tiles, whose launches have few waves
-// to hide a copy behind (64 x 4096 x 4096 25 -> 16 us; four: 19. 128 x 128 tiles of three
-// stages, one workgroup a CU: 2048 x 4096 x 4096 40 -> 53).
+// to hide a copy behind (64 x 4096 x 4096 15.9 us; two stages 19.4, four 18.1; 128 x 128 tiles
+// of three stages, one workgroup a CU: 2048 x 4096 x 4096 40 -> 53).
 template <int BM_, int BN_, int WM_, int NS_>
 struct Tile8 {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = BN / 64, NW = WM * WN;
@@ -81,6 +86,7 @@ __global__ __launch_bounds__(Sh::NW * 64, 2) void fp8_tile_kernel(Fp8Args f) {
   constexpr int BM = Sh::BM, BN = Sh::BN, TM = Sh::TM, TN = Sh::TN, WN = Sh::WN, NW = Sh::NW;
   constexpr int ROWB = Sh::ROWB, XB = Sh::XB, WB = Sh::WB, SB = Sh::SB, XI = Sh::XI, WI = Sh::WI;
   constexpr int WM = Sh::WM, RING = Sh::STAGES, COPIES = XI + WI + 1;
+  constexpr int OPEN = (RING - 2) * COPIES + WI;  // copies that may be under way at a late barrier
   constexpr bool GT = ACT == kActGeglu || ACT == kActSwiglu;
   constexpr int H = GT ? 2 : 1;
   constexpr int BC = GT ? BN / 2 : BN;            // output columns of a tile
@@ -169,6 +175,10 @@ __global__ __launch_bounds__(Sh::NW * 64, 2) void fp8_tile_kernel(Fp8Args f) {
   // pairs of this wave's sub-tile rows that hold data: all except in a partial row tile
   const int nsub = __builtin_amdgcn_readfirstlane(min(TM / 2, (M + (WM - 1 - wm) * 32 + 31) / (WM * 32)));
 
+  // Every wave's weight fragments of the stage are in registers (its first TN MFMAs have
+  // them): their buffer is free for those of the stage after next.
+  auto early_barrier = [] { asm volatile("s_barrier" ::: "memory"); };
+
   auto main_loop = [&](auto ns_tag) {
     constexpr int NS = decltype(ns_tag)::value;
     constexpr int NM = NS * TN;
@@ -184,13 +194,12 @@ __global__ __launch_bounds__(Sh::NW * 64, 2) void fp8_tile_kernel(Fp8Args f) {
       xf[i & 1][1] = ld16(smem + buf * XB + fx + sub_row<WM>(i) * ROWB + slot1);
       sx[i & 1] = *reinterpret_cast<const float*>(smem + buf * SB + fs + sub_row<WM>(i) * 4);
     };
-    // prologue: the stages that fill the ring but for the last one's weights
-    static_for<RING - 1>([&](auto st) {
+    // prologue: the stages that fill the ring
+    static_for<RING>([&](auto st) {
       constexpr int k = decltype(st)::value;
       static_for<COPIES>([&](auto q) { copy(min(k, last), k, decltype(q)::value); });
     });
-    static_for<XI>([&](auto q) { copy(min(RING - 1, last), RING - 1, decltype(q)::value); });
-    wait_vmcnt<(RING - 2) * COPIES + XI>();
+    wait_vmcnt<(RING - 1) * COPIES>();
     lds_barrier();
     if constexpr (NS > 0) {
       static_for<TN>([&](auto j) { read_w(0, decltype(j)::value); });
@@ -202,9 +211,8 @@ __global__ __launch_bounds__(Sh::NW * 64, 2) void fp8_tile_kernel(Fp8Args f) {
     }
     int buf = 0;                                  // of stage kt
     for (int kt = 0; kt < KT; ++kt) {
-      // the ring's last stage, whose rows are on their way, and the one after it
-      const int k1 = min(kt + RING - 1, last), k2 = min(kt + RING, last);
-      const int next = buf + 1 == RING ? 0 : buf + 1, b1 = buf == 0 ? RING - 1 : buf - 1;
+      const int k2 = min(kt + RING, last);        // the stage that takes this one's buffers
+      const int next = buf + 1 == RING ? 0 : buf + 1;
       if ((kt & 63) == 0) {
 #pragma unroll
         for (int h = 0; h < H; ++h) {
@@ -217,24 +225,29 @@ __global__ __launch_bounds__(Sh::NW * 64, 2) void fp8_tile_kernel(Fp8Args f) {
       for (int h = 0; h < H; ++h)
         sws[h] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsv[h]), kt & 63));
       if constexpr (NS == 0) {
-        static_for<WI + 1>([&](auto q) { copy(k1, b1, XI + decltype(q)::value); });
-        wait_vmcnt<(RING - 2) * COPIES>();
+        early_barrier();
+        static_for<WI>([&](auto q) { copy(k2, buf, XI + decltype(q)::value); });
+        wait_vmcnt<OPEN>();
         lds_barrier();
         static_for<XI>([&](auto q) { copy(k2, buf, decltype(q)::value); });
+        copy(k2, buf, XI + WI);
       } else {
         static_for<NM>([&](auto mc) {
           constexpr int m = decltype(mc)::value, i = m / TN, j = m % TN;
           if constexpr (i == NS - 1 && j == 0) {
-            // the last rows of this stage are in registers, stage kt + 1 landed: for everyone
-            wait_vmcnt<(RING - 2) * COPIES>();
+            // late: the last rows of this stage are in registers, stage kt + 1 landed: for everyone
+            wait_vmcnt<OPEN>();
             lds_barrier();
           }
           P[m % 4] = mma_block(wf[j][0], wf[j][1], xf[i & 1][0], xf[i & 1][1]);
           __builtin_amdgcn_sched_barrier(0);
-          if constexpr (m < WI) copy(k1, b1, XI + m);             // weights and scales
-          if constexpr (m == 0) copy(k1, b1, XI + WI);
+          if constexpr (m == TN - 1) early_barrier();
+          if constexpr (NS == 2 && m == TN - 1)                   // weights, before the late barrier
+            static_for<WI>([&](auto q) { copy(k2, buf, XI + decltype(q)::value); });
+          if constexpr (NS > 2 && m >= TN - 1 && m < TN - 1 + WI) copy(k2, buf, XI + m - (TN - 1));
           if constexpr (i == NS - 1) {
             if constexpr (j < XI) copy(k2, buf, j);               // rows
+            if constexpr (j == 0) copy(k2, buf, XI + WI);         // and scales
             read_w(next, j);
           }
           if constexpr (j == 1) {

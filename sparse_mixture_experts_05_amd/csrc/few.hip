@@ -611,8 +611,9 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
 // ----------------------------------------------------------------- host side
 
 // K slices of the down tasks: a task a CU, each wave of a task with 4 steps or more.
-int down_slices(int H, int F, int Fs, int k, bool bf16) {
-  const int steps = (int)(((long long)k * F + Fs) * (bf16 ? 2 : 4) / 64);
+int down_slices(int T, int H, int E, int k, int F, int Fs, bool bf16) {
+  const long long cols = (long long)std::min(E, T * k) * F + (long long)(T + 15) / 16 * Fs;
+  const long long steps = cols * (bf16 ? 2 : 4) / 64;
   int d = 1;
   while (d < kMaxDown && H / kCols * d * 2 <= 256 && steps / (d * 2) >= 4 * kWaves) d *= 2;
   return d;
@@ -631,7 +632,7 @@ struct FewLayout {
 };
 FewLayout layout(int T, int H, int E, int k, int F, int Fs, bool bf16) {
   FewLayout l{};
-  const int D = down_slices(H, F, Fs, k, bf16);
+  const int D = down_slices(T, H, E, k, F, Fs, bf16);
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t p = at;
@@ -696,7 +697,7 @@ hipError_t launch_few(const FewCall& c, hipStream_t s) {
   a.part = reinterpret_cast<float*>(ws + l.part);
   a.counters = reinterpret_cast<unsigned*>(ws + l.counters);
   a.KS = score_slices(c.T, c.H, c.E, c.bf16);
-  a.D = down_slices(c.H, c.F, c.Fs, c.k, c.bf16);
+  a.D = down_slices(c.T, c.H, c.E, c.k, c.F, c.Fs, c.bf16);
   a.idx = c.idx, a.w = c.w, a.out = c.out;
   return c.bf16 ? launch_few_t<uint16_t>(a, c.wg, s) : launch_few_t<float>(a, c.wg, s);
 }

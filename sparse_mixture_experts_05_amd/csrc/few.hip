@@ -136,11 +136,11 @@ __device__ __forceinline__ u32x4_t get16(Shared b, uint32_t at, uint32_t uniform
   return __builtin_amdgcn_raw_buffer_load_b128(b, at, uniform, 16);  // sc1
 }
 
-// Everything that this wave stored is at memory; then *p counts one more.
-__device__ __forceinline__ unsigned announce(unsigned* p) {
+// Everything that this wave stored is at memory; then *p counts n more.
+__device__ __forceinline__ unsigned announce(unsigned* p, unsigned n = 1) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   unsigned before = 0;
-  if ((threadIdx.x & 63) == 0) before = __hip_atomic_fetch_add(p, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if ((threadIdx.x & 63) == 0) before = __hip_atomic_fetch_add(p, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   return __builtin_amdgcn_readfirstlane(before);
 }
 
@@ -409,7 +409,8 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
 
   if (wave == kWaves) {
     int turn = 0;
-    while (t0 < nup) {
+    unsigned finished = 0;
+    for (; t0 < nup; ++finished) {
       if (lane == 0) L.ticket[turn] = draw_ticket(a);
       lds_barrier();
       // sums in wave order; with a gate, the up half is in the lanes 32 further on
@@ -431,12 +432,14 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
         if constexpr (ES == 2) put8(row, pack4(o));
         else put16(row, f32x4_t{o.v[0], o.v[1], o.v[2], o.v[3]});
       }
-      if (announce(a.counters + kLine) == (unsigned)(nup - 1) && lane < kGo)
-        __hip_atomic_store(a.counters + (2 + lane) * kLine, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       t0 = t1;
       t1 = uni(L.ticket[turn]);
       turn ^= 1;
     }
+    // all of them at once: a wait for the stores and the count after every task is in the way
+    // of the next one (64 tokens of 64 experts 2048 x 1024 223 -> 203 us)
+    if (finished > 0 && announce(a.counters + kLine, finished) + finished == (unsigned)nup && lane < kGo)
+      __hip_atomic_store(a.counters + (2 + lane) * kLine, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (task >= ndown) return;
     const bool done = wait_set(a.counters + (2 + blockIdx.x % kGo) * kLine);
     lds_barrier();

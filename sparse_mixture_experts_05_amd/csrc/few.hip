@@ -59,7 +59,7 @@ struct FewArgs {
   void* h;             // [T * k, F] in the order of the experts, then [T, Fs]
   float* part;         // [H / 16, D, T, 16]: partial columns of out
   unsigned* counters;  // tickets | up tasks done | go [kGo] | arrived [H / 16]
-  int KS, D;
+  int KS, D, batch;
   int32_t* idx;
   float* w;
   void* out;
@@ -243,7 +243,7 @@ struct FewLds {
   float w[kPairs];     // and weight
   // a unit: its expert (-1: the shared one), first place (the shared one's: token) and pairs
   int expert[kUnits], first[kUnits], pairs[kUnits];
-  int units, start[2], ticket[2];  // a workgroup's first two tickets, then every next one in turn
+  int units, start[2], ticket[2];  // a workgroup's first tickets, then every next one in turn
 };
 
 // The scores of token t, expert i * 64 + lane, summed in slice order.
@@ -281,8 +281,8 @@ __global__ __launch_bounds__(64) void few_choice_kernel(FewArgs a) {
 
 // The choice of every token, or its loads; the pairs in the experts' order, and the units:
 // the shared expert's, then each expert's. One wave a token, for itself, then one thread a
-// pair. The wave that finishes tasks draws the workgroup's first two tickets meanwhile, the
-// second when every workgroup has its first.
+// pair. The wave that finishes tasks draws the workgroup's first ticket meanwhile, and where a
+// ticket is one task the second, when every workgroup has its first.
 __device__ __forceinline__ int draw_ticket(const FewArgs& a) {
   return (int)__hip_atomic_fetch_add(a.counters, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -300,7 +300,7 @@ __device__ __forceinline__ void choose(const FewArgs& a, FewLds& L) {
   }
   for (int i = tid; i < kWaves * kMaxE; i += kWaves * 64) (&L.choice.count[0][0])[i] = 0;
   lds_barrier();
-  if (drawer) L.start[1] = draw_ticket(a);
+  if (drawer && a.batch == 1) L.start[1] = draw_ticket(a);
   // Places have to be the same in every workgroup: pairs of an expert keep their order.
   // Pairs of this wave with the lane's expert: by the 8 bits of its number.
   const bool pair = tid < a.T * a.k;  // the streams' threads
@@ -404,14 +404,16 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
     const int r = t - su * CS;
     return r < 0 ? Task{t / CS, t % CS * chunk} : Task{su + r / CF, r % CF * chunk};
   };
-  int t0 = uni(L.start[0]), t1 = uni(L.start[1]);
+  // A ticket is `batch` tasks one behind the other (a power of two).
+  int t0 = uni(L.start[0]) * a.batch, t1 = a.batch == 1 ? uni(L.start[1]) : t0 + 1;
+  auto draws = [&](int t) { return ((t + 1) & (a.batch - 1)) == 0; };  // behind task t
   int task = blockIdx.x;
 
   if (wave == kWaves) {
     int turn = 0;
     unsigned finished = 0;
     for (; t0 < nup; ++finished) {
-      if (lane == 0) L.ticket[turn] = draw_ticket(a);
+      if (lane == 0 && draws(t1)) L.ticket[turn] = draw_ticket(a);
       lds_barrier();
       // sums in wave order; with a gate, the up half is in the lanes 32 further on
       f32x4_t v = L.red[turn][0][lane], u = L.red[turn][0][lane ^ 32];
@@ -433,7 +435,7 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
         else put16(row, f32x4_t{o.v[0], o.v[1], o.v[2], o.v[3]});
       }
       t0 = t1;
-      t1 = uni(L.ticket[turn]);
+      t1 = draws(t1) ? uni(L.ticket[turn]) * a.batch : t1 + 1;
       turn ^= 1;
     }
     // all of them at once: a wait for the stores and the count after every task is in the way
@@ -568,7 +570,7 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
       });
       lds_barrier();
       t0 = t1;
-      t1 = uni(L.ticket[turn]);
+      t1 = draws(t1) ? uni(L.ticket[turn]) * a.batch : t1 + 1;
       turn ^= 1;
       u = n;
     }
@@ -620,6 +622,18 @@ int down_slices(int T, int H, int E, int k, int F, int Fs, bool bf16) {
   int d = 1;
   while (d < kMaxDown && H / kCols * d * 2 <= 256 && steps / (d * 2) >= 4 * kWaves) d *= 2;
   return d;
+}
+
+// Tasks of a ticket: up to 8 and 128 KiB of weights, with two tickets a CU. The workgroups'
+// draws from one counter are 10 ns apart, 2.7 us a round of 256, in which a CU reads 55 KB:
+// 64 tokens of 64 experts 256 x 512 75 us with a task a ticket, 54 so; 2048 x 1024 204 and
+// 188; 32 tokens of 200 experts 128 x 1024 242 and 145 (16 or 32 tasks: 153, 173).
+int batch_tasks(int T, int H, int E, int k, int F, int act, bool bf16) {
+  const int chunk = act == kActGeglu || act == kActSwiglu ? kCols / 2 : kCols;
+  const long long tasks = (long long)std::min(E, T * k) * (F / chunk), bytes = (long long)kCols * H * (bf16 ? 2 : 4);
+  int n = 1;
+  while (n < 8 && bytes * n * 2 <= 131072 && tasks >= 512LL * n * 2) n *= 2;
+  return n;
 }
 
 // K slices of the scores: up to 128 workgroups, each wave of one with a step or more.
@@ -701,6 +715,7 @@ hipError_t launch_few(const FewCall& c, hipStream_t s) {
   a.counters = reinterpret_cast<unsigned*>(ws + l.counters);
   a.KS = score_slices(c.T, c.H, c.E, c.bf16);
   a.D = down_slices(c.T, c.H, c.E, c.k, c.F, c.Fs, c.bf16);
+  a.batch = batch_tasks(c.T, c.H, c.E, c.k, c.F, c.act, c.bf16);
   a.idx = c.idx, a.w = c.w, a.out = c.out;
   return c.bf16 ? launch_few_t<uint16_t>(a, c.wg, s) : launch_few_t<float>(a, c.wg, s);
 }

@@ -25,11 +25,13 @@
 // stored, those of the down weights while the last up tasks are waited for.
 //
 // Bound by HBM (T = 64 reads 5.8 TB/s of weights) and, for a token or two, by the launches'
-// starts, the choice and the wait between up and down (22 of 1 token's 56 us). bf16, eager,
-// cold weights, against the separate calls (route, dispatch, products, combine) in a graph:
-//   1 token, 128 experts of 4096 x 1536 swiglu, 8 chosen, one shared   75 us (108)
-//   16 tokens, 128 experts of 4096 x 1024 gelu, 8 chosen              222 us (270)
-//   64 tokens, 128 experts of 4096 x 1024 swiglu, 8 chosen            548 us (559)
+// starts, the choice and the wait between up and down (18 of 1 token's 55 us). bf16, eager,
+// cold weights, against the separate calls (route, dispatch, products, combine), eager and
+// from a graph:
+//   1 token, 128 experts of 4096 x 1536 swiglu, 8 chosen, one shared   75 us (108, 107)
+//   16 tokens, 128 experts of 4096 x 1024 gelu, 8 chosen              223 us (246, 268)
+//   64 tokens, 128 experts of 4096 x 1024 swiglu, 8 chosen            547 us (584, 556)
+//   64 tokens, 64 experts of 256 x 512 swiglu, 8 chosen                57 us (63, 42)
 // 4 steps in flight a wave (R): 2, 3, 5, 6, 8, 12 and 16 are slower by 1 to 20 % (1 token of
 // gelu 58.3 us; 62.7, 62.0, 64.9, 60.1, 61.6, 70.6, 69.0), as are two workgroups a CU (70.7).
 #include <algorithm>

@@ -15,8 +15,9 @@
 // when it has drawn a ticket past the last up task, so by then every up task is held by a
 // workgroup that runs, and that waits for nothing before it is through with its tickets:
 // the wait ends whatever number of workgroups is resident and whatever else the GPU runs.
-// (It gives up after some seconds, and out is NaN then: so a workspace that another call is
-// using at the same time does not hang the GPU.)
+// (It gives up after some seconds and writes NaN, few_slices.hpp: so a workspace that
+// another call is using at the same time, which clears the counters, does not hang the GPU.
+// That is all that is ensured then: what both calls write is undefined.)
 //
 // The pairs (token, chosen expert) are sorted by expert in every workgroup's LDS; up to 16
 // pairs of an expert make a unit, the columns of one MFMA tile, and the shared expert has
@@ -36,6 +37,7 @@
 // gelu 58.3 us; 62.7, 62.0, 64.9, 60.1, 61.6, 70.6, 69.0), as are two workgroups a CU (70.7).
 #include <algorithm>
 
+#include "few_slices.hpp"
 #include "kernels.hpp"
 #include "linear.hpp"
 #include "route_choice.hpp"
@@ -447,6 +449,7 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
     if (task >= ndown) return;
     const bool done = wait_set(a.counters + (2 + blockIdx.x % kGo) * kLine);
     lds_barrier();
+    const few::Slice what = few::slice_step(done, a.D);
     for (turn = 0; task < ndown; task += gridDim.x, turn ^= 1) {
       lds_barrier();
       const int d = task / ntile, nt = task % ntile;
@@ -460,16 +463,16 @@ __global__ __launch_bounds__((kWaves + 1) * 64, 3) void few_kernel(FewArgs a) {
         v[i] = *reinterpret_cast<const f32x4_t*>(&L.out[turn][0][t][c]);
 #pragma unroll
         for (int q = 1; q < kWaves; ++q) v[i] += *reinterpret_cast<const f32x4_t*>(&L.out[turn][q][t][c]);
-        if (!done) v[i] = f32x4_t{NAN, NAN, NAN, NAN};
+        if (what == few::kGiveUp) v[i] = f32x4_t{NAN, NAN, NAN, NAN};
       }
-      if (a.D > 1) {
+      if (what == few::kHandOver) {
         // the slice that arrives last adds all of them up, in slice order
         const uint32_t tile = (uint32_t)a.T * kCols * 4, at = (uint32_t)(nt * a.D) * tile + lane * 16;
         uint8_t* P = reinterpret_cast<uint8_t*>(a.part) + at + d * tile;
 #pragma unroll
         for (int i = 0; i < kFewT / 16; ++i)
           if (i < n && i * 16 + (lane >> 2) < a.T) put16(P + i * 1024, v[i]);
-        if (announce(a.counters + kArrived + nt) != (unsigned)(a.D - 1)) continue;
+        if (!few::adds_up(announce(a.counters + kArrived + nt), a.D)) continue;
         const Shared pb = shared_buffer(a.part, (uint32_t)ndown * tile);
 #pragma unroll
         for (int i = 0; i < kFewT / 16; ++i) {

@@ -1,0 +1,31 @@
+// Who writes a column tile of the few-token layer's out, whose K is cut into D slices that
+// different workgroups hold: the rules of few.hip's finishing wave, compiled into the kernel
+// and into host code (tests/slices_host.cpp), where every order of arrival can be played.
+//
+// A slice whose wait for the up tasks ended well is handed over, and the one that arrives
+// last adds all D up. A slice that gave the wait up has no sum to hand over: it writes NaN
+// to out itself, and does not arrive. So the tile of a call that owns its workspace is NaN
+// if one slice gave up, whoever arrives when; and where a call on the same workspace has
+// cleared the arrivals, a slice that gave up does not leave out as it was either.
+#pragma once
+
+#if defined(__HIPCC__)
+#define MOE_HD __host__ __device__
+#else
+#define MOE_HD
+#endif
+
+namespace moe {
+namespace few {
+
+enum Slice { kStore, kHandOver, kGiveUp };
+
+MOE_HD inline Slice slice_step(bool waited, int D) {
+  return !waited ? kGiveUp : D > 1 ? kHandOver : kStore;
+}
+
+// before: slices that had arrived
+MOE_HD inline bool adds_up(unsigned before, int D) { return before == (unsigned)(D - 1); }
+
+}  // namespace few
+}  // namespace moe

@@ -494,6 +494,9 @@ int moe_linear_path(int E, int rows, int N, int K, int act, int grouped, int dty
  * x     [rows,K] dtype         device, read
  * q     [rows,K] e4m3 bytes    device, written
  * scale [K/128,rows] fp32      device, written (the rows of a block side by side)
+ * Power-of-two scales keep a block's largest element less exactly than amax / 448 does
+ * (error 2.7e-2 of the data's norm whatever the data; amax / 448 gives 2.6e-2 on Gaussian
+ * data, 1.0e-2 where 1 % of the elements are up to 200 times as large).
  * K % 128 == 0; rows * K up to about 2^37 (else MOE_ERR_UNSUPPORTED). x and q
  * 16-byte, scale 4-byte aligned; outputs that overlap each other or x are
  * MOE_ERR_INVALID_ARG. No workspace.

@@ -6,15 +6,19 @@
 //   s    = the least power of two with amax / s <= 448, at least 2^-126; 1 if amax = 0
 //   q    = x / s rounded to e4m3, nearest, ties to even
 //
-// A power of two divides x exactly, so q is one rounding of x; a scale of any mantissa
-// (amax / 448) would round twice and keeps no more of a floating-point block. The product
-// takes either. An infinity or NaN becomes e4m3's NaN and leaves the rest of its block
-// alone.
+// A power of two divides x exactly, so q is one rounding of x, the same in any arithmetic,
+// and a scale is one byte of exponent. It costs accuracy where a few elements hold most of a
+// block: amax / 448 rounds twice and uses the range up to 448, which keeps the block's
+// largest element (all but) exactly. Error of the quantised values relative to the data's
+// norm, power of two against amax / 448, 2^22 bf16 values: Gaussian 2.66e-2 and 2.57e-2,
+// with 1 % of the elements up to 200 times as large 2.67e-2 and 0.98e-2. The products
+// (linear_fp8.hip) take scales of any mantissa, so a caller can bring those. An infinity or
+// NaN becomes e4m3's NaN and leaves the rest of its block alone.
 //
 // Bound by memory: one read, half (bf16) or a quarter (fp32) of that written, in one pass: a
-// block stays in registers between its maximum and its rounding. 16384 x 4096 bf16 37 us, 8
-// weights of 14336 x 4096 260 us, 5.4 TB/s both (a copy: 5.1-5.3); one row of 4096 is a
-// launch (3 us on the GPU, 9 a call).
+// block stays in registers between its maximum and its rounding. In a graph (a copy: 5.1 to
+// 5.3 TB/s): 16384 x 4096 bf16 33 us (6.0 TB/s), fp32 62 us (5.4); 8 weights of 14336 x 4096
+// bf16 248 us (5.7), fp32 407 us (5.8). One row of 4096 is a launch (2.7 us, 9 a call).
 #include "common.hpp"
 #include "kernels.hpp"
 

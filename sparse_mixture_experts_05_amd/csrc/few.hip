@@ -15,9 +15,10 @@
 // when it has drawn a ticket past the last up task, so by then every up task is held by a
 // workgroup that runs, and that waits for nothing before it is through with its tickets:
 // the wait ends whatever number of workgroups is resident and whatever else the GPU runs.
-// (It gives up after some seconds and writes NaN, few_slices.hpp: so a workspace that
+// (It gives up after some seconds and writes NaN, few_rules.hpp: so a workspace that
 // another call is using at the same time, which clears the counters, does not hang the GPU.
-// That is all that is ensured then: what both calls write is undefined.)
+// That, and that no access leaves the operands, is all that is ensured then: what both calls
+// write is undefined.)
 //
 // The pairs (token, chosen expert) are sorted by expert in every workgroup's LDS; up to 16
 // pairs of an expert make a unit, the columns of one MFMA tile, and the shared expert has
@@ -37,7 +38,7 @@
 // gelu 58.3 us; 62.7, 62.0, 64.9, 60.1, 61.6, 70.6, 69.0), as are two workgroups a CU (70.7).
 #include <algorithm>
 
-#include "few_slices.hpp"
+#include "few_rules.hpp"
 #include "kernels.hpp"
 #include "linear.hpp"
 #include "route_choice.hpp"
@@ -73,6 +74,7 @@ struct FewArgs {
 // down those that count, and they look at one of kGo places, which the last up task sets.
 constexpr int kLine = 128, kGo = 16;
 constexpr int kArrived = (2 + kGo) * kLine;
+static_assert((unsigned long long)kUnits * (1 << 20) / (kCols / 2) < few::kNoTicket, "tickets of all up tasks");
 inline int counter_ints(int H) { return kArrived + H / kCols; }
 
 // ----------------------------------------------------------------- scores
@@ -288,7 +290,7 @@ __global__ __launch_bounds__(64) void few_choice_kernel(FewArgs a) {
 // pair. The wave that finishes tasks draws the workgroup's first ticket meanwhile, and where a
 // ticket is one task the second, when every workgroup has its first.
 __device__ __forceinline__ int draw_ticket(const FewArgs& a) {
-  return (int)__hip_atomic_fetch_add(a.counters, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return few::ticket_number(__hip_atomic_fetch_add(a.counters, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
 }
 
 template <int EPX>

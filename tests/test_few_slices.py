@@ -1,5 +1,5 @@
 """Who writes a column tile of moe_layer_few's out when K is cut into slices (host check, no
-GPU): the kernel's own rules (csrc/few_slices.hpp) are compiled for the host and played
+GPU): the kernel's own rules (csrc/few_rules.hpp) are compiled for the host and played
 through orders of arrival, with slices that gave their wait up, and with a clear of the
 arrivals by another call on the same workspace.
 

@@ -495,8 +495,8 @@ int moe_linear_path(int E, int rows, int N, int K, int act, int grouped, int dty
  * q     [rows,K] e4m3 bytes    device, written
  * scale [K/128,rows] fp32      device, written (the rows of a block side by side)
  * Power-of-two scales keep a block's largest element less exactly than amax / 448 does
- * (error 2.7e-2 of the data's norm whatever the data; amax / 448 gives 2.6e-2 on Gaussian
- * data, 1.0e-2 where 1 % of the elements are up to 200 times as large).
+ * (error relative to the data's norm: 2.7e-2 against 2.6e-2 on Gaussian data, against 1.0e-2
+ * where 1 % of the elements are up to 200 times as large).
  * K % 128 == 0; rows * K up to about 2^37 (else MOE_ERR_UNSUPPORTED). x and q
  * 16-byte, scale 4-byte aligned; outputs that overlap each other or x are
  * MOE_ERR_INVALID_ARG. No workspace.
@@ -523,8 +523,10 @@ int moe_quantize_weight(const void* w, int count, int N, int K, int dtype, void*
  * at 2^-13 of the largest of the 8, then in fp32), the blocks scaled and summed in fp32;
  * bias, act, gate and residual as moe_linear's bf16 form; one rounding.
  * x [M,K] e4m3, x_scale [K/128,M] fp32, w [N,K] or [2,N,K] e4m3, w_scale
- *   [ceil(N/128),K/128] or [2,ceil(N/128),K/128] fp32 (any values: those of
- *   moe_quantize and moe_quantize_weight, or a checkpoint's), bias [N] or [2,N] bf16 or
+ *   [ceil(N/128),K/128] or [2,ceil(N/128),K/128] fp32 (those of moe_quantize and
+ *   moe_quantize_weight, or a checkpoint's, of any mantissa; x_scale[b,m] * w_scale[n/128,b]
+ *   is one fp32 number, so it has to stay below 2^128, where a block's sum would become
+ *   infinite or, if it is 0, NaN, and loses bits below 2^-126), bias [N] or [2,N] bf16 or
  *   NULL, residual [M,N] bf16 or NULL: device, read; y [M,N] bf16: device, written; it
  *   may be residual itself.
  * K % 128 == 0, N % 64 == 0. Scales 4-byte, the others 16-byte aligned. Sizes whose
@@ -562,7 +564,8 @@ typedef enum {
 } moe_fp8_path;
 
 /* The kernels and K slices that an 8-bit product of these sizes takes, as
- * moe_linear_path: a moe_fp8_path, or a negative status. */
+ * moe_linear_path: a moe_fp8_path, or a negative status. (Rows gathered from an x of 4 GiB
+ * or more take MOE_FP8_ROWS, whatever the sizes.) */
 int moe_linear_fp8_path(int E, int rows, int N, int K, int act, int grouped, int* slices);
 
 /* What a routing bias moves. */
@@ -572,7 +575,12 @@ typedef enum {
 } moe_bias_mode;
 
 /*
- * moe_layer_few - a whole MoE layer for a few tokens (1 <= T <= 64), in two or three launches:
+ * moe_layer_few - a whole MoE layer for a few tokens (1 <= T <= 64), in two or three launches.
+ * Called one by one it is faster than the separate calls (route, dispatch, products, combine)
+ * wherever those are bound by the host, some 65 us. Against a HIP graph of them it pays for
+ * experts of about 3 MB of weights (1024 x 512 gated, bf16) or more with up to 4 pairs of a
+ * token and an expert each (T k / E); a graph of the separate calls is up to 1.2 times as
+ * fast with 8 pairs an expert, 1.5 with 16, and 1.7 with smaller experts from 4 tokens on.
  *   s[t,e] = sum_h x[t,h] * wg[e,h]  (+ bias[e] with MOE_BIAS_SCORE)
  *   topk_idx, topk_w from s as moe_route_grouped (bias as its bias with
  *            MOE_BIAS_CHOICE, none with MOE_BIAS_SCORE; softmax, MOE_BIAS_SCORE, one
@@ -593,7 +601,8 @@ typedef enum {
  * output or workspace that overlaps another operand MOE_ERR_INVALID_ARG.
  * ws / ws_bytes: device workspace of at least
  *   moe_layer_few_workspace_bytes(T,H,E,k,F,Fs,dtype); its content does not matter. Calls
- *   that may run at the same time need workspaces of their own.
+ *   that may run at the same time need workspaces of their own: with a shared one the
+ *   outputs of both are undefined (no access leaves the operands, and both calls end).
  */
 int moe_layer_few(const void* x, const void* wg, const float* bias, int bias_mode,
                   const void* w_up, const void* w_down, const void* b_up, const void* b_down,

@@ -20,6 +20,10 @@
 // That, and that no access leaves the operands, is all that is ensured then: what both calls
 // write is undefined.)
 //
+// h is rounded to bf16 because the matrix instruction takes no wider operand (the separate
+// calls do the same): out is 2.3e-3 of its norm from float64 with it and would be 1.7e-3, its
+// own rounding, with h in two bf16 parts, at twice the MFMAs and twice h's way through memory.
+//
 // The pairs (token, chosen expert) are sorted by expert in every workgroup's LDS; up to 16
 // pairs of an expert make a unit, the columns of one MFMA tile, and the shared expert has
 // units of 16 tokens. Weights go straight to registers (nothing else on the chip reads
@@ -27,13 +31,20 @@
 // stored, those of the down weights while the last up tasks are waited for.
 //
 // Bound by HBM (T = 64 reads 5.8 TB/s of weights) and, for a token or two, by the launches'
-// starts, the choice and the wait between up and down (18 of 1 token's 55 us). bf16, eager,
-// cold weights, against the separate calls (route, dispatch, products, combine), eager and
-// from a graph:
-//   1 token, 128 experts of 4096 x 1536 swiglu, 8 chosen, one shared   75 us (108, 107)
-//   16 tokens, 128 experts of 4096 x 1024 gelu, 8 chosen              223 us (246, 268)
-//   64 tokens, 128 experts of 4096 x 1024 swiglu, 8 chosen            547 us (584, 556)
-//   64 tokens, 64 experts of 256 x 512 swiglu, 8 chosen                57 us (63, 42)
+// starts, the choice and the wait between up and down (18 of 1 token's 55 us). bf16, in a
+// graph of 20 calls (eager the same within 2 %), against the separate calls (route, dispatch,
+// products, combine), eager and in such a graph:
+//   1 token, 128 experts of 4096 x 1536 swiglu, 8 chosen, one shared   75 us (111, 111)
+//   16 tokens, 128 experts of 4096 x 1024 gelu, 8 chosen              224 us (253, 251)
+//   64 tokens, 128 experts of 4096 x 1024 swiglu, 8 chosen            545 us (558, 557)
+//   64 tokens, 64 experts of 256 x 512 swiglu, 8 chosen                55 us (62, 39)
+// The separate calls are bound by the host when eager (62 us and more), not in a graph. Of
+// their time in a graph, over 168 shapes with cold weights, this layer takes
+//   experts of 3 MB (1024 x 512 gated) or more: 0.6 to 1.04 with up to 2 pairs an expert
+//     (T k / E), 0.8 to 1.17 with 4, 0.9 to 1.17 with 8, 1.15 to 1.5 with 16 (an expert's
+//     second unit is a second pass over its weights);
+//   smaller ones: 0.9 to 1.06 with 1 token, 1 to 1.7 with 4 tokens or more (its steps wait
+//     for each other, and launches of that size cost no more than the wait).
 // 4 steps in flight a wave (R): 2, 3, 5, 6, 8, 12 and 16 are slower by 1 to 20 % (1 token of
 // gelu 58.3 us; 62.7, 62.0, 64.9, 60.1, 61.6, 70.6, 69.0), as are two workgroups a CU (70.7).
 #include <algorithm>

@@ -36,7 +36,7 @@ using namespace lin;
 // round the 4 waves (with a slice of K a wave, the workgroups read more often from the same
 // HBM channels at one time: 81 of 128 experts 2048 x 4096 126 -> 121 us); their sums are
 // added in wave order through LDS. Bound by HBM: 5.6 TB/s of weights there, and by a
-// launch's start below some 50 MB (8 x 4096 x 4096: 8 us, of which its bytes take 3).
+// launch's start below some 50 MB (8 x 4096 x 4096: 7.3 us, of which its bytes take 3).
 template <bool GT>
 __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args f) {
   constexpr int KQ = 4, U = 2, H = GT ? 2 : 1;
@@ -151,7 +151,7 @@ struct Fp8Plan {
 };
 
 // Path of a product: the least estimated time, in us. The estimates hold what was measured
-// (graph replay, no act; M x N x K dense, then 64 experts with evenly drawn rows):
+// (graphs of three calls with their replay's start, no act; M x N x K dense, then 64 experts with evenly drawn rows):
 //                        rows    64 (slices)   128 (slices)   256
 //   16 x 4096 x 4096      8.5     12.1 (4)      12.9 (8)       25
 //   32 x 4096 x 4096     12.0     12.2 (4)      13.3 (8)       25

@@ -62,7 +62,8 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t u) {
 // list[0 .. k-1] <- the k largest keys of a token that has a whole wave: lane g holds the
 // high halves (scores) of the keys of experts g, g + 64, ... (0: none). k times the largest
 // score, then its lowest expert from the lanes' masks, in scalar registers: 20 instructions
-// a round, where merging sorted lists of 8 over 64 lanes takes 700.
+// a round, where merging sorted lists of 8 over 64 lanes takes 700 (grouped route, k 8, 16
+// tokens of 128 experts 12.0 -> 10.2 us, 1000 of 256 26.5 -> 24.8; k 1 and 2 the same).
 template <int KP, int NSUB>
 __device__ __forceinline__ void pop_top(uint32_t (&o)[NSUB], int k, uint64_t (&list)[KP]) {
   const int lane = threadIdx.x & 63;

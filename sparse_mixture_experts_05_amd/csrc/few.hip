@@ -40,7 +40,7 @@
 //   64 tokens, 64 experts of 256 x 512 swiglu, 8 chosen                55 us (62, 39)
 // The separate calls are bound by the host when eager (62 us and more), not in a graph. Of
 // their time in a graph, over 168 shapes with cold weights, this layer takes
-//   experts of 3 MB (1024 x 512 gated) or more: 0.6 to 1.04 with up to 2 pairs an expert
+//   experts of 3 MB (1024 x 512 gated) or more: 0.66 to 1.04 with up to 2 pairs an expert
 //     (T k / E), 0.8 to 1.17 with 4, 0.9 to 1.17 with 8, 1.15 to 1.5 with 16 (an expert's
 //     second unit is a second pass over its weights);
 //   smaller ones: 0.9 to 1.06 with 1 token, 1 to 1.7 with 4 tokens or more (its steps wait

@@ -3,9 +3,9 @@
 // where every order of arrival can be played.
 //
 // Tickets. A call that uses the workspace at the same time, against the rules, may have its
-// scores or rows where this one counts tickets. Any word read from there is a ticket past
-// the last task or the number of tasks' worth that it says: no task has a negative number,
-// and a ticket times the tasks of a ticket stays an int.
+// scores or rows where this one counts tickets. Any word read there becomes the ticket of
+// that number, or one past the last task: no task has a negative number, and a ticket times
+// the tasks of a ticket stays an int.
 //
 // Slices of out: who writes a column tile whose K is cut into D slices that different
 // workgroups hold. A slice whose wait for the up tasks ended well is handed over, and the one that arrives
